@@ -1,0 +1,411 @@
+"""What is measured of the operators around the token mixer: cross attention to an encoder's
+states (forward and gradients), layer norm (forward and gradients), and the global gradient norm
+with clipping.
+
+``own`` False: ``run`` computes an operator in elementary torch operations, in 32 bits whatever the
+inputs' type, rounded once at the end.  ``own`` True: it calls the framework's entry points.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+# ------------------------------------------------------------------------------------- cases
+def _cross(op, B, H, Hkv, Nq, Nk, d, dtype, pad="none", layout="bhnd"):
+    return dict(op=op, B=B, H=H, Hkv=Hkv, Nq=Nq, Nk=Nk, d=d, dtype=dtype, pad=pad, layout=layout)
+
+
+def _norm(op, rows, cols, groups, dtype):
+    return dict(op=op, rows=rows, cols=cols, groups=groups, dtype=dtype)
+
+
+def _clip(tensors, largest, f32_every, max_norm):
+    return dict(op="clip", tensors=tensors, largest=largest, f32_every=f32_every, max_norm=max_norm)
+
+
+def listed():
+    return [
+        # the latent tokens of a 720p/5s clip (21 x 45 x 80 grid, 32 heads) attend to a full prompt
+        dict(_cross("cross_fwd", 1, 32, 32, 75600, 300, 128, "bf16"), name="cross_fwd_720p"),
+        # a guidance pair at 480p (21 x 30 x 52): prompts of different lengths, a mask with holes,
+        # projections left in [B, N, H, d] order
+        dict(_cross("cross_fwd", 2, 24, 24, 32760, 512, 128, "bf16", "mask", "bnhd"), name="cross_fwd_480p_mask"),
+        # serving: one new token per sequence against long encoder states, shared key heads
+        dict(_cross("cross_fwd", 8, 32, 8, 1, 16384, 128, "bf16", "len"), name="cross_fwd_one_token"),
+        # a small fp32 model: latency of one call
+        dict(_cross("cross_fwd", 3, 5, 5, 77, 33, 64, "f32", "len"), name="cross_fwd_small_f32"),
+        # training step of the first case
+        dict(_cross("cross_bwd", 1, 32, 32, 75600, 300, 128, "bf16"), name="cross_bwd_720p"),
+        # training of a small fp32 model on ragged prompts, shared key heads
+        dict(_cross("cross_bwd", 2, 8, 2, 1021, 257, 64, "f32", "mask", "bnhd"), name="cross_bwd_f32_mask"),
+        # the pre-norm of a 32-head block over a 720p/5s clip
+        dict(_norm("ln_fwd", 75600, 4096, 1, "bf16"), name="ln_fwd_720p"),
+        # the norm of one new token per sequence, odd width
+        dict(_norm("ln_fwd", 3, 1001, 1, "f32"), name="ln_fwd_few_rows"),
+        # training step of a norm modulated per clip, two clips
+        dict(_norm("ln_bwd", 151200, 4096, 2, "bf16"), name="ln_bwd_720p_b2"),
+        # fp32 training at 480p, a width that is no power of two
+        dict(_norm("ln_bwd", 32760, 1000, 1, "f32"), name="ln_bwd_480p_f32"),
+        # the gradients of several blocks of a large model: beyond the L2 cache
+        dict(_clip(96, 50_331_648, 3, 1.0), name="clip_large"),
+        # the gradients of a small model: many short tensors
+        dict(_clip(157, 70_001, 4, 1.0), name="clip_small"),
+    ]
+
+
+def _spread(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    kind = rng.choice(["cross_fwd", "cross_fwd", "cross_bwd", "cross_bwd", "ln_fwd", "ln_bwd", "clip"])
+    if kind.startswith("cross"):
+        dtype = rng.choice(["bf16", "bf16", "f32"])
+        while True:
+            H = rng.choice([1, 2, 3, 4, 8, 12, 16, 24, 32])
+            Hkv = rng.choice([g for g in range(1, H + 1) if H % g == 0])
+            B = rng.choice([1, 1, 2, 3, 5, 8])
+            Nq, Nk = _spread(rng, 1, 75600), _spread(rng, 1, 16384)
+            d = rng.choice([32, 64, 128])
+            # no more than the largest listed case: scores, and bytes of queries
+            if B * H * Nq * Nk * d <= (32 * 75600 * 300 * 128 if dtype == "bf16" else 1 << 33) and \
+                    B * H * Nq * d <= 32 * 75600 * 128:
+                break
+        return _cross(kind, B, H, Hkv, Nq, Nk, d, dtype, rng.choice(["none", "len", "mask"]),
+                      rng.choice(["bhnd", "bnhd"]))
+    if kind.startswith("ln"):
+        dtype = rng.choice(["bf16", "bf16", "f32"])
+        groups = rng.choice([1, 1, 2, 3])
+        cols = rng.choice([_spread(rng, 1, 8192), 8 * _spread(rng, 1, 1024)])
+        top = 75600 * 4096 if dtype == "bf16" else 75600 * 2048
+        return _norm(kind, groups * _spread(rng, 1, max(2, min(75600, top // cols) // groups)), cols, groups, dtype)
+    tensors = _spread(rng, 1, 400)
+    return _clip(tensors, _spread(rng, 64, min(1 << 26, 1_600_000_000 // tensors)), rng.choice([1, 2, 3, 5, 500]),
+                 rng.choice([0.1, 1.0, 1e9]))
+
+
+# ------------------------------------------------------------------------------------- inputs
+def _attended(c):
+    """How many keys each batch row attends, in some order: the whole of them without padding, else
+    spread from none (where there are several rows) to all."""
+    B, Nk = c["B"], c["Nk"]
+    if c["pad"] == "none":
+        return [Nk] * B
+    if B == 1:
+        return [max(1, (2 * Nk) // 3)]
+    if B == 2:
+        return [Nk - Nk // 16, max(1, Nk // 5)]
+    return [(Nk * i) // (B - 1) for i in range(B)]
+
+
+def _sizes(c):
+    """Element counts of the gradient list: matrices among many short vectors, odd ones too."""
+    n, top = c["tensors"], c["largest"]
+    out = []
+    for i in range(n):
+        if i % 4 == 0:
+            out.append(max(1, top >> (i // 4 % 3)))
+        else:
+            out.append(max(1, (top // (64 << (i % 5))) + (i * 7) % 13 - 3))
+    return out
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(shape, g, dt):
+    out = torch.empty(shape, dtype=dt, device="cuda")
+    if out.numel() <= 1 << 26:
+        return out.copy_(torch.randn(shape, generator=g, device="cuda"))
+    flat = out.view(-1)
+    for a in range(0, flat.numel(), 1 << 28):
+        n = min(1 << 28, flat.numel() - a)
+        flat[a:a + n].copy_(torch.randn(n, generator=g, device="cuda"))
+    return out
+
+
+def _cross_inputs(c, seed):
+    g, dt = _gen(seed), DTYPES[c["dtype"]]
+    B, H, Hkv, Nq, Nk, d = c["B"], c["H"], c["Hkv"], c["Nq"], c["Nk"], c["d"]
+    if c["layout"] == "bhnd":
+        Q, K, V = _randn((B, H, Nq, d), g, dt), _randn((B, Hkv, Nk, d), g, dt), _randn((B, Hkv, Nk, d), g, dt)
+    else:  # the projections' own order, keys and values side by side
+        Q = _randn((B, Nq, H, d), g, dt).transpose(1, 2)
+        kv = _randn((B, Nk, 2, Hkv, d), g, dt)
+        K, V = kv[:, :, 0].transpose(1, 2), kv[:, :, 1].transpose(1, 2)
+    s = dict(c, Q=Q, K=K, V=V, scale=1.0 / math.sqrt(d), kv_len=None, key_mask=None)
+    counts = torch.tensor(_attended(c), device="cuda")[torch.randperm(B, generator=g, device="cuda")]
+    if c["pad"] == "len":
+        s["kv_len"] = counts.to(torch.int32)
+    elif c["pad"] == "mask":
+        order = torch.rand((B, Nk), generator=g, device="cuda").argsort(1).argsort(1)
+        s["key_mask"] = order < counts[:, None]
+    return s, g, dt
+
+
+def prepare(case, seed):
+    op = case["op"]
+    if op.startswith("cross"):
+        s, g, dt = _cross_inputs(case, seed)
+        if op == "cross_bwd":
+            s["O"], s["lse"] = _cross_forward(s)
+            s["dO"] = _randn(tuple(s["O"].shape), g, dt)
+        return s
+    if op.startswith("ln"):
+        g, dt = _gen(seed), DTYPES[case["dtype"]]
+        rows, cols, groups = case["rows"], case["cols"], case["groups"]
+        s = dict(case, eps=1e-6, x=_randn((rows, cols), g, dt))
+        s["x"].mul_(1.7).add_(0.3)
+        s["weight"] = 1 + 0.1 * torch.randn((groups, cols), generator=g, device="cuda")
+        s["bias"] = 0.1 * torch.randn((groups, cols), generator=g, device="cuda")
+        if op == "ln_bwd":
+            _, s["mean"], s["rstd"] = _norm_forward(s)
+            s["dy"] = _randn((rows, cols), g, dt)
+        return s
+    # gradients in one flat buffer for each type, as optimizers and buckets keep them, every tensor
+    # at a 16-byte boundary; the clipped ones go to the buffers that the optimizer reads
+    g = _gen(seed)
+    sizes = _sizes(case)
+    s = dict(case)
+    for name, dt in DTYPES.items():
+        spans, at = [], 0
+        for i, n in enumerate(sizes):
+            if (i % case["f32_every"] == 1) == (name == "f32"):
+                spans.append((at, n))
+                at += -(-n // 8) * 8
+        flat = torch.zeros(at, dtype=dt, device="cuda")
+        for a, n in spans:
+            flat[a:a + n] = _randn((n,), g, dt)
+        if at:
+            flat.mul_(1e-3)
+        s["flat_" + name], s["spans_" + name] = flat, spans
+        s["out_" + name] = torch.zeros_like(flat)
+    return s
+
+
+# ------------------------------------------------------------------------------------- plain forms
+def _allowed(s):
+    """[B, Nk] truth values of the keys that are attended, or None for all."""
+    if s["key_mask"] is not None:
+        return s["key_mask"]
+    if s["kv_len"] is not None:
+        return torch.arange(s["Nk"], device="cuda")[None] < s["kv_len"][:, None]
+    return None
+
+
+def _scores(s, allowed):
+    B, H, Hkv, Nq, Nk, d = s["B"], s["H"], s["Hkv"], s["Nq"], s["Nk"], s["d"]
+    q = s["Q"].float().reshape(B, Hkv, H // Hkv * Nq, d)
+    k, v = s["K"].float(), s["V"].float()
+    if allowed is not None:
+        k = k.masked_fill(~allowed[:, None, :, None], 0.0)
+        v = v.masked_fill(~allowed[:, None, :, None], 0.0)
+    x = torch.matmul(q, k.transpose(2, 3)).mul_(s["scale"])
+    if allowed is not None:
+        x.masked_fill_(~allowed[:, None, None, :], -math.inf)
+    return q, k, v, x
+
+
+def _cross_forward(s):
+    B, H, Nq, d = s["B"], s["H"], s["Nq"], s["d"]
+    _, _, v, x = _scores(s, _allowed(s))
+    m = x.amax(3, keepdim=True)
+    m = torch.where(m == -math.inf, torch.zeros_like(m), m)
+    x = x.sub_(m).exp_()
+    total = x.sum(3, keepdim=True)
+    o = torch.matmul(x, v) / torch.where(total == 0, torch.ones_like(total), total)
+    return o.reshape(B, H, Nq, d).to(s["Q"].dtype), (m + total.log()).reshape(B, H, Nq)
+
+
+def _cross_backward(s):
+    B, H, Hkv, Nq, d = s["B"], s["H"], s["Hkv"], s["Nq"], s["d"]
+    q, k, v, x = _scores(s, _allowed(s))
+    lse = s["lse"].reshape(B, Hkv, H // Hkv * Nq, 1)
+    p = x.sub_(torch.where(lse == -math.inf, torch.zeros_like(lse), lse)).exp_()
+    do = s["dO"].float().reshape(B, Hkv, H // Hkv * Nq, d)
+    dv = torch.matmul(p.transpose(2, 3), do)
+    dp = torch.matmul(do, v.transpose(2, 3))
+    delta = (do * s["O"].float().reshape(do.shape)).sum(3, keepdim=True)
+    ds = dp.sub_(delta).mul_(p).mul_(s["scale"])
+    dq = torch.matmul(ds, k).reshape(B, H, Nq, d)
+    dk = torch.matmul(ds.transpose(2, 3), q)
+    dt = s["Q"].dtype
+    return dq.to(dt), dk.to(dt), dv.to(dt)
+
+
+def _per_row(s, w):
+    return w.repeat_interleave(s["rows"] // s["groups"], 0) if s["groups"] > 1 else w
+
+
+def _norm_forward(s):
+    x = s["x"].float()
+    mean = x.mean(1, keepdim=True)
+    x = x - mean
+    rstd = (x.square().mean(1, keepdim=True) + s["eps"]).rsqrt()
+    y = (x * rstd) * _per_row(s, s["weight"]) + _per_row(s, s["bias"])
+    return y.to(s["x"].dtype), mean[:, 0], rstd[:, 0]
+
+
+def _norm_backward(s):
+    dy, groups, cols = s["dy"].float(), s["groups"], s["cols"]
+    xh = (s["x"].float() - s["mean"][:, None]) * s["rstd"][:, None]
+    dw = (dy * xh).reshape(groups, -1, cols).sum(1)
+    db = dy.reshape(groups, -1, cols).sum(1)
+    a = dy * _per_row(s, s["weight"])
+    dx = s["rstd"][:, None] * (a - a.mean(1, keepdim=True) - xh * (a * xh).mean(1, keepdim=True))
+    return dx.to(s["x"].dtype), dw, db
+
+
+def _clip_plain(s):
+    both = [n for n in DTYPES if s["flat_" + n].numel()]
+    norm = sum(s["flat_" + n].float().square().sum(dtype=torch.float64) for n in both).sqrt()
+    coef = (s["max_norm"] / (norm + 1e-6)).clamp(max=1.0)
+    out = {n: (s["flat_" + n].float() * coef.float()).to(DTYPES[n]) for n in both}
+    return dict(out, norm=norm.float())
+
+
+# ------------------------------------------------------------------------------------- the framework's calls
+def _views(flat, spans):
+    return [flat[a:a + n] for a, n in spans]
+
+
+def _own(s):
+    import gated_linear_attention_relu_b200 as la
+
+    op = s["op"]
+    if op.startswith("cross"):
+        if "problem" not in s:  # kept from call to call, with its workspace, as a model keeps them
+            s["problem"] = la.CrossProblem(B=s["B"], H=s["H"], Hkv=s["Hkv"], Nq=s["Nq"], Nk=s["Nk"], d=s["d"],
+                                           scale=s["scale"], dtype=s["dtype"])
+            s["ws"] = la.cross_workspace(s["problem"])
+        p, kw = s["problem"], dict(kv_len=s["kv_len"], key_mask=s["key_mask"], ws=s["ws"])
+        if op == "cross_fwd":
+            return la.cross_forward(p, s["Q"], s["K"], s["V"], return_lse=True, **kw)
+        return la.cross_backward(p, s["Q"], s["K"], s["V"], s["O"], s["lse"], s["dO"], **kw)
+    if op.startswith("ln"):
+        if "problem" not in s:
+            s["problem"] = la.NormProblem(rows=s["rows"], cols=s["cols"], groups=s["groups"], eps=s["eps"],
+                                          dtype=s["dtype"])
+            s["ws"] = la.layernorm_workspace(s["problem"])
+        p = s["problem"]
+        if op == "ln_fwd":
+            return la.layernorm_forward(p, s["x"], s["weight"], s["bias"], return_stats=True)
+        return la.layernorm_backward(p, s["x"], s["dy"], s["mean"], s["rstd"], s["weight"], ws=s["ws"])
+    if "grads" not in s:  # the parameters' gradients and where the clipped ones go, once per model
+        s["grads"] = [t for n in DTYPES for t in _views(s["flat_" + n], s["spans_" + n])]
+        s["outs"] = [t for n in DTYPES for t in _views(s["out_" + n], s["spans_" + n])]
+    norm = la.clip_grad_norm(s["grads"], s["max_norm"], out=s["outs"])
+    return dict({n: s["out_" + n] for n in DTYPES if s["flat_" + n].numel()}, norm=norm)
+
+
+def run(state):
+    if own:
+        return _own(state)
+    return {"cross_fwd": _cross_forward, "cross_bwd": _cross_backward, "ln_fwd": _norm_forward,
+            "ln_bwd": _norm_backward, "clip": _clip_plain}[state["op"]](state)
+
+
+# ------------------------------------------------------------------------------------- work and 64 bits
+def work(case):
+    c = case
+    if c["op"].startswith("cross"):
+        e = 2 if c["dtype"] == "bf16" else 4
+        keys = sum(_attended(c))
+        rows = c["B"] * c["H"] * c["Nq"]
+        pairs = c["H"] * c["Nq"] * keys * c["d"]
+        kv = 2 * c["Hkv"] * keys * c["d"] * e
+        if c["op"] == "cross_fwd":
+            return {"bytes": 2 * rows * c["d"] * e + kv + 4 * rows, "flops": 4 * pairs}
+        return {"bytes": 4 * rows * c["d"] * e + kv + 2 * c["B"] * c["Hkv"] * c["Nk"] * c["d"] * e + 4 * rows,
+                "flops": 10 * pairs}
+    if c["op"].startswith("ln"):
+        e = 2 if c["dtype"] == "bf16" else 4
+        n = c["rows"] * c["cols"]
+        if c["op"] == "ln_fwd":
+            return {"bytes": 2 * n * e + 8 * (c["rows"] + c["groups"] * c["cols"]), "flops": 8 * n}
+        return {"bytes": 3 * n * e + 8 * c["rows"] + 12 * c["groups"] * c["cols"], "flops": 14 * n}
+    sizes = _sizes(c)
+    each = [4 if i % c["f32_every"] == 1 else 2 for i in range(len(sizes))]
+    return {"bytes": 2 * sum(n * e for n, e in zip(sizes, each)), "flops": 3 * sum(sizes)}
+
+
+def _exact_cross(c, s):
+    """One head at a time, from softmax's definition, over the attended keys alone."""
+    B, H, Hkv, Nq, d = c["B"], c["H"], c["Hkv"], c["Nq"], c["d"]
+    f64 = dict(dtype=torch.float64, device="cuda")
+    back = c["op"] == "cross_bwd"
+    O, lse = torch.zeros((B, H, Nq, d), **f64), torch.full((B, H, Nq), -math.inf, **f64)
+    dQ, dK, dV = (torch.zeros((B, h, n, d), **f64) for h, n in ((H, Nq), (Hkv, c["Nk"]), (Hkv, c["Nk"])))
+    for b in range(B):
+        if s["key_mask"] is not None:
+            at = s["key_mask"][b].nonzero()[:, 0]
+        else:
+            at = torch.arange(c["Nk"] if s["kv_len"] is None else int(s["kv_len"][b]), device="cuda")
+        if at.numel() == 0:
+            continue
+        for h in range(H):
+            kh = h // (H // Hkv)
+            k, v = s["K"][b, kh, at].double(), s["V"][b, kh, at].double()
+            step = max(1, (1 << 27) // at.numel())
+            for a in range(0, Nq, step):
+                q = s["Q"][b, h, a:a + step].double()
+                x = (q @ k.T) * s["scale"]
+                top = torch.logsumexp(x, 1)
+                p = torch.exp(x - top[:, None])
+                if not back:
+                    O[b, h, a:a + step], lse[b, h, a:a + step] = p @ v, top
+                    continue
+                do = s["dO"][b, h, a:a + step].double()
+                g = do @ v.T
+                g = p * (g - (p * g).sum(1, keepdim=True)) * s["scale"]
+                dQ[b, h, a:a + step] = g @ k
+                dK[b, kh, at] += g.T @ q
+                dV[b, kh, at] += p.T @ do
+    return (dQ, dK, dV) if back else (O, lse)
+
+
+def _exact_norm(c, s):
+    rows, cols, groups = c["rows"], c["cols"], c["groups"]
+    back = c["op"] == "ln_bwd"
+    f64 = dict(dtype=torch.float64, device="cuda")
+    y, mean, rstd = torch.empty((rows, cols), **f64), torch.empty(rows, **f64), torch.empty(rows, **f64)
+    dw, db = torch.zeros((groups, cols), **f64), torch.zeros((groups, cols), **f64)
+    per = rows // groups
+    step = max(1, (1 << 26) // cols)
+    for g in range(groups):
+        w, b = s["weight"][g].double(), s["bias"][g].double()
+        for a in range(g * per, (g + 1) * per, step):
+            e = min(a + step, (g + 1) * per)
+            x = s["x"][a:e].double()
+            var, mu = torch.var_mean(x, 1, correction=0)
+            r = 1 / torch.sqrt(var + s["eps"])
+            mean[a:e], rstd[a:e] = mu, r
+            xh = (x - mu[:, None]) * r[:, None]
+            if not back:
+                y[a:e] = xh * w + b
+                continue
+            dy = s["dy"][a:e].double()
+            dw[g] += (dy * xh).sum(0)
+            db[g] += dy.sum(0)
+            t = dy * w
+            y[a:e] = r[:, None] * (t - t.mean(1, keepdim=True) - xh * (t * xh).mean(1, keepdim=True))
+    return (y, dw, db) if back else (y, mean, rstd)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"].startswith("cross"):
+        return _exact_cross(case, s)
+    if case["op"].startswith("ln"):
+        return _exact_norm(case, s)
+    names = [n for n in DTYPES if s["flat_" + n].numel()]
+    norm = torch.sqrt(sum(torch.linalg.vector_norm(s["flat_" + n].double()) ** 2 for n in names))
+    coef = min(1.0, case["max_norm"] / (float(norm) + 1e-6))
+    return dict({n: s["flat_" + n].double() * coef for n in names}, norm=norm)
