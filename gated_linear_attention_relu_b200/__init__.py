@@ -12,3 +12,7 @@ from .binding import (  # noqa: F401
     last_launch_count, load, state_reduce, state_scan, state_update, status_string, workspace,
     workspace_bytes,
 )
+from .block import (  # noqa: F401
+    CrossProblem, NormProblem, clip_grad_norm, cross_backward, cross_forward, cross_workspace, cross_workspace_bytes,
+    grad_norm, layernorm_backward, layernorm_forward, layernorm_workspace, layernorm_workspace_bytes,
+)

@@ -9,7 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblinattn.so")
-SOURCES = [os.path.join(CSRC, "la_api.cu")]
+SOURCES = [os.path.join(CSRC, "la_api.cu"), os.path.join(CSRC, "block_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
     os.path.join(ROOT, "include", "la.h")]
 
@@ -24,7 +24,7 @@ def nvcc() -> str:
 def command(out: str = LIB, extra=()) -> list:
     ptxas = ["-Xptxas", "-v"] if os.environ.get("LA_PTXAS_V") else []
     return [nvcc(), "-std=c++17", "-O3", "-lineinfo",
-            "-gencode", "arch=compute_100a,code=sm_100a", "-Xcompiler", "-fPIC", "-shared",
+            "--threads", "0", "-gencode", "arch=compute_100a,code=sm_100a", "-Xcompiler", "-fPIC", "-shared",
             "-cudart", "shared", *ptxas,
             "-I", os.path.join(ROOT, "include"), "-I", CSRC, *extra, "-o", out, *SOURCES]
 

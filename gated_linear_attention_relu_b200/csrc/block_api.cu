@@ -1,0 +1,757 @@
+// block_api.cu -- the part of the C ABI (include/la.h) for the operators of the block around the
+// token mixer: cross attention, layer norm, gradient norm and clipping.  Argument checks, work
+// planning and kernel launches.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <new>
+#include <utility>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "la.h"
+#include "host.cuh"
+#include "common.cuh"
+#include "sm100.cuh"
+#include "norm.cuh"
+#include "clip.cuh"
+#include "cross_simt.cuh"
+
+namespace la {
+cudaError_t take_block_error(unsigned int* value) {
+  cudaError_t e = cudaMemcpyFromSymbol(value, g_la_error, sizeof *value);
+  if (e != cudaSuccess || *value == 0) return e;
+  const unsigned int zero = 0;
+  return cudaMemcpyToSymbol(g_la_error, &zero, sizeof zero);
+}
+}  // namespace la
+
+namespace {
+
+using la::align256;
+using la::aligned16;
+using la::current_sm_count;
+using la::g_last_launches;
+using la::launch_k;
+using la::set_smem;
+
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1024;
+constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
+
+size_t elem_size(int32_t dtype) { return dtype == LA_BF16 ? 2 : 4; }
+
+// ------------------------------------------------------------------------------- cross attention
+enum Tensor { TQ, TK, TV, TO, TDO, TDQ, TDK, TDV, TENSORS };
+
+struct View {
+  int64_t heads, tokens;
+  la_strides s;
+  bool output;
+};
+
+void cross_views(const la_cross_problem& p, View (&v)[TENSORS]) {
+  v[TQ] = {p.H, p.Nq, p.q, false};
+  v[TK] = {p.Hkv, p.Nk, p.k, false};
+  v[TV] = {p.Hkv, p.Nk, p.v, false};
+  v[TO] = {p.H, p.Nq, p.o, true};
+  v[TDO] = {p.H, p.Nq, p.dout, false};
+  v[TDQ] = {p.H, p.Nq, p.dq, true};
+  v[TDK] = {p.Hkv, p.Nk, p.dk, true};
+  v[TDV] = {p.Hkv, p.Nk, p.dv, true};
+}
+
+// The strides of a tensor that has elements: positive multiples of 16 bytes where the extent is
+// above 1, offsets within 2^62 bytes, and no overlap within an output.
+int check_strides(const la_cross_problem& p, const View& v) {
+  const int64_t ext[3] = {p.B, v.heads, v.tokens};
+  const int64_t str[3] = {v.s.b, v.s.h, v.s.n};
+  if (ext[0] == 0 || ext[1] == 0 || ext[2] == 0) return LA_OK;
+  const int64_t per16 = 16 / int64_t(elem_size(p.dtype));
+  std::pair<int64_t, int64_t> dim[3];
+  int n = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (ext[i] == 1) continue;
+    if (str[i] <= 0) return LA_ERR_SHAPE;
+    if (str[i] % per16) return LA_ERR_ALIGN;
+    if (double(str[i]) * double(ext[i]) > 1.0e18) return LA_ERR_SHAPE;
+    dim[n++] = {str[i], ext[i]};
+  }
+  if (!v.output) return LA_OK;
+  std::sort(dim, dim + n);
+  int64_t span = p.d;  // elements from the first to one past the last of the dimensions so far
+  for (int i = 0; i < n; ++i) {
+    if (dim[i].first < span) return LA_ERR_SHAPE;
+    span += dim[i].first * (dim[i].second - 1);
+  }
+  return LA_OK;
+}
+
+int validate(const la_cross_problem* p, bool backward) {
+  if (!p) return LA_ERR_NULL;
+  if (p->B < 0 || p->H < 0 || p->Hkv < 0 || p->Nq < 0 || p->Nk < 0) return LA_ERR_SHAPE;
+  if (p->dtype != LA_BF16 && p->dtype != LA_F32) return LA_ERR_UNSUPPORTED;
+  if (p->flags & ~uint32_t(LA_FLAG_FORCE_SIMT)) return LA_ERR_UNSUPPORTED;
+  if (p->d != 32 && p->d != 64 && p->d != 128) return LA_ERR_UNSUPPORTED;
+  if (!(p->scale > 0.f) || !std::isfinite(p->scale)) return LA_ERR_SHAPE;
+  const int64_t lim = int64_t(1) << 31;
+  if (p->B >= lim || p->H >= lim || p->Nq > kMaxTokens || p->Nk > kMaxTokens) return LA_ERR_SHAPE;
+  if (p->H > 0 && (p->Hkv == 0 || p->H % p->Hkv)) return LA_ERR_SHAPE;
+  if (p->H == 0 && p->Hkv != 0) return LA_ERR_SHAPE;
+  // tiles and rows stay in 32 (grids) and 62 (offsets) bits
+  const double bh = double(p->B) * double(p->H);
+  if (bh * (double(p->Nq) / 64 + 1) >= double(lim) / 64 || bh * (double(p->Nk) / 64 + 1) >= double(lim) / 64)
+    return LA_ERR_SHAPE;
+  View v[TENSORS];
+  cross_views(*p, v);
+  for (int i = 0; i < (backward ? TENSORS : TDO); ++i)
+    if (const int rc = check_strides(*p, v[i])) return rc;
+  return LA_OK;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// How a long axis of `tiles` is split over blocks where `blocks` alone do not fill the machine:
+// at most as many parts as bring the grid to `want` blocks, each of at least `least` tiles.
+struct Split {
+  int parts, per;  // parts * per >= tiles
+};
+Split split_axis(int64_t tiles, int64_t blocks, int64_t want, int64_t least) {
+  if (tiles <= 0 || blocks <= 0) return {1, static_cast<int>(std::max<int64_t>(tiles, 1))};
+  int64_t parts = std::min(ceil_div(want, blocks), ceil_div(tiles, least));
+  parts = std::max<int64_t>(1, std::min<int64_t>(parts, 1024));
+  const int64_t per = ceil_div(tiles, parts);
+  return {static_cast<int>(ceil_div(tiles, per)), static_cast<int>(per)};
+}
+
+struct CrossPlan {
+  int64_t rows, keys;            // B * H * Nq, B * Hkv * Nk
+  int64_t q_tiles, k_tiles;      // per head
+  Split fwd, dq, dkv;
+  size_t off_o, off_ml;          // forward: partial outputs, maxima and sums
+  size_t off_delta, off_part;    // gradients: D_i, partial sums (dQ, then dK and dV)
+  size_t total;
+};
+
+CrossPlan cross_plan(const la_cross_problem& p, int sm) {
+  CrossPlan c;
+  std::memset(&c, 0, sizeof c);
+  c.rows = p.B * p.H * p.Nq;
+  c.keys = p.B * p.Hkv * p.Nk;
+  c.q_tiles = ceil_div(p.Nq, la::xs::BT);
+  c.k_tiles = ceil_div(p.Nk, la::xs::BT);
+  const int64_t want = 2 * int64_t(sm);
+  const int64_t group = p.Hkv > 0 ? p.H / p.Hkv : 1;
+  c.fwd = split_axis(c.k_tiles, p.B * p.H * c.q_tiles, want, 2);
+  c.dq = split_axis(c.k_tiles, p.B * p.H * c.q_tiles, want, 2);
+  c.dkv = split_axis(c.q_tiles * group, p.B * p.Hkv * c.k_tiles, want, 2);
+  const size_t D = size_t(p.d);
+  size_t fwd = 0;
+  if (c.fwd.parts > 1) {
+    c.off_o = 0;
+    c.off_ml = align256(size_t(c.fwd.parts) * size_t(c.rows) * D * 4);
+    fwd = align256(c.off_ml + size_t(c.fwd.parts) * size_t(c.rows) * 8);
+  }
+  c.off_delta = 0;
+  c.off_part = align256(size_t(c.rows) * 4);
+  const size_t part_dq = c.dq.parts > 1 ? size_t(c.dq.parts) * size_t(c.rows) * D * 4 : 0;
+  const size_t part_kv = c.dkv.parts > 1 ? 2 * size_t(c.dkv.parts) * size_t(c.keys) * D * 4 : 0;
+  c.total = std::max(fwd, align256(c.off_part + std::max(part_dq, part_kv)));
+  return c;
+}
+
+la::xs::Str str(const la_strides& s) { return {s.b, s.h, s.n}; }
+
+la::xs::Args cross_args(const la_cross_problem& p, const CrossPlan& c, const int32_t* kv_len, const uint8_t* mask) {
+  la::xs::Args a;
+  std::memset(&a, 0, sizeof a);
+  a.B = p.B; a.H = p.H; a.Hkv = p.Hkv; a.Nq = p.Nq; a.Nk = p.Nk;
+  a.q_tiles = c.q_tiles;
+  a.k_tiles = c.k_tiles;
+  a.rows = c.rows;
+  a.group = static_cast<int32_t>(p.Hkv > 0 ? p.H / p.Hkv : 1);
+  a.scale = p.scale;
+  a.q = str(p.q); a.k = str(p.k); a.v = str(p.v); a.o = str(p.o);
+  a.dout = str(p.dout); a.dq = str(p.dq); a.dk = str(p.dk); a.dv = str(p.dv);
+  a.kv_len = kv_len;
+  a.mask = mask;
+  return a;
+}
+
+void use(la::xs::Args& a, const Split& s) {
+  a.splits = s.parts;
+  a.tiles_per_split = s.per;
+}
+
+template <int D, typename T>
+int cross_forward_simt(const la_cross_problem& p, const CrossPlan& c, la::xs::Args a, const void* Q, const void* K,
+                       const void* V, void* O, float* lse, uint8_t* ws, cudaStream_t st, int* nl) {
+  use(a, c.fwd);
+  float* part_o = reinterpret_cast<float*>(ws + c.off_o);
+  float2* part_ml = reinterpret_cast<float2*>(ws + c.off_ml);
+  const size_t smem = la::xs::fwd_smem<D>();
+  if (set_smem(la::xs::forward_kernel<D, T>, smem)) return LA_ERR_CUDA;
+  if (launch_k(la::xs::forward_kernel<D, T>, dim3(unsigned(c.q_tiles * c.fwd.parts * p.B * p.H)), la::xs::THREADS, smem, st,
+               false, a, static_cast<const T*>(Q), static_cast<const T*>(K), static_cast<const T*>(V),
+               static_cast<T*>(O), lse, part_o, part_ml))
+    return LA_ERR_CUDA;
+  ++*nl;
+  if (c.fwd.parts > 1) {
+    if (launch_k(la::xs::join_kernel<D, T>, dim3(unsigned(ceil_div(c.rows, la::xs::THREADS / 32))), la::xs::THREADS, 0, st,
+                 true, a, part_o, part_ml, static_cast<T*>(O), lse))
+      return LA_ERR_CUDA;
+    ++*nl;
+  }
+  return LA_OK;
+}
+
+template <int D, typename T>
+int cross_backward_simt(const la_cross_problem& p, const CrossPlan& c, la::xs::Args a, const void* Q, const void* K,
+                        const void* V, const void* O, const float* lse, const void* dO, void* dQ, void* dK, void* dV,
+                        uint8_t* ws, cudaStream_t st, int* nl) {
+  float* delta = reinterpret_cast<float*>(ws + c.off_delta);
+  float* part = reinterpret_cast<float*>(ws + c.off_part);
+  const size_t smem = la::xs::bwd_smem<D>();
+  const T *q = static_cast<const T*>(Q), *k = static_cast<const T*>(K), *v = static_cast<const T*>(V),
+          *g = static_cast<const T*>(dO);
+  bool pdl = false;
+  if (c.rows > 0) {
+    if (launch_k(la::xs::delta_kernel<D, T>, dim3(unsigned(ceil_div(c.rows, la::xs::THREADS / 32))), la::xs::THREADS, 0, st,
+                 false, a, static_cast<const T*>(O), g, delta))
+      return LA_ERR_CUDA;
+    use(a, c.dq);
+    if (set_smem(la::xs::dq_kernel<D, T>, smem)) return LA_ERR_CUDA;
+    if (launch_k(la::xs::dq_kernel<D, T>, dim3(unsigned(c.q_tiles * c.dq.parts * p.B * p.H)), la::xs::THREADS, smem, st, true,
+                 a, q, k, v, g, lse, delta, static_cast<T*>(dQ), part))
+      return LA_ERR_CUDA;
+    *nl += 2;
+    if (c.dq.parts > 1) {
+      if (launch_k(la::xs::sum_kernel<D, T>, dim3(unsigned(ceil_div(c.rows * (D / 2), la::xs::THREADS))), la::xs::THREADS, 0,
+                   st, true, c.rows, p.H, p.Nq, c.dq.parts, part, static_cast<float*>(nullptr), static_cast<T*>(dQ),
+                   static_cast<T*>(nullptr), a.dq, a.dq))
+        return LA_ERR_CUDA;
+      ++*nl;
+    }
+    pdl = true;
+  }
+  if (c.keys > 0) {
+    use(a, c.dkv);
+    float* part_v = part + int64_t(c.dkv.parts) * c.keys * D;
+    if (set_smem(la::xs::dkv_kernel<D, T>, smem)) return LA_ERR_CUDA;
+    if (launch_k(la::xs::dkv_kernel<D, T>, dim3(unsigned(c.k_tiles * c.dkv.parts * p.B * p.Hkv)), la::xs::THREADS, smem, st, pdl,
+                 a, q, k, v, g, lse, delta, static_cast<T*>(dK), static_cast<T*>(dV), part, part_v))
+      return LA_ERR_CUDA;
+    ++*nl;
+    if (c.dkv.parts > 1) {
+      if (launch_k(la::xs::sum_kernel<D, T>, dim3(unsigned(ceil_div(c.keys * (D / 2), la::xs::THREADS)), 2), la::xs::THREADS, 0,
+                   st, true, c.keys, p.Hkv, p.Nk, c.dkv.parts, part, part_v, static_cast<T*>(dK), static_cast<T*>(dV),
+                   a.dk, a.dv))
+        return LA_ERR_CUDA;
+      ++*nl;
+    }
+  }
+  return LA_OK;
+}
+
+template <typename F>
+int with_type(const la_cross_problem& p, F&& f) {
+  auto dim = [&](auto t) {
+    switch (p.d) {
+      case 32: return f(std::integral_constant<int, 32>(), t);
+      case 64: return f(std::integral_constant<int, 64>(), t);
+      default: return f(std::integral_constant<int, 128>(), t);
+    }
+  };
+  return p.dtype == LA_BF16 ? dim(__nv_bfloat16()) : dim(float());
+}
+
+int need(const void* ptr, bool needed) {
+  if (!needed) return LA_OK;
+  if (!ptr) return LA_ERR_NULL;
+  return aligned16(ptr) ? LA_OK : LA_ERR_ALIGN;
+}
+
+// kv_len: 4-byte aligned.  (key_mask has no alignment.)
+int check_len(const int32_t* kv_len) { return (reinterpret_cast<uintptr_t>(kv_len) & 3u) ? LA_ERR_ALIGN : LA_OK; }
+
+// ------------------------------------------------------------------------------- layer norm
+constexpr int64_t kMaxCols = 16384;
+
+int validate(const la_norm_problem* p, bool backward) {
+  if (!p) return LA_ERR_NULL;
+  if (p->dtype != LA_BF16 && p->dtype != LA_F32) return LA_ERR_UNSUPPORTED;
+  if (p->flags) return LA_ERR_UNSUPPORTED;
+  if (p->rows < 0 || p->cols < 1 || p->cols > kMaxCols || p->groups < 1) return LA_ERR_SHAPE;
+  if (p->rows > kMaxTokens || p->groups > kMaxTokens || p->rows % p->groups) return LA_ERR_SHAPE;
+  if (!std::isfinite(p->eps) || p->eps < 0.f) return LA_ERR_SHAPE;
+  if (double(p->groups) * double(p->cols) >= 1.0e12) return LA_ERR_SHAPE;
+  const int64_t s[4] = {p->sx, p->sy, p->sdy, p->sdx};
+  for (int i = 0; i < 4; ++i) {
+    if (p->rows <= 1 || (backward ? i == 1 : i >= 2)) continue;
+    if (s[i] < p->cols || double(s[i]) * double(p->rows) > 1.0e18) return LA_ERR_SHAPE;
+  }
+  return LA_OK;
+}
+
+// Whether rows of `in` (stride si) and of `out` (stride so) are the same rows or share no element.
+bool norm_alias_ok(const la_norm_problem& p, const void* in, int64_t si, const void* out, int64_t so) {
+  const int64_t e = int64_t(elem_size(p.dtype)), last = p.rows - 1;
+  const int64_t a = reinterpret_cast<int64_t>(in), b = reinterpret_cast<int64_t>(out);
+  if (last < 0) return true;
+  if (a == b) return last == 0 || si == so;
+  if (a + (last * si + p.cols) * e <= b || b + (last * so + p.cols) * e <= a) return true;
+  if (last == 0 || si != so) return false;
+  const int64_t s = si * e, d = ((b - a) % s + s) % s;  // columns of one buffer, side by side
+  return d >= p.cols * e && d <= s - p.cols * e;
+}
+
+// Blocks (and slots of dweight and dbias) per group of the backward kernel: enough to fill the
+// machine, each with at least 8 steps over its rows.
+struct NormPlan {
+  int wpr;          // warps per row
+  int parts;
+  size_t total;
+};
+
+template <typename T>
+bool norm_vec(const la_norm_problem& p, int n, const void* const* ptr, const int64_t* stride) {
+  const int64_t vec = 16 / int64_t(sizeof(T));
+  if (p.cols % vec) return false;
+  for (int i = 0; i < n; ++i)
+    if (!aligned16(ptr[i]) || (p.rows > 1 && stride[i] % vec)) return false;
+  return true;
+}
+
+// Per-thread elements are bounded by the registers (16 in the backward pass, which holds the row,
+// its weight and two sums for each; 128 bytes' worth of packs in the forward pass).
+int backward_wpr(int64_t cols, int64_t vec) {
+  const int64_t warp = vec == 1 ? 8 : 16;  // elements per lane of a row that one warp holds
+  if (cols <= 32 * warp) return 1;
+  return cols <= 4096 ? 8 : 16;
+}
+
+NormPlan norm_plan(const la_norm_problem& p, int sm) {
+  NormPlan n;
+  // The slots do not depend on the rows' alignment: both paths fit.
+  const int64_t blocks = int64_t(sm) * 4;
+  int64_t parts = blocks / std::max<int64_t>(p.groups, 1);
+  const int64_t per_group = p.rows / p.groups;
+  n.wpr = 0;
+  n.parts = static_cast<int>(std::max<int64_t>(1, std::min(parts, ceil_div(per_group, 8))));
+  n.total = n.parts > 1 ? align256(2 * size_t(p.groups) * size_t(n.parts) * size_t(p.cols) * 4) : 0;
+  return n;
+}
+
+template <typename T, int VEC, int NV, int WPR>
+int norm_forward(const la::ln::Args& a, const void* x, const float* w, const float* b, void* y, float* mean, float* rstd,
+                 cudaStream_t st) {
+  constexpr int THREADS = 32 * (WPR == 1 ? la::ln::WARP_ROWS : WPR);
+  const int64_t grid = WPR == 1 ? ceil_div(a.rows, la::ln::WARP_ROWS) : a.rows;
+  return launch_k(la::ln::forward_kernel<T, VEC, NV, WPR>, dim3(unsigned(grid)), THREADS, 0, st, false, a,
+                  static_cast<const T*>(x), w, b, static_cast<T*>(y), mean, rstd);
+}
+
+template <typename T>
+int norm_forward_any(const la_norm_problem& p, const la::ln::Args& a, const void* x, const float* w, const float* b, void* y,
+                     float* mean, float* rstd, cudaStream_t st) {
+  const void* ptr[2] = {x, y};
+  const int64_t str[2] = {p.sx, p.sy};
+  const int64_t c = p.cols;
+  if (norm_vec<T>(p, 2, ptr, str)) {
+    constexpr int V = 16 / int(sizeof(T));
+    if (c <= 32 * V) return norm_forward<T, V, 1, 1>(a, x, w, b, y, mean, rstd, st);
+    if (c <= 64 * V) return norm_forward<T, V, 2, 1>(a, x, w, b, y, mean, rstd, st);
+    if (c <= 128 * V) return norm_forward<T, V, 4, 1>(a, x, w, b, y, mean, rstd, st);
+    if (c <= 256 * V) return norm_forward<T, V, 8, 1>(a, x, w, b, y, mean, rstd, st);
+    if (c <= 512 * V) return norm_forward<T, V, 16, 1>(a, x, w, b, y, mean, rstd, st);
+    if (c <= 1024 * V) return norm_forward<T, V, 4, 8>(a, x, w, b, y, mean, rstd, st);
+    if (c <= 2048 * V) return norm_forward<T, V, 4, 16>(a, x, w, b, y, mean, rstd, st);
+    return norm_forward<T, V, 8, 16>(a, x, w, b, y, mean, rstd, st);
+  }
+  if (c <= 32 * 4) return norm_forward<T, 1, 4, 1>(a, x, w, b, y, mean, rstd, st);
+  if (c <= 32 * 16) return norm_forward<T, 1, 16, 1>(a, x, w, b, y, mean, rstd, st);
+  if (c <= 256 * 8) return norm_forward<T, 1, 8, 8>(a, x, w, b, y, mean, rstd, st);
+  if (c <= 512 * 16) return norm_forward<T, 1, 16, 16>(a, x, w, b, y, mean, rstd, st);
+  return norm_forward<T, 1, 32, 16>(a, x, w, b, y, mean, rstd, st);
+}
+
+struct NormGrads {
+  const void *x, *dy;
+  const float *w, *mean, *rstd;
+  void* dx;
+  float *dw, *db;  // or the slots
+};
+
+template <typename T, int VEC, int NV, int WPR>
+int norm_backward(const la::ln::Args& a, int64_t groups, int parts, const NormGrads& g, cudaStream_t st) {
+  constexpr int THREADS = 32 * (WPR == 1 ? la::ln::WARP_ROWS : WPR);
+  const size_t smem = WPR == 1 && (g.dw || g.db) ? size_t(la::ln::WARP_ROWS) * size_t(a.cols) * 4 : 0;
+  return launch_k(la::ln::backward_kernel<T, VEC, NV, WPR>, dim3(unsigned(groups * parts)), THREADS, smem, st, false, a,
+                  parts, static_cast<const T*>(g.x), static_cast<const T*>(g.dy), g.w, g.mean, g.rstd,
+                  static_cast<T*>(g.dx), g.dw, g.db);
+}
+
+template <typename T>
+int norm_backward_any(const la_norm_problem& p, const la::ln::Args& a, int parts, const NormGrads& g, cudaStream_t st) {
+  const void* ptr[3] = {g.x, g.dy, g.dx};
+  const int64_t str[3] = {p.sx, p.sdy, p.sdx};
+  const int64_t c = p.cols, n = p.groups;
+  if (norm_vec<T>(p, 3, ptr, str)) {
+    constexpr int V = 16 / int(sizeof(T));
+    if (c <= 32 * V) return norm_backward<T, V, 1, 1>(a, n, parts, g, st);
+    if (c <= 512) return norm_backward<T, V, 16 / V, 1>(a, n, parts, g, st);
+    if (c <= 2048) return norm_backward<T, V, 8 / V, 8>(a, n, parts, g, st);
+    if (c <= 4096) return norm_backward<T, V, 16 / V, 8>(a, n, parts, g, st);
+    if (c <= 8192) return norm_backward<T, V, 16 / V, 16>(a, n, parts, g, st);
+    return norm_backward<T, V, 32 / V, 16>(a, n, parts, g, st);
+  }
+  if (c <= 32 * 8) return norm_backward<T, 1, 8, 1>(a, n, parts, g, st);
+  if (c <= 256 * 8) return norm_backward<T, 1, 8, 8>(a, n, parts, g, st);
+  if (c <= 256 * 16) return norm_backward<T, 1, 16, 8>(a, n, parts, g, st);
+  if (c <= 512 * 16) return norm_backward<T, 1, 16, 16>(a, n, parts, g, st);
+  return norm_backward<T, 1, 32, 16>(a, n, parts, g, st);
+}
+
+la::ln::Args norm_args(const la_norm_problem& p) {
+  la::ln::Args a;
+  a.rows = p.rows;
+  a.per_group = p.rows / p.groups;
+  a.sx = p.sx; a.sy = p.sy; a.sdy = p.sdy; a.sdx = p.sdx;
+  a.cols = static_cast<int32_t>(p.cols);
+  a.eps = p.eps;
+  a.inv_cols = static_cast<float>(1.0 / double(p.cols));
+  return a;
+}
+
+// ------------------------------------------------------------------------------- gradient clipping
+constexpr int kClipCap = 1024;           // tensors per launch (the list rides in 32 KB of parameters)
+constexpr int kClipBlocksPerSm = 4;
+
+int64_t clip_tables(int64_t count) { return std::max<int64_t>(1, ceil_div(count, kClipCap)); }
+
+size_t clip_need(int64_t count, int sm) { return align256(size_t(clip_tables(count)) * size_t(sm) * kClipBlocksPerSm * 8); }
+
+int validate(const la_grad* g, int64_t count, bool clip) {
+  if (count < 0 || count > (int64_t(1) << 24)) return LA_ERR_SHAPE;
+  if (count > 0 && !g) return LA_ERR_NULL;
+  double bytes = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (g[i].dtype != LA_BF16 && g[i].dtype != LA_F32) return LA_ERR_UNSUPPORTED;
+    if (g[i].reserved) return LA_ERR_UNSUPPORTED;
+    if (g[i].numel < 0) return LA_ERR_SHAPE;
+    bytes += double(g[i].numel) * double(elem_size(g[i].dtype));
+    if (bytes > 1.0e13) return LA_ERR_SHAPE;  // chunk numbers stay in 32 bits
+    if (g[i].numel == 0) continue;
+    const uintptr_t mask = elem_size(g[i].dtype) - 1;
+    if (!g[i].in || (clip && !g[i].out)) return LA_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(g[i].in) & mask) || (clip && (reinterpret_cast<uintptr_t>(g[i].out) & mask)))
+      return LA_ERR_ALIGN;
+  }
+  return LA_OK;
+}
+
+// Outputs may overlap nothing but their own input at the same address.  One sweep over all ranges
+// by rising start: an overlap shows between a range and the furthest end so far (kept for outputs
+// and for inputs apart).
+int clip_overlaps(const la_grad* g, int64_t count) {
+  struct Range {
+    uintptr_t a, b;
+    bool out;
+  };
+  Range* r = new (std::nothrow) Range[size_t(2 * count + 1)];
+  if (!r) return LA_ERR_SHAPE;
+  int64_t n = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (g[i].numel == 0) continue;
+    const uintptr_t bytes = uintptr_t(g[i].numel) * elem_size(g[i].dtype);
+    const uintptr_t o = reinterpret_cast<uintptr_t>(g[i].out), in = reinterpret_cast<uintptr_t>(g[i].in);
+    r[n++] = {o, o + bytes, true};
+    if (in != o) r[n++] = {in, in + bytes, false};  // (in place: the output's range stands for both)
+  }
+  auto before = [](const Range& x, const Range& y) { return x.a < y.a; };
+  if (!std::is_sorted(r, r + n, before)) std::sort(r, r + n, before);
+  uintptr_t end_out = 0, end_in = 0;
+  int rc = LA_OK;
+  for (int64_t i = 0; i < n && rc == LA_OK; ++i) {
+    if (r[i].a < end_out || (r[i].out && r[i].a < end_in)) rc = LA_ERR_SHAPE;
+    uintptr_t& end = r[i].out ? end_out : end_in;
+    end = std::max(end, r[i].b);
+  }
+  delete[] r;
+  return rc;
+}
+
+template <int CAP>
+int64_t fill_table(la::clip::Table<CAP>& t, const la_grad* g, int64_t count) {
+  std::memset(t.f32, 0, sizeof t.f32);
+  int n = 0;
+  int64_t chunks = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (g[i].numel == 0) continue;
+    const int64_t per = la::clip::CHUNK_BYTES / int64_t(elem_size(g[i].dtype));
+    t.in[n] = g[i].in;
+    t.out[n] = g[i].out;
+    t.numel[n] = g[i].numel;
+    t.chunk0[n] = static_cast<uint32_t>(chunks);
+    if (g[i].dtype == LA_F32) t.f32[n >> 5] |= 1u << (n & 31);
+    chunks += ceil_div(g[i].numel, per);
+    ++n;
+  }
+  t.count = n;
+  t.chunks = static_cast<uint32_t>(chunks);
+  return chunks;
+}
+
+template <int CAP>
+int clip_norm_launch(const la_grad* g, int64_t count, int max_blocks, double* partial, int* parts, cudaStream_t st, int* nl) {
+  la::clip::Table<CAP> t;
+  const int64_t chunks = fill_table(t, g, count);
+  if (chunks == 0) return LA_OK;
+  const int64_t blocks = std::min<int64_t>(chunks, max_blocks);
+  if (launch_k(la::clip::norm_kernel<CAP>, dim3(unsigned(blocks)), la::clip::THREADS, 0, st, false, t, partial + *parts))
+    return LA_ERR_CUDA;
+  *parts += static_cast<int>(blocks);
+  ++*nl;
+  return LA_OK;
+}
+
+template <int CAP>
+int clip_scale_launch(const la_grad* g, int64_t count, int max_blocks, const double* partial, int parts, float max_norm,
+                      float* norm, cudaStream_t st, int* nl) {
+  la::clip::Table<CAP> t;
+  const int64_t chunks = fill_table(t, g, count);
+  if (chunks == 0) return LA_OK;
+  const int64_t blocks = std::min<int64_t>(chunks, max_blocks);
+  if (launch_k(la::clip::scale_kernel<CAP>, dim3(unsigned(blocks)), la::clip::THREADS, 0, st, true, t, partial, parts,
+               max_norm, norm))
+    return LA_ERR_CUDA;
+  ++*nl;
+  return LA_OK;
+}
+
+int clip_common(const la_grad* g, int64_t count, bool clip, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                cudaStream_t st) {
+  int rc = validate(g, count, clip);
+  if (rc) return rc;
+  if (!norm) return LA_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(norm) & 3u) return LA_ERR_ALIGN;
+  if (clip && (!std::isfinite(max_norm) || max_norm < 0.f)) return LA_ERR_SHAPE;
+  if (clip && (rc = clip_overlaps(g, count))) return rc;
+  int sm = 0;
+  if ((rc = current_sm_count(&sm))) return rc;
+  if (!ws || ws_bytes < clip_need(count, sm)) return LA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return LA_ERR_ALIGN;
+  double* partial = static_cast<double*>(ws);
+  const int blocks = sm * kClipBlocksPerSm;
+  int nl = 0, parts = 0;
+  // The smallest table that holds a list: launch parameters cost time by their size.
+  auto each = [&](auto&& f) {
+    for (int64_t i = 0; i < count; i += kClipCap) {
+      const int64_t n = std::min<int64_t>(kClipCap, count - i);
+      const int r = n <= 32 ? f(std::integral_constant<int, 32>(), g + i, n)
+                            : n <= 256 ? f(std::integral_constant<int, 256>(), g + i, n)
+                                       : f(std::integral_constant<int, kClipCap>(), g + i, n);
+      if (r) return r;
+    }
+    return int(LA_OK);
+  };
+  if ((rc = each([&](auto cap, const la_grad* p, int64_t n) {
+         return clip_norm_launch<decltype(cap)::value>(p, n, blocks, partial, &parts, st, &nl);
+       })))
+    return rc;
+  if (clip && parts > 0) {
+    float* out = norm;
+    if ((rc = each([&](auto cap, const la_grad* p, int64_t n) {
+           const int before = nl;
+           const int r = clip_scale_launch<decltype(cap)::value>(p, n, blocks, partial, parts, max_norm, out, st, &nl);
+           if (nl > before) out = nullptr;  // the first launch writes the norm
+           return r;
+         })))
+      return rc;
+  } else {
+    if (launch_k(la::clip::finish_kernel, dim3(1), la::clip::THREADS, 0, st, parts > 0, partial, parts, norm)) return LA_ERR_CUDA;
+    ++nl;
+  }
+  g_last_launches = nl;
+  return LA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t la_cross_workspace_bytes_for(const la_cross_problem* p, int sm_count) {
+  if (validate(p, false) != LA_OK || sm_count <= 0) return 0;
+  return std::max<size_t>(cross_plan(*p, sm_count).total, 16);
+}
+
+size_t la_cross_workspace_bytes(const la_cross_problem* p) {
+  int sm = 0;
+  if (validate(p, false) != LA_OK || current_sm_count(&sm) != LA_OK) return 0;
+  return la_cross_workspace_bytes_for(p, sm);
+}
+
+int la_cross_forward(const la_cross_problem* p, const void* Q, const void* K, const void* V, const int32_t* kv_len,
+                     const uint8_t* key_mask, void* O, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  int rc = validate(p, false);
+  if (rc) return rc;
+  const bool has_q = p->B * p->H > 0 && p->Nq > 0, has_k = has_q && p->Nk > 0;
+  if ((rc = need(Q, has_q)) || (rc = need(K, has_k)) || (rc = need(V, has_k)) || (rc = need(O, has_q)) ||
+      (rc = need(lse, has_q && lse)) || (rc = check_len(kv_len)))
+    return rc;
+  if (has_q && (O == Q || (has_k && (O == K || O == V)))) return LA_ERR_SHAPE;  // O is written as K and V are read
+  int sm = 0;
+  if ((rc = current_sm_count(&sm))) return rc;
+  const CrossPlan c = cross_plan(*p, sm);
+  if (c.total > 0 && (!ws || ws_bytes < c.total)) return LA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return LA_ERR_ALIGN;
+  int nl = 0;
+  if (has_q) {
+    const la::xs::Args a = cross_args(*p, c, kv_len, key_mask);
+    rc = with_type(*p, [&](auto d, auto t) {
+      return cross_forward_simt<decltype(d)::value, decltype(t)>(*p, c, a, Q, K, V, O, lse, static_cast<uint8_t*>(ws), stream,
+                                                                 &nl);
+    });
+    if (rc) return rc;
+  }
+  g_last_launches = nl;
+  return LA_OK;
+}
+
+int la_cross_backward(const la_cross_problem* p, const void* Q, const void* K, const void* V, const int32_t* kv_len,
+                      const uint8_t* key_mask, const void* O, const float* lse, const void* dO, void* dQ, void* dK,
+                      void* dV, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  int rc = validate(p, true);
+  if (rc) return rc;
+  const bool has_q = p->B * p->H > 0 && p->Nq > 0, has_k = p->B * p->H > 0 && p->Nk > 0;
+  if ((rc = need(Q, has_q)) || (rc = need(K, has_k)) || (rc = need(V, has_k)) || (rc = need(O, has_q)) ||
+      (rc = need(lse, has_q)) || (rc = need(dO, has_q)) || (rc = need(dQ, has_q)) || (rc = need(dK, has_k)) ||
+      (rc = need(dV, has_k)) || (rc = check_len(kv_len)))
+    return rc;
+  const void* in[5] = {Q, K, V, O, dO};
+  const void* out[3] = {dQ, dK, dV};
+  for (int i = 0; i < 3; ++i) {
+    if (!out[i]) continue;
+    for (const void* x : in)
+      if (x == out[i]) return LA_ERR_SHAPE;  // an input is read after the first gradient is written
+    for (int j = 0; j < i; ++j)
+      if (out[j] == out[i]) return LA_ERR_SHAPE;
+  }
+  int sm = 0;
+  if ((rc = current_sm_count(&sm))) return rc;
+  const CrossPlan c = cross_plan(*p, sm);
+  if (c.total > 0 && (!ws || ws_bytes < c.total)) return LA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return LA_ERR_ALIGN;
+  int nl = 0;
+  const la::xs::Args a = cross_args(*p, c, kv_len, key_mask);
+  rc = with_type(*p, [&](auto d, auto t) {
+    return cross_backward_simt<decltype(d)::value, decltype(t)>(*p, c, a, Q, K, V, O, lse, dO, dQ, dK, dV,
+                                                                static_cast<uint8_t*>(ws), stream, &nl);
+  });
+  if (rc) return rc;
+  g_last_launches = nl;
+  return LA_OK;
+}
+
+size_t la_layernorm_workspace_bytes_for(const la_norm_problem* p, int sm_count) {
+  if (validate(p, false) != LA_OK || sm_count <= 0) return 0;
+  return std::max<size_t>(norm_plan(*p, sm_count).total, 16);
+}
+
+size_t la_layernorm_workspace_bytes(const la_norm_problem* p) {
+  int sm = 0;
+  if (validate(p, false) != LA_OK || current_sm_count(&sm) != LA_OK) return 0;
+  return la_layernorm_workspace_bytes_for(p, sm);
+}
+
+int la_layernorm_forward(const la_norm_problem* p, const void* x, const float* weight, const float* bias, void* y,
+                         float* mean, float* rstd, cudaStream_t stream) {
+  int rc = validate(p, false);
+  if (rc) return rc;
+  const bool has = p->rows > 0;
+  if (has && (!x || !y || !mean != !rstd)) return LA_ERR_NULL;
+  const uintptr_t mask = elem_size(p->dtype) - 1;
+  if ((reinterpret_cast<uintptr_t>(x) & mask) || (reinterpret_cast<uintptr_t>(y) & mask)) return LA_ERR_ALIGN;
+  if (!aligned16(weight) || !aligned16(bias) || !aligned16(mean) || !aligned16(rstd)) return LA_ERR_ALIGN;
+  if (has && !norm_alias_ok(*p, x, p->sx, y, p->sy)) return LA_ERR_SHAPE;
+  if (has) {
+    const la::ln::Args a = norm_args(*p);
+    rc = p->dtype == LA_BF16 ? norm_forward_any<__nv_bfloat16>(*p, a, x, weight, bias, y, mean, rstd, stream)
+                             : norm_forward_any<float>(*p, a, x, weight, bias, y, mean, rstd, stream);
+    if (rc) return rc;
+  }
+  g_last_launches = has ? 1 : 0;
+  return LA_OK;
+}
+
+int la_layernorm_backward(const la_norm_problem* p, const void* x, const void* dy, const float* weight, const float* mean,
+                          const float* rstd, void* dx, float* dweight, float* dbias, void* ws, size_t ws_bytes,
+                          cudaStream_t stream) {
+  int rc = validate(p, true);
+  if (rc) return rc;
+  const bool has = p->rows > 0;
+  if (has && (!x || !dy || !dx || !mean || !rstd)) return LA_ERR_NULL;
+  const uintptr_t mask = elem_size(p->dtype) - 1;
+  for (const void* t : {x, dy, static_cast<const void*>(dx)})
+    if (reinterpret_cast<uintptr_t>(t) & mask) return LA_ERR_ALIGN;
+  for (const float* t : {weight, mean, rstd, static_cast<const float*>(dweight), static_cast<const float*>(dbias)})
+    if (!aligned16(t)) return LA_ERR_ALIGN;
+  if (has && (!norm_alias_ok(*p, x, p->sx, dx, p->sdx) || !norm_alias_ok(*p, dy, p->sdy, dx, p->sdx))) return LA_ERR_SHAPE;
+  int sm = 0;
+  if ((rc = current_sm_count(&sm))) return rc;
+  const NormPlan n = norm_plan(*p, sm);
+  const bool grads = dweight || dbias;
+  if (grads && n.total > 0 && (!ws || ws_bytes < n.total)) return LA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return LA_ERR_ALIGN;
+  int nl = 0;
+  if (!has) {
+    // no rows: the sums are 0 (the parts' slots are not used)
+    const size_t bytes = size_t(p->groups) * size_t(p->cols) * 4;
+    if (dweight && cudaMemsetAsync(dweight, 0, bytes, stream) != cudaSuccess) return LA_ERR_CUDA;
+    if (dbias && cudaMemsetAsync(dbias, 0, bytes, stream) != cudaSuccess) return LA_ERR_CUDA;
+    g_last_launches = 0;
+    return LA_OK;
+  }
+  const la::ln::Args a = norm_args(*p);
+  const bool slots = grads && n.parts > 1;
+  float* s_dw = static_cast<float*>(ws);
+  float* s_db = s_dw + p->groups * int64_t(n.parts) * p->cols;
+  const NormGrads g = {x, dy, weight, mean, rstd, dx, slots ? (dweight ? s_dw : nullptr) : dweight,
+                       slots ? (dbias ? s_db : nullptr) : dbias};
+  rc = p->dtype == LA_BF16 ? norm_backward_any<__nv_bfloat16>(*p, a, n.parts, g, stream)
+                           : norm_backward_any<float>(*p, a, n.parts, g, stream);
+  if (rc) return rc;
+  ++nl;
+  if (slots) {
+    const int64_t blocks = p->groups * ceil_div(p->cols, la::ln::RED_COLS);
+    if (launch_k(la::ln::reduce_kernel, dim3(unsigned(blocks), 2), la::ln::RED_COLS * la::ln::RED_ROWS, 0, stream, true, p->cols,
+                 n.parts, s_dw, s_db, dweight, dbias))
+      return LA_ERR_CUDA;
+    ++nl;
+  }
+  g_last_launches = nl;
+  return LA_OK;
+}
+
+size_t la_clip_workspace_bytes_for(int64_t count, int sm_count) {
+  if (count < 0 || count > (int64_t(1) << 24) || sm_count <= 0) return 0;
+  return clip_need(count, sm_count);
+}
+
+size_t la_clip_workspace_bytes(int64_t count) {
+  int sm = 0;
+  if (current_sm_count(&sm) != LA_OK) return 0;
+  return la_clip_workspace_bytes_for(count, sm);
+}
+
+int la_grad_norm(const la_grad* grads, int64_t count, float* norm, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  return clip_common(grads, count, false, 0.f, norm, ws, ws_bytes, stream);
+}
+
+int la_clip_grad_norm(const la_grad* grads, int64_t count, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                      cudaStream_t stream) {
+  return clip_common(grads, count, true, max_norm, norm, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

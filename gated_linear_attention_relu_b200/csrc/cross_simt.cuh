@@ -1,0 +1,560 @@
+// cross_simt.cuh -- cross attention on the CUDA cores: fp32, and the reference point the
+// tensor-core kernels are measured against (LA_FLAG_FORCE_SIMT).
+//
+//   s_ij = scale q_i.k_j,  o_i = sum_j exp(s_ij - lse_i) v_j   (la_cross_forward / _backward)
+//
+// One pass over the keys with the running maximum and sum of the softmax; 64 x 64 score tiles,
+// 4 x 4 scores a thread, so a step along d feeds 16 FMAs from 8 shared-memory values and the FMA
+// pipe is what bounds it.  Products over many keys (or, in the gradients, many queries) are summed
+// per tile and the tiles' sums then added up, which keeps the rounding of long sums at the level of
+// one tile.  Where there are too few tiles to fill the machine the long axis is split over blocks,
+// whose partial results are joined in order by a second kernel.
+#pragma once
+#include "common.cuh"
+#include "sm100.cuh"
+#include "norm.cuh"
+
+namespace la {
+namespace xs {
+
+constexpr int THREADS = 256;
+constexpr int BT = 64;           // queries and keys per tile
+constexpr int PS = BT + 4;       // row stride (floats) of a score tile
+constexpr float NEG_INF = -__builtin_huge_valf();
+
+struct Str {
+  int64_t b, h, n;
+};
+
+struct Args {
+  int64_t B, H, Hkv, Nq, Nk;
+  int64_t q_tiles, k_tiles;   // tiles of 64 per head
+  int64_t rows;               // B * H * Nq
+  int32_t group;              // H / Hkv
+  int32_t splits, tiles_per_split;
+  float scale;
+  Str q, k, v, o, dout, dq, dk, dv;
+  const int32_t* kv_len;
+  const uint8_t* mask;
+};
+
+__device__ __forceinline__ int64_t key_limit(const Args& a, int64_t b) {
+  if (!a.kv_len) return a.Nk;
+  const int64_t n = a.kv_len[b];
+  return n < 0 ? 0 : (n < a.Nk ? n : a.Nk);
+}
+
+template <int D>
+__host__ __device__ constexpr int row_stride() { return D + 4; }  // floats: 16-byte rows whose float4 columns spread over the banks
+
+// 64 rows of D channels to shared memory as fp32; rows outside [0, valid) and unattended ones
+// (ok given: ok[r] = 0) become 0, whatever memory holds there.
+template <int D, typename T>
+__device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t stride, int valid, const uint8_t* ok) {
+  constexpr int VEC = sizeof(T) == 2 ? 8 : 4;
+  constexpr int PR = D / VEC;
+  for (int e = threadIdx.x; e < BT * PR; e += THREADS) {
+    const int r = e / PR, c = (e % PR) * VEC;
+    float f[VEC];
+    if (r < valid && (!ok || ok[r])) {
+      const ln::Pack<T, VEC> p = *reinterpret_cast<const ln::Pack<T, VEC>*>(src + r * stride + c);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) f[i] = ln::as_f(p.v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) f[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4)
+      *reinterpret_cast<float4*>(dst + r * row_stride<D>() + c + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+  }
+}
+
+// ok[j] = key k0 + j is attended.
+__device__ __forceinline__ void load_ok(const Args& a, int64_t b, int64_t k0, int64_t limit, uint8_t* ok) {
+  if (threadIdx.x < BT) {
+    const int64_t j = k0 + threadIdx.x;
+    ok[threadIdx.x] = j < limit && (!a.mask || a.mask[b * a.Nk + j] != 0);
+  }
+}
+
+// s[ii][jj] = A[ty + 16 ii] . B[tx + 16 jj]
+template <int D>
+__device__ __forceinline__ void mm_nt(const float* A, const float* B, int ty, int tx, float (&s)[4][4]) {
+  uint64_t acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0;
+#pragma unroll 4
+  for (int c = 0; c < D; c += 4) {
+    ulonglong2 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(A + (ty + 16 * i) * row_stride<D>() + c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const ulonglong2*>(B + (tx + 16 * j) * row_stride<D>() + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[i][j] = fma2(x[i].x, y[j].x, acc[i][j]);
+        acc[i][j] = fma2(x[i].y, y[j].y, acc[i][j]);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 t = upk(acc[i][j]);
+      s[i][j] = t.x + t.y;
+    }
+}
+
+// Channel of pair k (of D / 32) of a thread: float4 columns where D has them, else float2.
+template <int D>
+__device__ __forceinline__ int chan(int tx, int k) {
+  return D >= 64 ? 4 * tx + 64 * (k >> 1) + 2 * (k & 1) : 2 * tx;
+}
+
+// t[ii][k] = sum_j P[ty + 16 ii][j] B[j][chan(k)], j over the tile's 64 rows.
+template <int D>
+__device__ __forceinline__ void mm_nn(const float* P, const float* B, int ty, int tx, uint64_t (&t)[4][D / 32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) t[i][k] = 0;
+#pragma unroll 2
+  for (int j = 0; j < BT; j += 4) {
+    float4 p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(P + (ty + 16 * i) * PS + j);
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) {
+      uint64_t b[D / 32];
+      const float* row = B + (j + jj) * row_stride<D>();
+      if constexpr (D >= 64) {
+#pragma unroll
+        for (int k = 0; k < D / 32; k += 2) {
+          const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(row + chan<D>(tx, k));
+          b[k] = u.x;
+          b[k + 1] = u.y;
+        }
+      } else {
+        b[0] = *reinterpret_cast<const uint64_t*>(row + chan<D>(tx, 0));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v = jj == 0 ? p[i].x : (jj == 1 ? p[i].y : (jj == 2 ? p[i].z : p[i].w));
+        const uint64_t vv = pk(v, v);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) t[i][k] = fma2(vv, b[k], t[i][k]);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float lane16_max(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float lane16_sum(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <int D, typename T>
+__device__ __forceinline__ void store_pair(T* dst, float2 v) {
+  if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(v.x, v.y);
+  else
+    *reinterpret_cast<float2*>(dst) = v;
+}
+
+// Block -> (tile, split, head): tiles fastest, so that neighbouring blocks read the same keys.
+struct Where {
+  int64_t tile, b, h;
+  int split;
+};
+__device__ __forceinline__ Where where(const Args& a, int64_t tiles, int64_t heads) {
+  Where w;
+  int64_t i = blockIdx.x;
+  w.tile = i % tiles;
+  i /= tiles;
+  w.split = static_cast<int>(i % a.splits);
+  i /= a.splits;
+  w.h = i % heads;
+  w.b = i / heads;
+  return w;
+}
+
+template <int D>
+__host__ __device__ constexpr size_t fwd_smem() { return (2 * BT * row_stride<D>() + BT * PS) * 4 + BT; }
+
+// Forward.  part_o [splits][rows][D] (sums over the split's keys) and part_ml [splits][rows] (the
+// split's maximum and sum) when splits > 1, else O and lse themselves.
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS)
+forward_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __restrict__ K,
+               const T* __restrict__ V, T* __restrict__ O, float* __restrict__ lse, float* __restrict__ part_o,
+               float2* __restrict__ part_ml) {
+  extern __shared__ __align__(16) float sm[];
+  float* qs = sm;
+  float* kv = qs + BT * row_stride<D>();
+  float* ps = kv + BT * row_stride<D>();
+  uint8_t* ok = reinterpret_cast<uint8_t*>(ps + BT * PS);
+  pdl_trigger();
+  const Where w = where(a, a.q_tiles, a.H);
+  const int64_t kh = w.h / a.group, q0 = w.tile * BT;
+  const int qn = static_cast<int>(a.Nq - q0 < BT ? a.Nq - q0 : BT);
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const int64_t limit = key_limit(a, w.b);
+  const int64_t k_begin = int64_t(w.split) * a.tiles_per_split * BT;
+  int64_t k_end = k_begin + int64_t(a.tiles_per_split) * BT;
+  if (k_end > limit) k_end = limit;
+
+  load_tile<D>(qs, Q + w.b * a.q.b + w.h * a.q.h + q0 * a.q.n, a.q.n, qn, static_cast<const uint8_t*>(nullptr));
+  float m[4], l[4];
+  uint64_t acc[4][D / 32];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = NEG_INF;
+    l[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) acc[i][k] = 0;
+  }
+  for (int64_t k0 = k_begin; k0 < k_end; k0 += BT) {
+    const int kn = static_cast<int>(k_end - k0 < BT ? k_end - k0 : BT);
+    load_ok(a, w.b, k0, limit, ok);
+    __syncthreads();  // (also: the last tile's products have been read)
+    load_tile<D>(kv, K + w.b * a.k.b + kh * a.k.h + k0 * a.k.n, a.k.n, kn, ok);
+    __syncthreads();
+    float s[4][4];
+    mm_nt<D>(qs, kv, ty, tx, s);
+    float corr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mx = NEG_INF;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = ok[tx + 16 * j] ? s[i][j] * a.scale : NEG_INF;
+        mx = fmaxf(mx, s[i][j]);
+      }
+      const float m_new = fmaxf(m[i], lane16_max(mx));
+      const float m_use = m_new == NEG_INF ? 0.f : m_new;  // nothing attended so far
+      corr[i] = m[i] == NEG_INF ? 0.f : expf(m[i] - m_use);
+      m[i] = m_new;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = s[i][j] == NEG_INF ? 0.f : expf(s[i][j] - m_use);
+        sum += p;
+        ps[(ty + 16 * i) * PS + tx + 16 * j] = p;
+      }
+      l[i] = l[i] * corr[i] + lane16_sum(sum);
+    }
+    __syncthreads();  // the keys have been read
+    load_tile<D>(kv, V + w.b * a.v.b + kh * a.v.h + k0 * a.v.n, a.v.n, kn, ok);
+    __syncthreads();
+    uint64_t t[4][D / 32];
+    mm_nn<D>(ps, kv, ty, tx, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t c2 = pk(corr[i], corr[i]);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) acc[i][k] = fma2(acc[i][k], c2, t[i][k]);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty + 16 * i;
+    if (r >= qn) continue;
+    const int64_t row = (w.b * a.H + w.h) * a.Nq + q0 + r;
+    if (a.splits > 1) {
+      const int64_t slot = int64_t(w.split) * a.rows + row;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k)
+        *reinterpret_cast<float2*>(part_o + slot * D + chan<D>(tx, k)) = upk(acc[i][k]);
+      if (tx == 0) part_ml[slot] = make_float2(m[i], l[i]);
+    } else {
+      const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+      T* o = O + w.b * a.o.b + w.h * a.o.h + (q0 + r) * a.o.n;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        const float2 v = upk(acc[i][k]);
+        store_pair<D>(o + chan<D>(tx, k), make_float2(v.x * inv, v.y * inv));
+      }
+      if (lse && tx == 0) lse[row] = l[i] > 0.f ? m[i] + logf(l[i]) : NEG_INF;
+    }
+  }
+}
+
+// Joins the splits' partial results, one warp per row: with M the largest maximum,
+// o = sum_s e^(m_s - M) o_s / sum_s e^(m_s - M) l_s.
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS)
+join_kernel(const __grid_constant__ Args a, const float* __restrict__ part_o, const float2* __restrict__ part_ml,
+            T* __restrict__ O, float* __restrict__ lse) {
+  pdl_wait();
+  const int64_t row = int64_t(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= a.rows) return;
+  float M = NEG_INF;
+  for (int s = 0; s < a.splits; ++s) M = fmaxf(M, part_ml[int64_t(s) * a.rows + row].x);
+  constexpr int C = D / 32;
+  float acc[C], L = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = 0.f;
+  if (M > NEG_INF)
+    for (int s = 0; s < a.splits; ++s) {
+      const int64_t slot = int64_t(s) * a.rows + row;
+      const float2 ml = part_ml[slot];
+      if (ml.x == NEG_INF) continue;
+      const float f = expf(ml.x - M);
+      L += f * ml.y;
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] += f * part_o[slot * D + lane + 32 * c];
+    }
+  const int64_t n = row % a.Nq, bh = row / a.Nq;
+  T* o = O + (bh / a.H) * a.o.b + (bh % a.H) * a.o.h + n * a.o.n;
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) ln::put(o[lane + 32 * c], acc[c] * inv);
+  if (lse && lane == 0) lse[row] = L > 0.f ? M + logf(L) : NEG_INF;
+}
+
+// D_i = dO_i . O_i for every query row, one warp per row.
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS)
+delta_kernel(const __grid_constant__ Args a, const T* __restrict__ O, const T* __restrict__ dO, float* __restrict__ delta) {
+  pdl_trigger();
+  const int64_t row = int64_t(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= a.rows) return;
+  const int64_t n = row % a.Nq, bh = row / a.Nq, b = bh / a.H, h = bh % a.H;
+  const T* o = O + b * a.o.b + h * a.o.h + n * a.o.n;
+  const T* g = dO + b * a.dout.b + h * a.dout.h + n * a.dout.n;
+  float s = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) s += ln::as_f(o[lane + 32 * c]) * ln::as_f(g[lane + 32 * c]);
+  s = ln::warp_sum(s);
+  if (lane == 0) delta[row] = s;
+}
+
+template <int D>
+__host__ __device__ constexpr size_t bwd_smem() { return (4 * BT * row_stride<D>() + BT * PS + 2 * BT) * 4 + BT; }
+
+// dQ of one query tile over the split's keys; part [splits][rows][D] when splits > 1.
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS)
+dq_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __restrict__ K, const T* __restrict__ V,
+          const T* __restrict__ dO, const float* __restrict__ lse, const float* __restrict__ delta,
+          T* __restrict__ dQ, float* __restrict__ part) {
+  extern __shared__ __align__(16) float sm[];
+  constexpr int RS = row_stride<D>();
+  float* qs = sm;
+  float* gs = qs + BT * RS;
+  float* ks = gs + BT * RS;
+  float* vs = ks + BT * RS;
+  float* ps = vs + BT * RS;
+  uint8_t* ok = reinterpret_cast<uint8_t*>(ps + BT * PS + 2 * BT);
+  pdl_trigger();
+  const Where w = where(a, a.q_tiles, a.H);
+  const int64_t kh = w.h / a.group, q0 = w.tile * BT;
+  const int qn = static_cast<int>(a.Nq - q0 < BT ? a.Nq - q0 : BT);
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const int64_t limit = key_limit(a, w.b);
+  const int64_t k_begin = int64_t(w.split) * a.tiles_per_split * BT;
+  int64_t k_end = k_begin + int64_t(a.tiles_per_split) * BT;
+  if (k_end > limit) k_end = limit;
+  const int64_t row0 = (w.b * a.H + w.h) * a.Nq + q0;
+
+  load_tile<D>(qs, Q + w.b * a.q.b + w.h * a.q.h + q0 * a.q.n, a.q.n, qn, static_cast<const uint8_t*>(nullptr));
+  load_tile<D>(gs, dO + w.b * a.dout.b + w.h * a.dout.h + q0 * a.dout.n, a.dout.n, qn, static_cast<const uint8_t*>(nullptr));
+  pdl_wait();
+  float L[4], dl[4];
+  uint64_t acc[4][D / 32];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty + 16 * i;
+    L[i] = r < qn ? lse[row0 + r] : 0.f;
+    dl[i] = r < qn ? delta[row0 + r] : 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) acc[i][k] = 0;
+  }
+  for (int64_t k0 = k_begin; k0 < k_end; k0 += BT) {
+    const int kn = static_cast<int>(k_end - k0 < BT ? k_end - k0 : BT);
+    __syncthreads();
+    load_ok(a, w.b, k0, limit, ok);
+    __syncthreads();
+    load_tile<D>(ks, K + w.b * a.k.b + kh * a.k.h + k0 * a.k.n, a.k.n, kn, ok);
+    load_tile<D>(vs, V + w.b * a.v.b + kh * a.v.h + k0 * a.v.n, a.v.n, kn, ok);
+    __syncthreads();
+    float s[4][4], dp[4][4];
+    mm_nt<D>(qs, ks, ty, tx, s);
+    mm_nt<D>(gs, vs, ty, tx, dp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = ok[tx + 16 * j] ? expf(s[i][j] * a.scale - L[i]) : 0.f;
+        ps[(ty + 16 * i) * PS + tx + 16 * j] = p * (dp[i][j] - dl[i]) * a.scale;
+      }
+    __syncthreads();
+    uint64_t t[4][D / 32];
+    mm_nn<D>(ps, ks, ty, tx, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) acc[i][k] = add2(acc[i][k], t[i][k]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty + 16 * i;
+    if (r >= qn) continue;
+    T* o = dQ + w.b * a.dq.b + w.h * a.dq.h + (q0 + r) * a.dq.n;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+      const float2 v = upk(acc[i][k]);
+      if (a.splits > 1)
+        *reinterpret_cast<float2*>(part + (int64_t(w.split) * a.rows + row0 + r) * D + chan<D>(tx, k)) = v;
+      else
+        store_pair<D>(o + chan<D>(tx, k), v);
+    }
+  }
+}
+
+// dK and dV of one key tile over the split's query tiles (all heads of the group, head after head);
+// part_k, part_v [splits][B * Hkv * Nk][D] when splits > 1.
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS)
+dkv_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __restrict__ K, const T* __restrict__ V,
+           const T* __restrict__ dO, const float* __restrict__ lse, const float* __restrict__ delta,
+           T* __restrict__ dK, T* __restrict__ dV, float* __restrict__ part_k, float* __restrict__ part_v) {
+  extern __shared__ __align__(16) float sm[];
+  constexpr int RS = row_stride<D>();
+  float* qs = sm;
+  float* gs = qs + BT * RS;
+  float* ks = gs + BT * RS;
+  float* vs = ks + BT * RS;
+  float* ps = vs + BT * RS;
+  float* ls = ps + BT * PS;
+  float* ds = ls + BT;
+  uint8_t* ok = reinterpret_cast<uint8_t*>(ds + BT);
+  pdl_trigger();
+  const Where w = where(a, a.k_tiles, a.Hkv);
+  const int64_t k0 = w.tile * BT;
+  const int kn = static_cast<int>(a.Nk - k0 < BT ? a.Nk - k0 : BT);
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const int64_t limit = key_limit(a, w.b);
+  load_ok(a, w.b, k0, limit, ok);
+  __syncthreads();
+  load_tile<D>(ks, K + w.b * a.k.b + w.h * a.k.h + k0 * a.k.n, a.k.n, kn, ok);
+  load_tile<D>(vs, V + w.b * a.v.b + w.h * a.v.h + k0 * a.v.n, a.v.n, kn, ok);
+  pdl_wait();
+  uint64_t ak[4][D / 32], av[4][D / 32];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) ak[i][k] = av[i][k] = 0;
+  const int64_t tiles = a.q_tiles * a.group;
+  const int64_t t0 = int64_t(w.split) * a.tiles_per_split;
+  int64_t t1 = t0 + a.tiles_per_split;
+  if (t1 > tiles) t1 = tiles;
+  if (k0 >= limit) t1 = t0;  // no key of this tile is attended
+  for (int64_t it = t0; it < t1; ++it) {
+    const int64_t h = w.h * a.group + it / a.q_tiles, q0 = (it % a.q_tiles) * BT;
+    const int qn = static_cast<int>(a.Nq - q0 < BT ? a.Nq - q0 : BT);
+    __syncthreads();
+    load_tile<D>(qs, Q + w.b * a.q.b + h * a.q.h + q0 * a.q.n, a.q.n, qn, static_cast<const uint8_t*>(nullptr));
+    load_tile<D>(gs, dO + w.b * a.dout.b + h * a.dout.h + q0 * a.dout.n, a.dout.n, qn, static_cast<const uint8_t*>(nullptr));
+    if (threadIdx.x < BT) {
+      const int64_t row = (w.b * a.H + h) * a.Nq + q0 + threadIdx.x;
+      const bool in = int(threadIdx.x) < qn;
+      ls[threadIdx.x] = in ? lse[row] : 0.f;
+      ds[threadIdx.x] = in ? delta[row] : 0.f;
+    }
+    __syncthreads();
+    float s[4][4], dp[4][4];
+    mm_nt<D>(ks, qs, ty, tx, s);   // s[key][query]
+    mm_nt<D>(vs, gs, ty, tx, dp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = tx + 16 * j;
+        const float p = (ok[ty + 16 * i] && c < qn) ? expf(s[i][j] * a.scale - ls[c]) : 0.f;
+        s[i][j] = p * (dp[i][j] - ds[c]) * a.scale;
+        ps[(ty + 16 * i) * PS + c] = p;
+      }
+    __syncthreads();
+    uint64_t t[4][D / 32];
+    mm_nn<D>(ps, gs, ty, tx, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) av[i][k] = add2(av[i][k], t[i][k]);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ps[(ty + 16 * i) * PS + tx + 16 * j] = s[i][j];
+    __syncthreads();
+    mm_nn<D>(ps, qs, ty, tx, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) ak[i][k] = add2(ak[i][k], t[i][k]);
+  }
+  const int64_t keys = a.B * a.Hkv * a.Nk;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty + 16 * i;
+    if (r >= kn) continue;
+    const int64_t key = (w.b * a.Hkv + w.h) * a.Nk + k0 + r;
+    T* ok_ = dK + w.b * a.dk.b + w.h * a.dk.h + (k0 + r) * a.dk.n;
+    T* ov = dV + w.b * a.dv.b + w.h * a.dv.h + (k0 + r) * a.dv.n;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+      const int c = chan<D>(tx, k);
+      if (a.splits > 1) {
+        const int64_t at = (int64_t(w.split) * keys + key) * D + c;
+        *reinterpret_cast<float2*>(part_k + at) = upk(ak[i][k]);
+        *reinterpret_cast<float2*>(part_v + at) = upk(av[i][k]);
+      } else {
+        store_pair<D>(ok_ + c, upk(ak[i][k]));
+        store_pair<D>(ov + c, upk(av[i][k]));
+      }
+    }
+  }
+}
+
+// out[b, h, n] = sum over the splits, in order, of part[s][(b * heads + h) * N + n]; one thread per
+// pair of channels.  blockIdx.y selects the second output (dV beside dK).
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS)
+sum_kernel(int64_t rows, int64_t heads, int64_t N, int splits, const float* __restrict__ part0, const float* __restrict__ part1,
+           T* __restrict__ out0, T* __restrict__ out1, Str s0, Str s1) {
+  pdl_wait();
+  const int64_t e = int64_t(blockIdx.x) * THREADS + threadIdx.x;
+  const int64_t row = e / (D / 2);
+  const int c = static_cast<int>(e % (D / 2)) * 2;
+  if (row >= rows) return;
+  const float* part = blockIdx.y == 0 ? part0 : part1;
+  T* out = blockIdx.y == 0 ? out0 : out1;
+  const Str st = blockIdx.y == 0 ? s0 : s1;
+  float2 v = make_float2(0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float2 u = *reinterpret_cast<const float2*>(part + (int64_t(s) * rows + row) * D + c);
+    v.x += u.x;
+    v.y += u.y;
+  }
+  const int64_t n = row % N, bh = row / N;
+  store_pair<D>(out + (bh / heads) * st.b + (bh % heads) * st.h + n * st.n + c, v);
+}
+
+}  // namespace xs
+}  // namespace la

@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include "la.h"
+#include "host.cuh"
 #include "common.cuh"
 #include "sm100.cuh"
 #include "state_tc.cuh"
@@ -20,12 +21,23 @@
 #include "simt.cuh"
 #include "simt_ext.cuh"
 
+namespace la {
+thread_local int g_last_launches = 0;
+}
+
 namespace {
 
+using la::align256;
+using la::aligned16;
+using la::current_sm_count;
+using la::encode_fn;
+using la::EncodeTiledFn;
+using la::g_last_launches;
+using la::launch_k;
+using la::launched_ok;
 using la::Plan;
 using la::Rope;
-
-thread_local int g_last_launches = 0;
+using la::set_smem;
 
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1024;  // token indices stay in 32 bits
 
@@ -55,8 +67,6 @@ int validate(const la_problem* p) {
   if (double(p->B) * double(p->H) * (n / 32.0 + double(p->T) + 1.0) >= double(lim - 1)) return LA_ERR_SHAPE;
   return LA_OK;
 }
-
-bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 
 // Checks a tensor pointer that must be present whenever the problem has elements.
 int check_ptr(const void* ptr, bool needed) {
@@ -139,8 +149,6 @@ struct PlanSet {
   int64_t tab_entries;
 };
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 PlanSet make_plans(const la_problem& q, int sm_count) {
   PlanSet s;
   s.tc = q.dtype == LA_BF16 && q.d == 128 && !(q.flags & LA_FLAG_FORCE_SIMT);
@@ -218,30 +226,6 @@ Rope make_rope(const la_problem& q) {
 
 
 // ------------------------------------------------------------------------------- CUDA helpers
-int current_sm_count(int* sm) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return LA_ERR_CUDA;
-  if (cudaDeviceGetAttribute(sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return LA_ERR_CUDA;
-  return LA_OK;
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult qr;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &qr) == cudaSuccess &&
-        qr == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
-}
-
 // [BH, N, 128] bf16 viewed as a 3D tensor {128, N, BH}; boxes of 64 channels x 128 tokens,
 // 128-byte swizzle (the canonical UMMA operand layout).
 bool make_tmap(CUtensorMap* m, const void* base, int64_t BH, int64_t N, uint32_t box_rows = 128) {
@@ -255,36 +239,6 @@ bool make_tmap(CUtensorMap* m, const void* base, int64_t BH, int64_t N, uint32_t
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
-}
-
-int launched_ok() { return cudaGetLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA; }
-
-// Launches `kern`; with `pdl` it may start while the previous kernel in the stream is still
-// running (programmatic stream serialization).  Only kernels whose predecessor in the stream is
-// one of this library's own kernels get `pdl`, and each of them calls pdl_wait() before reading
-// anything produced before it; what they read earlier (K, V, G) was produced before the first
-// kernel of the call, which is launched normally.
-template <typename... KArgs, typename... Args>
-int launch_k(void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, bool pdl,
-             Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
-}
-
-template <typename F>
-int set_smem(F* kern, size_t bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) == cudaSuccess
-             ? LA_OK
-             : LA_ERR_CUDA;
 }
 
 // Optional terms of the full gated form (la_gates), as the launchers see them.
@@ -1022,7 +976,7 @@ const char* la_status_string(int status) {
     case LA_ERR_NULL: return "a required pointer is NULL";
     case LA_ERR_SHAPE: return "invalid or inconsistent sizes";
     case LA_ERR_BANDS: return "RoPE bands must be even, non-negative and add up to d";
-    case LA_ERR_ALIGN: return "a device pointer is not 16-byte aligned";
+    case LA_ERR_ALIGN: return "a device pointer or stride is not 16-byte aligned";
     case LA_ERR_UNSUPPORTED: return "unsupported head dimension, dtype or flag";
     case LA_ERR_WORKSPACE: return "workspace missing or smaller than la_workspace_bytes()";
     case LA_ERR_CUDA: return "a CUDA call or kernel launch failed";
@@ -1033,9 +987,10 @@ const char* la_status_string(int status) {
 
 int la_device_error(cudaStream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return LA_ERR_CUDA;
-  unsigned int v = 0;
+  unsigned int v = 0, block = 0;
   if (cudaMemcpyFromSymbol(&v, la::g_la_error, sizeof v) != cudaSuccess) return LA_ERR_CUDA;
-  if (v == 0) return LA_OK;
+  if (la::take_block_error(&block) != cudaSuccess) return LA_ERR_CUDA;
+  if (v == 0) return block ? LA_ERR_DEVICE : LA_OK;
   const unsigned int zero = 0;
   if (cudaMemcpyToSymbol(la::g_la_error, &zero, sizeof zero) != cudaSuccess) return LA_ERR_CUDA;
   return LA_ERR_DEVICE;

@@ -263,6 +263,121 @@ int la_forward_marked(const la_problem* p, const la_gates* gates, const void* Q,
 int la_forward_bidir_static(const la_problem* p, const void* Q, const void* K, const void* V,
                             const void* G, void* O, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Operators of the block around the token mixer, and of its training step.
+ *
+ * They follow the conventions above, with these differences: tensors may be strided views where
+ * strides are given, rows of every tensor are contiguous, and sizes of zero are allowed (an output
+ * that has elements is still written).  All are bitwise deterministic and allocate nothing.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Element strides of the batch, head and token dimensions of a [B, heads, tokens, d] tensor whose
+ * d channels are contiguous: a dense [B,H,N,d] tensor has {H*N*d, N*d, d}, a [B,N,H,d] projection
+ * read as [B,H,N,d] has {N*H*d, d, H*d}.  A dimension of extent 1 may have any stride; the others
+ * must be positive multiples of 16 bytes.  Outputs must not overlap themselves: taken by rising
+ * stride, each dimension has to step past the whole extent of the ones before it. */
+typedef struct {
+  int64_t b, h, n;
+} la_strides;
+
+/* Cross attention of latent tokens to an encoder's states of another length (the cross-attention
+ * of the DiT block around the mixer: SANA-Video 2.0, Sec. 2, "hybrid" backbone).  Per (b, h):
+ *   s_ij = scale * q_i . k_j over the attended keys j,  lse_i = ln sum_j exp(s_ij),
+ *   o_i  = sum_j exp(s_ij - lse_i) v_j.
+ * Query head h reads key head h / (H / Hkv).  Key j of batch row b is attended when
+ * j < kv_len[b] (kv_len given; values are clamped to [0, Nk]) and key_mask[b][j] != 0 (key_mask
+ * given).  What stands in unattended rows of K and V has no influence, not even infinities and
+ * NaN.  Where nothing is attended, o = 0, lse = -inf and every gradient is 0. */
+typedef struct {
+  int64_t B, H, Hkv;     /* batch, query heads, key/value heads (H a multiple of Hkv) */
+  int64_t Nq, Nk;        /* latent tokens; encoder states per batch row, padding included */
+  int32_t d;             /* head dimension: 32, 64 or 128 */
+  int32_t dtype;         /* la_dtype of Q, K, V, O and of the gradients */
+  float scale;           /* > 0, finite; e.g. 1/sqrt(d) */
+  uint32_t flags;        /* 0 or LA_FLAG_FORCE_SIMT */
+  la_strides q, k, v, o;             /* of Q, K, V and O */
+  la_strides dout, dq, dk, dv;       /* of dO, dQ, dK and dV (la_cross_backward only) */
+} la_cross_problem;
+
+/* Bytes of workspace for both cross-attention calls on the current device / for an SM count;
+ * 0 for an invalid problem. */
+size_t la_cross_workspace_bytes(const la_cross_problem* p);
+size_t la_cross_workspace_bytes_for(const la_cross_problem* p, int sm_count);
+
+/* O [B,H,Nq,d] and, when lse is non-NULL, lse [B,H,Nq] fp32 (dense; natural logarithm).
+ * kv_len: int32 [B] on the device or NULL; key_mask: one byte per key, dense [B,Nk], or NULL. */
+int la_cross_forward(const la_cross_problem* p, const void* Q, const void* K, const void* V, const int32_t* kv_len,
+                     const uint8_t* key_mask, void* O, float* lse, void* workspace, size_t workspace_bytes,
+                     cudaStream_t stream);
+
+/* Gradients, from the forward's O and lse and the output gradient dO: with p_ij = exp(s_ij - lse_i),
+ * D_i = dO_i . O_i and ds_ij = scale * p_ij (dO_i . v_j - D_i),
+ *   dQ_i = sum_j ds_ij k_j,  dK_j = sum_i ds_ij q_i,  dV_j = sum_i p_ij dO_i
+ * (i over the tokens of every query head that reads the key head).  dK and dV rows of unattended
+ * keys are written as 0.  kv_len and key_mask as in the forward call. */
+int la_cross_backward(const la_cross_problem* p, const void* Q, const void* K, const void* V, const int32_t* kv_len,
+                      const uint8_t* key_mask, const void* O, const float* lse, const void* dO, void* dQ, void* dK,
+                      void* dV, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Layer norm over the last dimension of [rows, cols], with the weight and bias of the row's group
+ * (rows / groups consecutive rows form a group: groups = 1 is a plain layer norm, groups = B one
+ * modulated per batch row, weight = 1 + scale_b and bias = shift_b):
+ *   mean = sum x / cols,  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),
+ *   y = (x - mean) rstd weight_g + bias_g. */
+typedef struct {
+  int64_t rows, cols;    /* 1 <= cols <= 16384 */
+  int64_t groups;        /* >= 1, divides rows */
+  int64_t sx, sy;        /* element strides between rows of x and y (>= cols; rows > 1) */
+  int64_t sdy, sdx;      /* the same of dy and dx (la_layernorm_backward only) */
+  float eps;             /* finite, >= 0 */
+  int32_t dtype;         /* la_dtype of x, y, dy and dx */
+  uint32_t flags;        /* 0 */
+} la_norm_problem;
+
+size_t la_layernorm_workspace_bytes(const la_norm_problem* p);
+size_t la_layernorm_workspace_bytes_for(const la_norm_problem* p, int sm_count);
+
+/* weight, bias: fp32 [groups, cols] or NULL (1 and 0); mean, rstd: fp32 [rows], both or neither.
+ * y may be x (same stride).  x and y need the alignment of their type only; rows that are not
+ * 16-byte aligned take a slower path. */
+int la_layernorm_forward(const la_norm_problem* p, const void* x, const float* weight, const float* bias, void* y,
+                         float* mean, float* rstd, cudaStream_t stream);
+
+/* dx and, where given, dweight and dbias (fp32 [groups, cols]), from the forward's mean and rstd:
+ * with xh = (x - mean) rstd and a = dy weight_g,
+ *   dx = rstd (a - mean_c(a) - xh mean_c(a xh)),  dweight_g = sum dy xh,  dbias_g = sum dy
+ * (sums over the group's rows).  dx may be dy or x (same stride). */
+int la_layernorm_backward(const la_norm_problem* p, const void* x, const void* dy, const float* weight,
+                          const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* One gradient of a list: `numel` contiguous elements, aligned to their type. */
+typedef struct {
+  const void* in;
+  void* out;             /* la_clip_grad_norm: where the clipped gradient goes; may be `in` */
+  int64_t numel;         /* >= 0 */
+  int32_t dtype;         /* la_dtype of in and out */
+  int32_t reserved;      /* 0 */
+} la_grad;
+
+size_t la_clip_workspace_bytes(int64_t count);
+size_t la_clip_workspace_bytes_for(int64_t count, int sm_count);
+
+/* norm[0] = sqrt(sum of squares over every element of every tensor), fp32 on the device, over the
+ * whole range of the types (squares neither overflow nor vanish; a norm beyond fp32's range is
+ * handed out as infinity).  The list itself is host memory, read before the call returns.  An empty
+ * list has norm 0. */
+int la_grad_norm(const la_grad* grads, int64_t count, float* norm, void* workspace, size_t workspace_bytes,
+                 cudaStream_t stream);
+
+/* The same norm, and out_i = in_i * min(1, max_norm / (norm + 1e-6)) for every tensor, the
+ * coefficient from the norm in fp64.  An infinite or NaN gradient gives the coefficient 0 or NaN, as
+ * the formula says.  max_norm: finite, >= 0.
+ * Memory that an output writes may be read as that output's own `in` (same address) and as
+ * nothing else: LA_ERR_SHAPE for outputs that overlap one another or another input. */
+int la_clip_grad_norm(const la_grad* grads, int64_t count, float max_norm, float* norm, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream);
+
 /* Static description of a status code. */
 const char* la_status_string(int status);
 
