@@ -18,6 +18,7 @@
 #include "norm.cuh"
 #include "clip.cuh"
 #include "cross_simt.cuh"
+#include "cross_tc.cuh"
 
 namespace la {
 cudaError_t take_block_error(unsigned int* value) {
@@ -126,9 +127,13 @@ Split split_axis(int64_t tiles, int64_t blocks, int64_t want, int64_t least) {
 }
 
 struct CrossPlan {
+  bool tc;                       // tensor-core kernels (bf16)
   int64_t rows, keys;            // B * H * Nq, B * Hkv * Nk
   int64_t q_tiles, k_tiles;      // per head
+  int64_t pairs;                 // pairs of 128-query tiles per head (tensor cores)
+  int64_t pad;                   // rows per head of the gathered keys
   Split fwd, dq, dkv;
+  size_t off_kc, off_vc, off_count, off_place;  // gathered keys
   size_t off_o, off_ml;          // forward: partial outputs, maxima and sums
   size_t off_delta, off_part;    // gradients: D_i, partial sums (dQ, then dK and dV)
   size_t total;
@@ -143,18 +148,31 @@ CrossPlan cross_plan(const la_cross_problem& p, int sm) {
   c.k_tiles = ceil_div(p.Nk, la::xs::BT);
   const int64_t want = 2 * int64_t(sm);
   const int64_t group = p.Hkv > 0 ? p.H / p.Hkv : 1;
-  c.fwd = split_axis(c.k_tiles, p.B * p.H * c.q_tiles, want, 2);
+  c.tc = p.dtype == LA_BF16 && !(p.flags & LA_FLAG_FORCE_SIMT) && c.rows > 0 && c.keys > 0;
+  c.pairs = ceil_div(p.Nq, 2 * la::xt::BM);
+  c.pad = ceil_div(p.Nk, 16) * 16;
+  c.fwd = c.tc ? split_axis(ceil_div(p.Nk, la::xt::BN), p.B * p.H * c.pairs, sm, 4)
+               : split_axis(c.k_tiles, p.B * p.H * c.q_tiles, want, 2);
   c.dq = split_axis(c.k_tiles, p.B * p.H * c.q_tiles, want, 2);
   c.dkv = split_axis(c.q_tiles * group, p.B * p.Hkv * c.k_tiles, want, 2);
   const size_t D = size_t(p.d);
-  size_t fwd = 0;
+  size_t off = 0;
+  if (c.tc) {
+    const size_t rows = size_t(p.B) * size_t(p.Hkv) * size_t(c.pad) * D * 2;
+    c.off_kc = 0;
+    c.off_vc = align256(rows);
+    c.off_count = align256(c.off_vc + rows);
+    c.off_place = align256(c.off_count + size_t(p.B) * 4);
+    off = align256(c.off_place + size_t(p.B) * size_t(p.Nk) * 4);
+  }
+  size_t fwd = off;
   if (c.fwd.parts > 1) {
-    c.off_o = 0;
-    c.off_ml = align256(size_t(c.fwd.parts) * size_t(c.rows) * D * 4);
+    c.off_o = off;
+    c.off_ml = align256(c.off_o + size_t(c.fwd.parts) * size_t(c.rows) * D * 4);
     fwd = align256(c.off_ml + size_t(c.fwd.parts) * size_t(c.rows) * 8);
   }
-  c.off_delta = 0;
-  c.off_part = align256(size_t(c.rows) * 4);
+  c.off_delta = off;
+  c.off_part = align256(c.off_delta + size_t(c.rows) * 4);
   const size_t part_dq = c.dq.parts > 1 ? size_t(c.dq.parts) * size_t(c.rows) * D * 4 : 0;
   const size_t part_kv = c.dkv.parts > 1 ? 2 * size_t(c.dkv.parts) * size_t(c.keys) * D * 4 : 0;
   c.total = std::max(fwd, align256(c.off_part + std::max(part_dq, part_kv)));
@@ -250,6 +268,104 @@ int cross_backward_simt(const la_cross_problem& p, const CrossPlan& c, la::xs::A
         return LA_ERR_CUDA;
       ++*nl;
     }
+  }
+  return LA_OK;
+}
+
+// A [B, heads, tokens, d] bf16 view as a 4D tensor {d, tokens, heads, B}; boxes of 64 channels x 128
+// tokens, 128-byte swizzle (the canonical UMMA operand layout).  Channels and tokens outside read 0.
+bool make_tmap4(CUtensorMap* m, const void* base, int64_t d, int64_t tokens, int64_t heads, int64_t B, const la::xs::Str& s) {
+  la::EncodeTiledFn enc = la::encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(tokens), cuuint64_t(heads), cuuint64_t(B)};
+  // (the stride of a dimension of extent 1 is never used: any legal value)
+  cuuint64_t strides[3] = {tokens > 1 ? cuuint64_t(s.n) * 2 : 256, heads > 1 ? cuuint64_t(s.h) * 2 : 256,
+                           B > 1 ? cuuint64_t(s.b) * 2 : 256};
+  for (cuuint64_t x : strides)
+    if (x >= cuuint64_t(1) << 40) return false;
+  cuuint32_t box[4] = {64, 128, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether the kernel's launch grants at least `regs` registers a thread (what its setmaxnreg split
+// adds up to).
+template <typename F>
+bool launch_regs(F* kern, uint32_t regs) {
+  cudaFuncAttributes at;
+  return cudaFuncGetAttributes(&at, kern) == cudaSuccess && uint32_t(at.numRegs) >= regs;
+}
+
+// The keys as the tensor-core kernels read them: the tensors themselves, or (with lengths or a
+// mask) the attended rows, gathered.
+struct Keys {
+  CUtensorMap k, v;
+  const int32_t* count;
+};
+
+template <int D>
+int prepare_keys(const la_cross_problem& p, const CrossPlan& c, const la::xs::Args& a, const void* K, const void* V,
+                 uint8_t* ws, cudaStream_t st, Keys* out, int* nl) {
+  out->count = nullptr;
+  if (!a.kv_len && !a.mask)
+    return make_tmap4(&out->k, K, D, p.Nk, p.Hkv, p.B, a.k) && make_tmap4(&out->v, V, D, p.Nk, p.Hkv, p.B, a.v) ? LA_OK
+                                                                                                          : LA_ERR_CUDA;
+  __nv_bfloat16* kc = reinterpret_cast<__nv_bfloat16*>(ws + c.off_kc);
+  __nv_bfloat16* vc = reinterpret_cast<__nv_bfloat16*>(ws + c.off_vc);
+  int32_t* count = reinterpret_cast<int32_t*>(ws + c.off_count);
+  const la::xs::Str s = {p.Hkv * c.pad * D, c.pad * D, D};
+  if (!make_tmap4(&out->k, kc, D, c.pad, p.Hkv, p.B, s) || !make_tmap4(&out->v, vc, D, c.pad, p.Hkv, p.B, s))
+    return LA_ERR_CUDA;
+  const int64_t grid = ceil_div(p.Nk, la::xt::G_KEYS) * p.Hkv * p.B;
+  if (launch_k(la::xt::gather_kernel<D>, dim3(unsigned(grid)), la::xt::G_THREADS, 0, st, false, p.Hkv, p.Nk, c.pad,
+               static_cast<const __nv_bfloat16*>(K), static_cast<const __nv_bfloat16*>(V), a.k, a.v, a.kv_len, a.mask, kc, vc,
+               count, reinterpret_cast<int32_t*>(ws + c.off_place)))
+    return LA_ERR_CUDA;
+  out->count = count;
+  ++*nl;
+  return LA_OK;
+}
+
+template <int D>
+int cross_forward_tc(const la_cross_problem& p, const CrossPlan& c, la::xs::Args a, const void* Q, const void* K,
+                     const void* V, void* O, float* lse, uint8_t* ws, int sm, cudaStream_t st, int* nl) {
+  constexpr int DP = D < 64 ? 64 : D;
+  CUtensorMap tq;
+  Keys keys;
+  if (!make_tmap4(&tq, Q, D, p.Nq, p.H, p.B, a.q)) return LA_ERR_CUDA;
+  if (const int rc = prepare_keys<D>(p, c, a, K, V, ws, st, &keys, nl)) return rc;
+  la::xt::Args t;
+  std::memset(&t, 0, sizeof t);
+  t.B = p.B; t.H = p.H; t.Nq = p.Nq; t.Nk = p.Nk;
+  t.rows = c.rows;
+  t.pairs = static_cast<int32_t>(c.pairs);
+  t.group = a.group;
+  t.splits = c.fwd.parts;
+  t.per = c.fwd.per;
+  t.total = p.B * p.H * c.pairs * c.fwd.parts;
+  t.c = p.scale * la::xt::LOG2E;
+  t.count = keys.count;
+  t.o = a.o;
+  // 32-byte stores where every row of O starts on a 32-byte boundary
+  const bool wide = (reinterpret_cast<uintptr_t>(O) & 31) == 0 && (p.Nq == 1 || p.o.n % 16 == 0) &&
+                    (p.H == 1 || p.o.h % 16 == 0) && (p.B == 1 || p.o.b % 16 == 0);
+  auto kern = la::xt::forward_kernel<DP, D>;
+  const size_t smem = la::xt::Cfg<DP>::SMEM;
+  if (set_smem(kern, smem) || !launch_regs(kern, la::xt::REGS_LAUNCH)) return LA_ERR_CUDA;
+  float* part_o = reinterpret_cast<float*>(ws + c.off_o);
+  float2* part_ml = reinterpret_cast<float2*>(ws + c.off_ml);
+  if (launch_k(kern, dim3(unsigned(std::min<int64_t>(t.total, sm))), la::xt::THREADS, smem, st, keys.count != nullptr, tq,
+               keys.k, keys.v, t, static_cast<__nv_bfloat16*>(O), lse, part_o, part_ml, int(wide)))
+    return LA_ERR_CUDA;
+  ++*nl;
+  if (c.fwd.parts > 1) {
+    use(a, c.fwd);
+    if (launch_k(la::xs::join_kernel<D, __nv_bfloat16>, dim3(unsigned(ceil_div(c.rows, la::xs::THREADS / 32))),
+                 la::xs::THREADS, 0, st, true, a, part_o, part_ml, static_cast<__nv_bfloat16*>(O), lse))
+      return LA_ERR_CUDA;
+    ++*nl;
   }
   return LA_OK;
 }
@@ -610,8 +726,12 @@ int la_cross_forward(const la_cross_problem* p, const void* Q, const void* K, co
   if (has_q) {
     const la::xs::Args a = cross_args(*p, c, kv_len, key_mask);
     rc = with_type(*p, [&](auto d, auto t) {
-      return cross_forward_simt<decltype(d)::value, decltype(t)>(*p, c, a, Q, K, V, O, lse, static_cast<uint8_t*>(ws), stream,
-                                                                 &nl);
+      constexpr int D = decltype(d)::value;
+      uint8_t* w = static_cast<uint8_t*>(ws);
+      if constexpr (sizeof(t) == 2) {
+        if (c.tc) return cross_forward_tc<D>(*p, c, a, Q, K, V, O, lse, w, sm, stream, &nl);
+      }
+      return cross_forward_simt<D, decltype(t)>(*p, c, a, Q, K, V, O, lse, w, stream, &nl);
     });
     if (rc) return rc;
   }

@@ -1,0 +1,548 @@
+// cross_tc.cuh -- cross attention forward on the 5th-generation tensor cores (bf16).
+//
+//   s_ij = scale q_i.k_j,  o_i = sum_j exp(s_ij - lse_i) v_j
+//
+// A CTA works on two tiles of 128 queries at a time and walks the keys in tiles of 128.  Per query
+// tile and key tile: S = Q K^T (accumulator in tensor memory), the softmax warps read a row each,
+// keep its running maximum and sum in registers and write P = 2^(S c - m) back to tensor memory as
+// bf16 (rounded once; the sum takes the unrounded values), and O += P V with P as the operand in
+// tensor memory.  The two query tiles alternate, so that the tensor cores work on one while the
+// exponentials of the other are computed.  With c = scale log2(e) and a reference maximum m that is
+// only raised when a row's maximum has grown by more than 2^8 (then O and the sum are rescaled),
+// the accumulator is hardly ever touched between the first and the last key tile.
+// The last key tile is cut to a multiple of 16 keys in both products and to a multiple of 32 in the
+// softmax.
+//
+// Warps (one CTA per SM, persistent; work item = pair of query tiles of a head, or a part of its
+// keys where there are too few items):
+//   0-3, 4-7   softmax of query tile 0 / 1 (thread = row)
+//   8-11       epilogue: O / sum to global memory, a row per thread in 32-byte stores
+//   12, 13     TMA producer, MMA issuer (14, 15 complete the warpgroup)
+// Tensor memory: S (and P) of the two tiles in columns [0, 256), O in [256, 512).
+// Every wait is bounded (mbar_wait).
+#pragma once
+#include "common.cuh"
+#include "cross_simt.cuh"
+#include "sm100.cuh"
+#include "tile_ops.cuh"
+
+namespace la {
+namespace xt {
+
+constexpr int BM = 128, BN = 128;
+constexpr int THREADS = 512;
+constexpr int QST = 3;  // query tiles in shared memory: the two at work and the next one
+constexpr uint32_t HALF = 128 * 128;  // bytes of 128 rows of 64 channels
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float RESCALE = 8.f;  // P stays below 2^8, its sum below Nk 2^8: far inside fp32 and bf16
+
+template <int DP>
+struct Cfg {
+  static constexpr uint32_t TILE = (DP / 64) * HALF;
+  static constexpr int KVST = DP == 128 ? 4 : 8;  // key and value tiles in flight
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_KV = QST * TILE;
+  static constexpr uint32_t OFF_L = OFF_KV + KVST * TILE;
+  static constexpr uint32_t OFF_BAR = OFF_L + 2 * BM * 4;
+  static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;
+};
+static_assert(Cfg<128>::SMEM <= 232448 && Cfg<64>::SMEM <= 232448, "shared memory budget");
+
+constexpr uint32_t S_COL = 0, O_COL = 256;  // + 128 t
+// Registers: 128 a thread at launch (the host checks that), handed on to the softmax warps.
+constexpr uint32_t REGS_LAUNCH = 128, REGS_SOFTMAX = 184, REGS_EPI = 80, REGS_CTRL = 64;
+static_assert(256 * REGS_SOFTMAX + 128 * REGS_EPI + 128 * REGS_CTRL <= THREADS * REGS_LAUNCH, "register split");
+
+template <int DP>
+struct Bars {
+  uint64_t qfull[QST], qempty[QST];
+  uint64_t kvfull[Cfg<DP>::KVST], kvempty[Cfg<DP>::KVST];
+  uint64_t sfull[2], pready[2], pvdone[2], ofull[2], ofree[2], lready[2];
+  uint64_t final_;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(Bars<64>) <= 512, "barrier block too large");
+
+struct Args {
+  int64_t B, H, Nq, Nk, rows;
+  int64_t total;          // work items: B * H * splits * pairs
+  int32_t pairs;          // pairs of query tiles per head
+  int32_t group;          // query heads per key head
+  int32_t splits, per;    // parts of the keys, key tiles per part
+  float c;                // scale * log2(e)
+  const int32_t* count;   // keys per batch row (gathered), or null: Nk
+  xs::Str o;
+};
+
+struct Work {
+  int64_t i;
+  int32_t b, h, pair, split;
+  int32_t k0, nk;   // first key tile, key tiles (0: nothing attended in this part)
+  int32_t keys;     // attended keys of the batch row
+  int32_t nt;       // query tiles with rows
+};
+
+__device__ __forceinline__ Work get_work(const Args& a, int64_t i) {
+  Work w;
+  w.i = i;
+  uint32_t r = static_cast<uint32_t>(i);
+  const uint32_t q = r / static_cast<uint32_t>(a.pairs);
+  w.pair = static_cast<int32_t>(r - q * a.pairs);
+  r = q / static_cast<uint32_t>(a.splits);
+  w.split = static_cast<int32_t>(q - r * a.splits);
+  w.b = static_cast<int32_t>(r / static_cast<uint32_t>(a.H));
+  w.h = static_cast<int32_t>(r - w.b * static_cast<uint32_t>(a.H));
+  w.keys = a.count ? __ldg(a.count + w.b) : static_cast<int32_t>(a.Nk);
+  const int32_t tiles = (w.keys + BN - 1) / BN;
+  w.k0 = w.split * a.per;
+  w.nk = tiles - w.k0 < a.per ? tiles - w.k0 : a.per;
+  if (w.nk < 0) w.nk = 0;
+  w.nt = int64_t(w.pair) * 2 * BM + BM < a.Nq ? 2 : 1;
+  return w;
+}
+// The first item at or after i (in this CTA's steps) that has keys; i >= total: none.
+__device__ __forceinline__ Work next_work(const Args& a, int64_t i) {
+  Work w;
+  w.i = i;
+  w.nk = 0;
+  for (; i < a.total; i += gridDim.x) {
+    w = get_work(a, i);
+    if (w.nk > 0) return w;
+  }
+  w.i = a.total;
+  return w;
+}
+// Attended keys in key tile j of an item.
+__device__ __forceinline__ int tile_keys(const Work& w, int j) {
+  const int left = w.keys - (w.k0 + j) * BN;
+  return left < BN ? left : BN;
+}
+
+template <uint32_t R>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <uint32_t R>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// DP: channels as the tensor cores see them (64 or 128); D: channels of the tensors (32 runs as 64
+// with zeros, which the loads fill in).
+template <int DP, int D>
+__global__ void __launch_bounds__(THREADS, 1)
+forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args a, __nv_bfloat16* __restrict__ O,
+               float* __restrict__ lse, float* __restrict__ part_o, float2* __restrict__ part_ml, int wide) {
+  using C = Cfg<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1k(smem_raw);
+  Bars<DP>* bars = reinterpret_cast<Bars<DP>*>(smem + C::OFF_BAR);
+  const uint32_t sbase = smem_u32(smem);
+  float* inv_l = reinterpret_cast<float*>(smem + C::OFF_L);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bars->abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < QST; ++s) {
+      mbar_init(&bars->qfull[s], 1);
+      mbar_init(&bars->qempty[s], 1);
+    }
+    for (int s = 0; s < C::KVST; ++s) {
+      mbar_init(&bars->kvfull[s], 1);
+      mbar_init(&bars->kvempty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->sfull[t], 1);
+      mbar_init(&bars->pready[t], 4);
+      mbar_init(&bars->pvdone[t], 1);
+      mbar_init(&bars->ofull[t], 1);
+      mbar_init(&bars->ofree[t], 4);
+      mbar_init(&bars->lready[t], 4);
+    }
+    mbar_init(&bars->final_, 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 13) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (warp == 12 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  pdl_trigger();
+  pdl_wait();  // the gathered keys and their counts
+
+  if (warp >= 12) {
+    regs_dec<REGS_CTRL>();
+    if (warp == 12 && lane == 0) {
+      // ---------------------------------------------------------- TMA producer
+      uint32_t qi = 0, ki = 0;
+      bool ok = true;
+      auto load_kv = [&](const CUtensorMap* m, const Work& w, int j) {
+        const uint32_t s = ki % C::KVST;
+        if (!mbar_wait(&bars->kvempty[s], ((ki / C::KVST) & 1) ^ 1, abort_flag, LA_SLEEP_PROD)) return false;
+        uint8_t* dst = smem + C::OFF_KV + s * C::TILE;
+        mbar_arrive_expect_tx(&bars->kvfull[s], C::TILE);
+        const int32_t n = (w.k0 + j) * BN, h = w.h / a.group;
+        tma_load_4d(dst, m, 0, n, h, w.b, &bars->kvfull[s]);
+        if (DP == 128) tma_load_4d(dst + HALF, m, 64, n, h, w.b, &bars->kvfull[s]);
+        ++ki;
+        return true;
+      };
+      for (Work w = next_work(a, blockIdx.x); ok && w.i < a.total; w = next_work(a, w.i + gridDim.x)) {
+        for (int t = 0; ok && t < w.nt; ++t) {
+          const uint32_t s = qi % QST;
+          if (!(ok = mbar_wait(&bars->qempty[s], ((qi / QST) & 1) ^ 1, abort_flag, LA_SLEEP_PROD))) break;
+          uint8_t* dst = smem + C::OFF_Q + s * C::TILE;
+          mbar_arrive_expect_tx(&bars->qfull[s], C::TILE);
+          const int32_t n = (w.pair * 2 + t) * BM;
+          tma_load_4d(dst, &tmQ, 0, n, w.h, w.b, &bars->qfull[s]);
+          if (DP == 128) tma_load_4d(dst + HALF, &tmQ, 64, n, w.h, w.b, &bars->qfull[s]);
+          ++qi;
+          if (t == 0 && !(ok = load_kv(&tmK, w, 0))) break;
+        }
+        for (int j = 0; ok && j < w.nk; ++j) {
+          ok = load_kv(&tmV, w, j);
+          if (ok && j + 1 < w.nk) ok = load_kv(&tmK, w, j + 1);
+        }
+      }
+      if (*abort_flag) {
+        // Let every copy still in flight land before the CTA's shared memory goes away.
+        for (uint32_t j = (qi > QST ? qi - QST : 0); j < qi; ++j) mbar_wait_drain(&bars->qfull[j % QST], (j / QST) & 1);
+        for (uint32_t j = (ki > C::KVST ? ki - C::KVST : 0); j < ki; ++j)
+          mbar_wait_drain(&bars->kvfull[j % C::KVST], (j / C::KVST) & 1);
+      }
+    } else if (warp == 13 && lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      uint32_t qi = 0, ki = 0;                 // query tiles and key/value tiles consumed so far
+      uint32_t steps[2] = {0, 0}, items[2] = {0, 0};
+      bool ok = true;
+      // S_t of (w, j): its Q tile is number q of the ring, its K tile number k.
+      auto issue_s = [&](int t, const Work& w, int j, uint32_t q, uint32_t k) {
+        const uint32_t n16 = static_cast<uint32_t>((tile_keys(w, j) + 15) & ~15);
+        const uint32_t id = idesc_bf16_f32(BM, 16, false, false) - (2u << 17) + ((n16 >> 3) << 17);
+        const uint32_t qa = sbase + C::OFF_Q + (q % QST) * C::TILE, ka = sbase + C::OFF_KV + (k % C::KVST) * C::TILE;
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)
+          mma_bf16(tmem + S_COL + 128u * t, tile::desc_k(qa, kk), tile::desc_k(ka, kk), id, kk > 0);
+        mma_commit(&bars->sfull[t]);
+        if (j == w.nk - 1) mma_commit(&bars->qempty[q % QST]);
+      };
+      Work w = next_work(a, blockIdx.x);
+      if (w.i < a.total) {
+        ok = mbar_wait(&bars->kvfull[0], 0, abort_flag);
+        for (int t = 0; ok && t < w.nt; ++t) {
+          ok = mbar_wait(&bars->qfull[t], 0, abort_flag);
+          tc_fence_after();
+          if (ok) issue_s(t, w, 0, t, 0);
+        }
+        if (ok) mma_commit(&bars->kvempty[0]);
+        qi = w.nt;
+        ki = 1;
+      }
+      while (ok && w.i < a.total) {
+        Work nx = w;
+        for (int j = 0; ok && j < w.nk; ++j) {
+          const bool last = j + 1 == w.nk;
+          if (last) nx = next_work(a, w.i + gridDim.x);
+          const bool more = !last || nx.i < a.total;
+          const int j2 = last ? 0 : j + 1;
+          const uint32_t v = ki++, k = ki;
+          if (more) ++ki;
+          const int nt2 = more ? nx.nt : 0;
+          const uint32_t q0 = last ? qi : qi - static_cast<uint32_t>(w.nt);
+          const int nv = tile_keys(w, j);
+          const int ksteps = (nv + 15) >> 4;
+          for (int t = 0; ok && t < (w.nt > nt2 ? w.nt : nt2); ++t) {
+            if (t < w.nt) {
+              // O_t += P_t V (first of an item: the epilogue has read the last item's O_t)
+              if (t == 0) ok = mbar_wait(&bars->kvfull[v % C::KVST], (v / C::KVST) & 1, abort_flag);
+              if (ok && j == 0) ok = mbar_wait(&bars->ofree[t], (items[t] & 1) ^ 1, abort_flag);
+              ok = ok && mbar_wait(&bars->pready[t], steps[t] & 1, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t va = sbase + C::OFF_KV + (v % C::KVST) * C::TILE;
+              const uint32_t id = idesc_bf16_f32(BM, DP, false, true);
+              for (int kk = 0; kk < ksteps; ++kk)
+                mma_bf16_ts(tmem + O_COL + 128u * t, tmem + S_COL + 128u * t + 8u * kk, tile::desc_mn(va, kk), id,
+                            j > 0 || kk > 0);
+              mma_commit(&bars->pvdone[t]);
+              if (last) mma_commit(&bars->ofull[t]);
+              ++steps[t];
+              if (last) ++items[t];
+              if (t == w.nt - 1) mma_commit(&bars->kvempty[v % C::KVST]);
+            }
+            if (t < nt2) {
+              if (t == 0) ok = mbar_wait(&bars->kvfull[k % C::KVST], (k / C::KVST) & 1, abort_flag);
+              if (ok && last) ok = mbar_wait(&bars->qfull[(q0 + t) % QST], ((q0 + t) / QST) & 1, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(t, nx, j2, q0 + t, k);
+              if (t == nt2 - 1) mma_commit(&bars->kvempty[k % C::KVST]);
+            }
+          }
+        }
+        if (nx.i < a.total) qi += nx.nt;
+        w = nx;
+      }
+      mma_commit(&bars->final_);
+      mbar_wait_drain(&bars->final_, 0);
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax, one row per thread
+    regs_inc<REGS_SOFTMAX>();
+    const int t = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t ts = tmem + S_COL + 128u * t + lane_bits;
+    const uint32_t to = tmem + O_COL + 128u * t + lane_bits;
+    uint32_t step = 0, item = 0;
+    bool ok = true;
+    for (Work w = next_work(a, blockIdx.x); ok && w.i < a.total; w = next_work(a, w.i + gridDim.x)) {
+      if (t >= w.nt) continue;
+      float m = 0.f, l = 0.f;
+      for (int j = 0; j < w.nk; ++j, ++step) {
+        const int nv = tile_keys(w, j);
+        if (!(ok = warp_wait(&bars->sfull[t], step & 1, abort_flag))) break;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (32 * c < nv) tmem_ld_x32(ts + 32 * c, s[c]);
+        tmem_ld_wait();
+        float mx[4] = {xs::NEG_INF, xs::NEG_INF, xs::NEG_INF, xs::NEG_INF};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (32 * c >= nv) break;
+          if (nv - 32 * c < 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i >= nv - 32 * c) s[c][i] = __float_as_uint(xs::NEG_INF);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[c][i]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
+        if (j == 0) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, top > m + RESCALE)) {
+          // rare: raise the reference maximum of the rows that need it
+          const float m2 = top > m + RESCALE ? top : m;
+          const float f = exp2_approx(m - m2);
+          m = m2;
+          l *= f;
+          if (!(ok = warp_wait(&bars->pvdone[t], (step - 1) & 1, abort_flag))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < DP / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld_x16(to + 16 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st_x16(to + 16 * c, o);
+          }
+        }
+        const uint64_t c2 = pk(a.c, a.c), m2 = pk(-m, -m);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (32 * c >= nv) break;
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = upk(fma2(pk(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), c2, m2));
+            const float e0 = exp2_approx(x.x), e1 = exp2_approx(x.y);
+            sum[i & 1] = add2(sum[i & 1], pk(e0, e1));
+            p[i] = pack_bf16(e0, e1);
+          }
+          tmem_st_x16(ts + 16 * c, p);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->pready[t]);
+        const float2 s0 = upk(sum[0]), s1 = upk(sum[1]);
+        l += (s0.x + s0.y) + (s1.x + s1.y);
+      }
+      if (!ok) break;
+      // the epilogue has read the last item's sums
+      if (!(ok = warp_wait(&bars->ofree[t], (item & 1) ^ 1, abort_flag))) break;
+      inv_l[t * BM + row] = 1.f / l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->lready[t]);
+      ++item;
+      const int64_t n = (int64_t(w.pair) * 2 + t) * BM + row;
+      if (n < a.Nq) {
+        const int64_t r = (int64_t(w.b) * a.H + w.h) * a.Nq + n;
+        if (a.splits > 1)
+          part_ml[int64_t(w.split) * a.rows + r] = make_float2(m * LN2, l);
+        else if (lse)
+          lse[r] = (m + __log2f(l)) * LN2;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    regs_dec<REGS_EPI>();
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
+    uint32_t item[2] = {0, 0};
+    bool ok = true;
+    for (int64_t i = blockIdx.x; ok && i < a.total; i += gridDim.x) {
+      const Work w = get_work(a, i);
+      for (int t = 0; t < w.nt; ++t) {
+        const int64_t n = (int64_t(w.pair) * 2 + t) * BM + row;
+        const int64_t r = (int64_t(w.b) * a.H + w.h) * a.Nq + n;
+        __nv_bfloat16* o = O + w.b * a.o.b + w.h * a.o.h + n * a.o.n;
+        float* po = part_o + (int64_t(w.split) * a.rows + r) * D;
+        const bool in = n < a.Nq;
+        float inv = 0.f;
+        if (w.nk > 0) {
+          ok = warp_wait(&bars->ofull[t], item[t] & 1, abort_flag) && warp_wait(&bars->lready[t], item[t] & 1, abort_flag);
+          if (!ok) break;
+          ++item[t];
+          tc_fence_after();
+          inv = inv_l[t * BM + row];
+        } else if (in) {  // nothing attended: o = 0, lse = -inf
+          if (a.splits > 1)
+            part_ml[int64_t(w.split) * a.rows + r] = make_float2(xs::NEG_INF, 0.f);
+          else if (lse)
+            lse[r] = xs::NEG_INF;
+        }
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          if (w.nk > 0) {
+            tmem_ld_x32(tmem + O_COL + 128u * t + lane_bits + 32 * c, v);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = 0;
+          }
+          if (c == D / 32 - 1 && w.nk > 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->ofree[t]);
+          }
+          if (!in) continue;
+          if (a.splits > 1) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t u[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) u[k] = v[e + k];
+              store32(po + 32 * c + e, u, true);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 16) {
+              uint32_t u[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                u[k] = pack_bf16(__uint_as_float(v[e + 2 * k]) * inv, __uint_as_float(v[e + 2 * k + 1]) * inv);
+              store32(o + 32 * c + e, u, wide != 0);
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) tmem_dealloc(tmem, 512);
+}
+
+// Gathers the attended keys: kc, vc [B, Hkv, pad, D] hold the rows of K and V that are attended, in
+// order, then zeros up to a multiple of 16 rows (what lies behind is never read); count[b] is their
+// number and place[b][j] where key j went (-1: unattended).  Unattended rows are not read.
+// One block per 64 keys, head and batch row; each counts the attended keys before its own.
+constexpr int G_THREADS = 256, G_KEYS = 64;
+
+template <int D>
+__global__ void __launch_bounds__(G_THREADS)
+gather_kernel(int64_t Hkv, int64_t Nk, int64_t pad, const __nv_bfloat16* __restrict__ K, const __nv_bfloat16* __restrict__ V,
+              xs::Str sk, xs::Str sv, const int32_t* __restrict__ kv_len, const uint8_t* __restrict__ mask,
+              __nv_bfloat16* __restrict__ kc, __nv_bfloat16* __restrict__ vc, int32_t* __restrict__ count,
+              int32_t* __restrict__ place) {
+  __shared__ int before[G_THREADS / 32];
+  __shared__ int pos[G_KEYS];
+  __shared__ int own[2];
+  pdl_trigger();
+  const int64_t chunks = (Nk + G_KEYS - 1) / G_KEYS;
+  const int64_t chunk = blockIdx.x % chunks, hb = blockIdx.x / chunks;
+  const int64_t h = hb % Hkv, b = hb / Hkv;
+  int64_t limit = Nk;
+  if (kv_len) limit = kv_len[b] < 0 ? 0 : (kv_len[b] < Nk ? kv_len[b] : Nk);
+  const int64_t k0 = chunk * G_KEYS;
+  const uint8_t* mb = mask ? mask + b * Nk : nullptr;
+  const int64_t head = k0 < limit ? k0 : limit;
+  int n = 0;
+  if (mb) {
+    for (int64_t j = threadIdx.x; j < head; j += G_THREADS) n += mb[j] != 0;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if ((threadIdx.x & 31) == 0) before[threadIdx.x >> 5] = n;
+  } else if ((threadIdx.x & 31) == 0) {
+    before[threadIdx.x >> 5] = threadIdx.x == 0 ? static_cast<int>(head) : 0;
+  }
+  bool at = false;
+  uint32_t ball = 0;
+  if (threadIdx.x < G_KEYS) {
+    const int64_t j = k0 + threadIdx.x;
+    at = j < limit && (!mb || mb[j] != 0);
+    ball = __ballot_sync(0xffffffffu, at);
+    if ((threadIdx.x & 31) == 0) own[threadIdx.x >> 5] = __popc(ball);
+  }
+  __syncthreads();
+  int base = 0;
+#pragma unroll
+  for (int i = 0; i < G_THREADS / 32; ++i) base += before[i];
+  if (threadIdx.x < G_KEYS) {
+    const int p = base + (threadIdx.x >= 32 ? own[0] : 0) + __popc(ball & ((1u << (threadIdx.x & 31)) - 1u));
+    pos[threadIdx.x] = at ? p : -1;
+    if (h == 0 && k0 + threadIdx.x < Nk) place[b * Nk + k0 + threadIdx.x] = at ? p : -1;
+  }
+  __syncthreads();
+  constexpr int PR = D / 8;  // 16-byte packs per row
+  const int64_t row0 = (b * Hkv + h) * pad;
+  for (int e = threadIdx.x; e < G_KEYS * PR; e += G_THREADS) {
+    const int r = e / PR, c = (e % PR) * 8;
+    if (pos[r] < 0) continue;
+    const int64_t j = k0 + r, to = (row0 + pos[r]) * D + c;
+    *reinterpret_cast<uint4*>(kc + to) = *reinterpret_cast<const uint4*>(K + b * sk.b + h * sk.h + j * sk.n + c);
+    *reinterpret_cast<uint4*>(vc + to) = *reinterpret_cast<const uint4*>(V + b * sv.b + h * sv.h + j * sv.n + c);
+  }
+  if (chunk == chunks - 1) {
+    const int total = base + own[0] + own[1];
+    if (h == 0 && threadIdx.x == 0) count[b] = total;
+    const int rows = ((total + 15) & ~15) - total;
+    for (int e = threadIdx.x; e < rows * PR; e += G_THREADS) {
+      const int64_t to = (row0 + total + e / PR) * D + (e % PR) * 8;
+      *reinterpret_cast<uint4*>(kc + to) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(vc + to) = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+}  // namespace xt
+}  // namespace la
