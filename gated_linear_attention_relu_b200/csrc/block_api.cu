@@ -19,6 +19,7 @@
 #include "clip.cuh"
 #include "cross_simt.cuh"
 #include "cross_tc.cuh"
+#include "cross_bwd_tc.cuh"
 
 namespace la {
 cudaError_t take_block_error(unsigned int* value) {
@@ -126,6 +127,23 @@ Split split_axis(int64_t tiles, int64_t blocks, int64_t want, int64_t least) {
   return {static_cast<int>(ceil_div(tiles, per)), static_cast<int>(per)};
 }
 
+// The split of a long axis whose parts are summed afterwards: the fewest parts that (nearly) bring
+// the last wave of blocks to an end with the others.  A part costs about 3 tiles of its own.
+Split split_waves(int64_t tiles, int64_t blocks, int64_t sm) {
+  Split best = {1, static_cast<int>(std::max<int64_t>(tiles, 1))};
+  if (tiles <= 0 || blocks <= 0) return best;
+  double cost = 0;
+  for (int64_t s = 1; s <= std::min<int64_t>(std::max<int64_t>(1, 8 * sm / blocks), ceil_div(tiles, 4)); ++s) {
+    const int64_t per = ceil_div(tiles, s), parts = ceil_div(tiles, per);
+    const double c = double(ceil_div(blocks * parts, sm)) * double(per + 3);
+    if (s == 1 || c < 0.97 * cost) {
+      cost = c;
+      best = {static_cast<int>(parts), static_cast<int>(per)};
+    }
+  }
+  return best;
+}
+
 struct CrossPlan {
   bool tc;                       // tensor-core kernels (bf16)
   int64_t rows, keys;            // B * H * Nq, B * Hkv * Nk
@@ -153,8 +171,10 @@ CrossPlan cross_plan(const la_cross_problem& p, int sm) {
   c.pad = ceil_div(p.Nk, 16) * 16;
   c.fwd = c.tc ? split_axis(ceil_div(p.Nk, la::xt::BN), p.B * p.H * c.pairs, sm, 4)
                : split_axis(c.k_tiles, p.B * p.H * c.q_tiles, want, 2);
-  c.dq = split_axis(c.k_tiles, p.B * p.H * c.q_tiles, want, 2);
-  c.dkv = split_axis(c.q_tiles * group, p.B * p.Hkv * c.k_tiles, want, 2);
+  const int64_t q128 = ceil_div(p.Nq, la::xt::BM), k128 = ceil_div(p.Nk, la::xt::BN);
+  c.dq = c.tc ? split_axis(k128, p.B * p.H * q128, sm, 4) : split_axis(c.k_tiles, p.B * p.H * c.q_tiles, want, 2);
+  c.dkv = c.tc ? split_waves(q128 * group, p.B * p.Hkv * k128, sm)
+               : split_axis(c.q_tiles * group, p.B * p.Hkv * c.k_tiles, want, 2);
   const size_t D = size_t(p.d);
   size_t off = 0;
   if (c.tc) {
@@ -174,7 +194,7 @@ CrossPlan cross_plan(const la_cross_problem& p, int sm) {
   c.off_delta = off;
   c.off_part = align256(c.off_delta + size_t(c.rows) * 4);
   const size_t part_dq = c.dq.parts > 1 ? size_t(c.dq.parts) * size_t(c.rows) * D * 4 : 0;
-  const size_t part_kv = c.dkv.parts > 1 ? 2 * size_t(c.dkv.parts) * size_t(c.keys) * D * 4 : 0;
+  const size_t part_kv = c.dkv.parts > 1 || c.tc ? 2 * size_t(c.dkv.parts) * size_t(c.keys) * D * 4 : 0;
   c.total = std::max(fwd, align256(c.off_part + std::max(part_dq, part_kv)));
   return c;
 }
@@ -367,6 +387,70 @@ int cross_forward_tc(const la_cross_problem& p, const CrossPlan& c, la::xs::Args
       return LA_ERR_CUDA;
     ++*nl;
   }
+  return LA_OK;
+}
+
+template <int D>
+int cross_backward_tc(const la_cross_problem& p, const CrossPlan& c, la::xs::Args a, const void* Q, const void* K,
+                      const void* V, const void* O, const float* lse, const void* dO, void* dQ, void* dK, void* dV,
+                      uint8_t* ws, int sm, cudaStream_t st, int* nl) {
+  constexpr int DP = D < 64 ? 64 : D;
+  using T = __nv_bfloat16;
+  CUtensorMap tq, tg;
+  Keys keys;
+  if (!make_tmap4(&tq, Q, D, p.Nq, p.H, p.B, a.q) || !make_tmap4(&tg, dO, D, p.Nq, p.H, p.B, a.dout)) return LA_ERR_CUDA;
+  if (const int rc = prepare_keys<D>(p, c, a, K, V, ws, st, &keys, nl)) return rc;
+  float* delta = reinterpret_cast<float*>(ws + c.off_delta);
+  float* part = reinterpret_cast<float*>(ws + c.off_part);
+  la::xb::Args t;
+  std::memset(&t, 0, sizeof t);
+  t.B = p.B; t.H = p.H; t.Hkv = p.Hkv; t.Nq = p.Nq; t.Nk = p.Nk;
+  t.rows = c.rows;
+  t.keys = c.keys;
+  t.q_tiles = static_cast<int32_t>(ceil_div(p.Nq, la::xt::BM));
+  t.group = a.group;
+  t.c = p.scale * la::xt::LOG2E;
+  t.scale = p.scale;
+  t.count = keys.count;
+  t.o = a.o; t.dout = a.dout; t.dq = a.dq;
+  const bool wide = (reinterpret_cast<uintptr_t>(dQ) & 31) == 0 && (p.Nq == 1 || p.dq.n % 16 == 0) &&
+                    (p.H == 1 || p.dq.h % 16 == 0) && (p.B == 1 || p.dq.b % 16 == 0);
+  auto kq = la::xb::dq_kernel<DP, D>;
+  auto kk = la::xb::dkv_kernel<DP, D>;
+  const size_t mq = la::xb::CfgQ<DP>::SMEM, mk = la::xb::CfgK<DP>::SMEM;
+  if (set_smem(kq, mq) || set_smem(kk, mk) || !launch_regs(kq, la::xb::REGS_LAUNCH) || !launch_regs(kk, la::xb::REGS_LAUNCH))
+    return LA_ERR_CUDA;
+  // dQ (and D_i, which the dK / dV kernel reads)
+  t.tiles = t.q_tiles;
+  t.splits = c.dq.parts;
+  t.per = c.dq.per;
+  t.total = p.B * p.H * int64_t(t.tiles) * t.splits;
+  if (launch_k(kq, dim3(unsigned(std::min<int64_t>(t.total, sm))), la::xb::THREADS, mq, st, keys.count != nullptr, tq, tg,
+               keys.k, keys.v, t, static_cast<const T*>(O), static_cast<const T*>(dO), lse, delta, static_cast<T*>(dQ), part,
+               int(wide)))
+    return LA_ERR_CUDA;
+  ++*nl;
+  if (c.dq.parts > 1) {
+    if (launch_k(la::xs::sum_kernel<D, T>, dim3(unsigned(ceil_div(c.rows * (D / 2), la::xs::THREADS))), la::xs::THREADS, 0, st,
+                 true, c.rows, p.H, p.Nq, c.dq.parts, part, static_cast<float*>(nullptr), static_cast<T*>(dQ),
+                 static_cast<T*>(nullptr), a.dq, a.dq))
+      return LA_ERR_CUDA;
+    ++*nl;
+  }
+  t.tiles = static_cast<int32_t>(ceil_div(p.Nk, la::xt::BN));
+  t.splits = c.dkv.parts;
+  t.per = c.dkv.per;
+  t.total = p.B * p.Hkv * int64_t(t.tiles) * t.splits;
+  float* part_v = part + int64_t(c.dkv.parts) * c.keys * D;
+  if (launch_k(kk, dim3(unsigned(std::min<int64_t>(t.total, sm))), la::xb::THREADS, mk, st, true, tq, tg, keys.k, keys.v, t,
+               lse, delta, part, part_v))
+    return LA_ERR_CUDA;
+  if (launch_k(la::xb::sum_kernel<D>, dim3(unsigned(ceil_div(c.keys * (D / 2), 256)), 2), 256, 0, st, true, c.keys, p.Hkv,
+               p.Nk, c.dkv.parts, part, part_v,
+               keys.count ? reinterpret_cast<const int32_t*>(ws + c.off_place) : static_cast<const int32_t*>(nullptr),
+               static_cast<T*>(dK), static_cast<T*>(dV), a.dk, a.dv))
+    return LA_ERR_CUDA;
+  *nl += 2;
   return LA_OK;
 }
 
@@ -766,8 +850,12 @@ int la_cross_backward(const la_cross_problem* p, const void* Q, const void* K, c
   int nl = 0;
   const la::xs::Args a = cross_args(*p, c, kv_len, key_mask);
   rc = with_type(*p, [&](auto d, auto t) {
-    return cross_backward_simt<decltype(d)::value, decltype(t)>(*p, c, a, Q, K, V, O, lse, dO, dQ, dK, dV,
-                                                                static_cast<uint8_t*>(ws), stream, &nl);
+    constexpr int D = decltype(d)::value;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    if constexpr (sizeof(t) == 2) {
+      if (c.tc) return cross_backward_tc<D>(*p, c, a, Q, K, V, O, lse, dO, dQ, dK, dV, w, sm, stream, &nl);
+    }
+    return cross_backward_simt<D, decltype(t)>(*p, c, a, Q, K, V, O, lse, dO, dQ, dK, dV, w, stream, &nl);
   });
   if (rc) return rc;
   g_last_launches = nl;

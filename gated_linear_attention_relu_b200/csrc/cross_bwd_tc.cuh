@@ -1,0 +1,842 @@
+// cross_bwd_tc.cuh -- gradients of cross attention on the 5th-generation tensor cores (bf16).
+//
+//   p_ij = exp(s_ij - lse_i),  D_i = dO_i . O_i,  ds_ij = p_ij (dO_i . v_j - D_i)
+//   dQ_i = scale sum_j ds_ij k_j,  dK_j = scale sum_i ds_ij q_i,  dV_j = sum_i p_ij dO_i
+//
+// Two kernels, so that every sum has one owner and a fixed order (no atomics): dq_kernel keeps a
+// query tile and walks the keys, dkv_kernel keeps a key tile and walks the queries.  Each forms the
+// scores and dP = dO V^T again (7 products of a tile pair instead of 5).  p and ds go back to tensor
+// memory as bf16 (rounded once each) as the operand of the product that follows; the softmax scale
+// is applied to the fp32 sums at the end.
+//
+// dq_kernel, tensor memory: S of even and odd steps [0, 256), dP [256, 384), dQ [384, 512); ds
+// overwrites its S.  S of the next step and dP of the next step are computed while the math warps
+// work on this one.
+// dkv_kernel, scores transposed (keys are the rows): S^T [0, 128), dP^T [128, 256), dV [256, 384),
+// dK [384, 512); p overwrites S^T, ds overwrites dP^T.  dV of this step and S^T of the next run while
+// the math warps form ds, dK and the next dP^T while they form the next p.
+//
+// Warps: 0-7 math (warps 0-3 the first 64 columns of a tile, 4-7 the others; thread = row);
+// 8-11 dq: D_i of the next query tile, dQ to memory; dkv: lse and D of the query tiles to come;
+// 12 TMA producer, 13 MMA issuer.  One CTA per SM, persistent.  Every wait is bounded.
+#pragma once
+#include "cross_tc.cuh"
+
+namespace la {
+namespace xb {
+
+using xt::BM;
+using xt::BN;
+using xt::HALF;
+using xt::LOG2E;
+using xt::regs_dec;
+using xt::regs_inc;
+using xt::store32;
+
+constexpr int THREADS = 512;
+constexpr uint32_t REGS_LAUNCH = 128, REGS_MATH = 184, REGS_AUX = 80, REGS_CTRL = 64;
+static_assert(256 * REGS_MATH + 128 * REGS_AUX + 128 * REGS_CTRL <= THREADS * REGS_LAUNCH, "register split");
+
+struct Args {
+  int64_t B, H, Hkv, Nq, Nk, rows, keys;
+  int64_t total;          // work items
+  int32_t tiles;          // dq: query tiles per head; dkv: key tiles per head
+  int32_t q_tiles;        // query tiles per head
+  int32_t group;
+  int32_t splits, per;    // dq: parts of the keys; dkv: parts of the group's query tiles
+  float c, scale;         // scale * log2(e), scale
+  const int32_t* count;
+  xs::Str o, dout, dq;
+};
+
+// ------------------------------------------------------------------------------------ dQ
+template <int DP>
+struct CfgQ {
+  static constexpr uint32_t TILE = (DP / 64) * HALF;
+  static constexpr int QST = DP == 128 ? 3 : 4;   // Q and dO tiles, in turn
+  static constexpr int KST = DP == 128 ? 2 : 4;
+  static constexpr int VST = DP == 128 ? 2 : 4;
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_K = QST * TILE;
+  static constexpr uint32_t OFF_V = OFF_K + KST * TILE;
+  static constexpr uint32_t OFF_D = OFF_V + VST * TILE;
+  static constexpr uint32_t OFF_BAR = OFF_D + 2 * BM * 4;
+  static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;
+};
+static_assert(CfgQ<128>::SMEM <= 232448 && CfgQ<64>::SMEM <= 232448, "shared memory budget");
+
+template <int DP>
+struct BarsQ {
+  uint64_t qfull[CfgQ<DP>::QST], qempty[CfgQ<DP>::QST];
+  uint64_t kfull[CfgQ<DP>::KST], kempty[CfgQ<DP>::KST];
+  uint64_t vfull[CfgQ<DP>::VST], vempty[CfgQ<DP>::VST];
+  uint64_t sfull[2], dsready[2], dready[2];
+  uint64_t dpfull, dpfree, dqfull, dqfree, final_;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(BarsQ<64>) <= 512, "barrier block too large");
+
+constexpr uint32_t Q_S = 0, Q_DP = 256, Q_DQ = 384;
+
+struct WorkQ {
+  int64_t i;
+  int32_t b, h, qt, split;
+  int32_t k0, nk, keys;
+};
+__device__ __forceinline__ WorkQ get_q(const Args& a, int64_t i) {
+  WorkQ w;
+  w.i = i;
+  uint32_t r = static_cast<uint32_t>(i);
+  const uint32_t q = r / static_cast<uint32_t>(a.tiles);
+  w.qt = static_cast<int32_t>(r - q * a.tiles);
+  r = q / static_cast<uint32_t>(a.splits);
+  w.split = static_cast<int32_t>(q - r * a.splits);
+  w.b = static_cast<int32_t>(r / static_cast<uint32_t>(a.H));
+  w.h = static_cast<int32_t>(r - w.b * static_cast<uint32_t>(a.H));
+  w.keys = a.count ? __ldg(a.count + w.b) : static_cast<int32_t>(a.Nk);
+  w.k0 = w.split * a.per;
+  const int32_t tiles = (w.keys + BN - 1) / BN - w.k0;
+  w.nk = tiles < a.per ? tiles : a.per;
+  if (w.nk < 0) w.nk = 0;
+  return w;
+}
+__device__ __forceinline__ WorkQ next_q(const Args& a, int64_t i) {
+  WorkQ w;
+  w.nk = 0;
+  for (; i < a.total; i += gridDim.x) {
+    w = get_q(a, i);
+    if (w.nk > 0) return w;
+  }
+  w.i = a.total;
+  return w;
+}
+__device__ __forceinline__ int keys_of(const WorkQ& w, int j) {
+  const int left = w.keys - (w.k0 + j) * BN;
+  return left < BN ? left : BN;
+}
+
+template <int DP>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* m, int32_t n, int32_t h, int32_t b, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, (DP / 64) * HALF);
+  tma_load_4d(dst, m, 0, n, h, b, bar);
+  if (DP == 128) tma_load_4d(dst + HALF, m, 64, n, h, b, bar);
+}
+
+// Instruction descriptor of a product with N columns (a multiple of 16).
+__device__ __forceinline__ uint32_t idesc_n(uint32_t n) {
+  return idesc_bf16_f32(BM, 16, false, false) - (2u << 17) + ((n >> 3) << 17);
+}
+
+// Drains the copies of a ring that were issued and may still be in flight.
+__device__ __forceinline__ void drain(uint64_t* full, uint32_t stages, uint32_t issued) {
+  for (uint32_t j = issued > stages ? issued - stages : 0; j < issued; ++j)
+    mbar_wait_drain(&full[j % stages], (j / stages) & 1);
+}
+
+template <int DP, int D>
+__global__ void __launch_bounds__(THREADS, 1)
+dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
+          const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+          const __grid_constant__ Args a, const __nv_bfloat16* __restrict__ O, const __nv_bfloat16* __restrict__ dO,
+          const float* __restrict__ lse, float* __restrict__ delta, __nv_bfloat16* __restrict__ dQ,
+          float* __restrict__ part, int wide) {
+  using C = CfgQ<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1k(smem_raw);
+  BarsQ<DP>* bars = reinterpret_cast<BarsQ<DP>*>(smem + C::OFF_BAR);
+  const uint32_t sbase = smem_u32(smem);
+  float* d_sm = reinterpret_cast<float*>(smem + C::OFF_D);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bars->abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::QST; ++s) mbar_init(&bars->qfull[s], 1), mbar_init(&bars->qempty[s], 1);
+    for (int s = 0; s < C::KST; ++s) mbar_init(&bars->kfull[s], 1), mbar_init(&bars->kempty[s], 1);
+    for (int s = 0; s < C::VST; ++s) mbar_init(&bars->vfull[s], 1), mbar_init(&bars->vempty[s], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->sfull[s], 1);
+      mbar_init(&bars->dsready[s], 8);
+      mbar_init(&bars->dready[s], 4);
+    }
+    mbar_init(&bars->dpfull, 1);
+    mbar_init(&bars->dpfree, 8);
+    mbar_init(&bars->dqfull, 1);
+    mbar_init(&bars->dqfree, 4);
+    mbar_init(&bars->final_, 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 13) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (warp == 12 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmG);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  pdl_trigger();
+  pdl_wait();  // the gathered keys and their counts
+
+  if (warp >= 12) {
+    regs_dec<REGS_CTRL>();
+    if (warp == 12 && lane == 0) {
+      // ---------------------------------------------------------- TMA producer
+      uint32_t qi = 0, ki = 0;
+      bool ok = true;
+      auto load_q = [&](const CUtensorMap* m, const WorkQ& w) {
+        const uint32_t s = qi % C::QST;
+        if (!mbar_wait(&bars->qempty[s], ((qi / C::QST) & 1) ^ 1, abort_flag, LA_SLEEP_PROD)) return false;
+        load_tile<DP>(smem + C::OFF_Q + s * C::TILE, m, w.qt * BM, w.h, w.b, &bars->qfull[s]);
+        ++qi;
+        return true;
+      };
+      for (WorkQ w = next_q(a, blockIdx.x); ok && w.i < a.total; w = next_q(a, w.i + gridDim.x)) {
+        const int32_t kh = w.h / a.group;
+        for (int j = 0; ok && j < w.nk; ++j, ++ki) {
+          const int32_t n = (w.k0 + j) * BN;
+          if (j == 0 && !(ok = load_q(&tmQ, w))) break;
+          const uint32_t sk = ki % C::KST, sv = ki % C::VST;
+          if (!(ok = mbar_wait(&bars->kempty[sk], ((ki / C::KST) & 1) ^ 1, abort_flag, LA_SLEEP_PROD))) break;
+          load_tile<DP>(smem + C::OFF_K + sk * C::TILE, &tmK, n, kh, w.b, &bars->kfull[sk]);
+          if (j == 0) ok = load_q(&tmG, w);
+          if (ok) ok = mbar_wait(&bars->vempty[sv], ((ki / C::VST) & 1) ^ 1, abort_flag, LA_SLEEP_PROD);
+          if (!ok) {
+            mbar_wait_drain(&bars->kfull[sk], (ki / C::KST) & 1);
+            break;
+          }
+          load_tile<DP>(smem + C::OFF_V + sv * C::TILE, &tmV, n, kh, w.b, &bars->vfull[sv]);
+        }
+      }
+      if (*abort_flag) {
+        // Let every copy still in flight land before the CTA's shared memory goes away.
+        drain(bars->qfull, C::QST, qi);
+        drain(bars->kfull, C::KST, ki);
+        drain(bars->vfull, C::VST, ki);
+      }
+    } else if (warp == 13 && lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      uint32_t i = 0, items = 0;  // steps (key tiles) and items done
+      bool ok = true;
+      auto issue_s = [&](const WorkQ& w, int j, uint32_t step, uint32_t item) {
+        const uint32_t qs = (2 * item) % C::QST, ks = step % C::KST;
+        ok = mbar_wait(&bars->kfull[ks], (step / C::KST) & 1, abort_flag);
+        if (ok && j == 0) ok = mbar_wait(&bars->qfull[qs], ((2 * item) / C::QST) & 1, abort_flag);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t id = idesc_n(static_cast<uint32_t>((keys_of(w, j) + 15) & ~15));
+        const uint32_t qa = sbase + C::OFF_Q + qs * C::TILE, ka = sbase + C::OFF_K + ks * C::TILE;
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)
+          mma_bf16(tmem + Q_S + 128u * (step & 1), tile::desc_k(qa, kk), tile::desc_k(ka, kk), id, kk > 0);
+        mma_commit(&bars->sfull[step & 1]);
+        if (j == w.nk - 1) mma_commit(&bars->qempty[qs]);
+      };
+      auto issue_dp = [&](const WorkQ& w, int j, uint32_t step, uint32_t item) {
+        const uint32_t gs = (2 * item + 1) % C::QST, vs = step % C::VST;
+        ok = mbar_wait(&bars->vfull[vs], (step / C::VST) & 1, abort_flag);
+        if (ok && j == 0) ok = mbar_wait(&bars->qfull[gs], ((2 * item + 1) / C::QST) & 1, abort_flag);
+        // the math warps have read the last dP
+        if (ok) ok = mbar_wait(&bars->dpfree, (step & 1) ^ 1, abort_flag);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t id = idesc_n(static_cast<uint32_t>((keys_of(w, j) + 15) & ~15));
+        const uint32_t ga = sbase + C::OFF_Q + gs * C::TILE, va = sbase + C::OFF_V + vs * C::TILE;
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)
+          mma_bf16(tmem + Q_DP, tile::desc_k(ga, kk), tile::desc_k(va, kk), id, kk > 0);
+        mma_commit(&bars->dpfull);
+        mma_commit(&bars->vempty[vs]);
+        if (j == w.nk - 1) mma_commit(&bars->qempty[gs]);
+      };
+      WorkQ w = next_q(a, blockIdx.x);
+      if (w.i < a.total) {
+        issue_s(w, 0, 0, 0);
+        if (ok) issue_dp(w, 0, 0, 0);
+      }
+      while (ok && w.i < a.total) {
+        WorkQ nx = w;
+        for (int j = 0; ok && j < w.nk; ++j, ++i) {
+          const bool last = j + 1 == w.nk;
+          if (last) nx = next_q(a, w.i + gridDim.x);
+          if (!last || nx.i < a.total) {
+            issue_s(nx, last ? 0 : j + 1, i + 1, items + (last ? 1 : 0));
+            if (ok) issue_dp(nx, last ? 0 : j + 1, i + 1, items + (last ? 1 : 0));
+            if (!ok) break;
+          }
+          // dQ += ds K
+          ok = mbar_wait(&bars->dsready[i & 1], (i >> 1) & 1, abort_flag);
+          if (ok && j == 0) ok = mbar_wait(&bars->dqfree, (items & 1) ^ 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const int ksteps = (keys_of(w, j) + 15) >> 4;
+          const uint32_t ka = sbase + C::OFF_K + (i % C::KST) * C::TILE;
+          const uint32_t ds = tmem + Q_S + 128u * (i & 1);
+          for (int kk = 0; kk < ksteps; ++kk)
+            mma_bf16_ts(tmem + Q_DQ, ds + 8u * (kk & 3) + 64u * (kk >> 2), tile::desc_mn(ka, kk),
+                        idesc_bf16_f32(BM, DP, false, true), j > 0 || kk > 0);
+          mma_commit(&bars->kempty[i % C::KST]);
+          if (last) mma_commit(&bars->dqfull);
+        }
+        ++items;
+        w = nx;
+      }
+      mma_commit(&bars->final_);
+      mbar_wait_drain(&bars->final_, 0);
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ math: p, ds of half a row
+    regs_inc<REGS_MATH>();
+    const int hf = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 64u * hf;
+    uint32_t i = 0, item = 0;
+    bool ok = true;
+    for (WorkQ w = next_q(a, blockIdx.x); ok && w.i < a.total; w = next_q(a, w.i + gridDim.x), ++item) {
+      const int64_t n = int64_t(w.qt) * BM + row;
+      const float nl = n < a.Nq ? -lse[(int64_t(w.b) * a.H + w.h) * a.Nq + n] * LOG2E : 0.f;
+      if (!(ok = warp_wait(&bars->dready[item & 1], (item >> 1) & 1, abort_flag))) break;
+      const float nd = -d_sm[(item & 1) * BM + row];
+      const uint64_t c2 = pk(a.c, a.c), nl2 = pk(nl, nl), nd2 = pk(nd, nd);
+      for (int j = 0; j < w.nk; ++j, ++i) {
+        const int nv = keys_of(w, j) - 64 * hf;  // keys of this half
+        const uint32_t ts = t_row + Q_S + 128u * (i & 1);
+        if (!(ok = warp_wait(&bars->sfull[i & 1], (i >> 1) & 1, abort_flag))) break;
+        tc_fence_after();
+        uint32_t s[2][32];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (32 * q < nv) tmem_ld_x32(ts + 32 * q, s[q]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (32 * q >= nv) break;
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = upk(fma2(pk(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), c2, nl2));
+            s[q][e] = __float_as_uint(exp2_approx(x.x));
+            s[q][e + 1] = __float_as_uint(exp2_approx(x.y));
+          }
+          if (nv - 32 * q < 32) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (e >= nv - 32 * q) s[q][e] = 0;
+          }
+        }
+        if (!(ok = warp_wait(&bars->dpfull, i & 1, abort_flag))) break;
+        tc_fence_after();
+        uint32_t g[2][32];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (32 * q < nv) tmem_ld_x32(t_row + Q_DP + 32 * q, g[q]);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->dpfree);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (32 * q >= nv) break;
+          uint32_t d[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint64_t x = add2(pk(__uint_as_float(g[q][2 * e]), __uint_as_float(g[q][2 * e + 1])), nd2);
+            const float2 y = upk(mul2(x, pk(__uint_as_float(s[q][2 * e]), __uint_as_float(s[q][2 * e + 1]))));
+            d[e] = pack_bf16(y.x, y.y);
+          }
+          tmem_st_x16(ts + 16 * q, d);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->dsready[i & 1]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ D of the next item, dQ of the last
+    regs_dec<REGS_AUX>();
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t t_dq = tmem + Q_DQ + (static_cast<uint32_t>(quarter * 32) << 16);
+    uint32_t item = 0, done = 0;  // items whose D is computed / whose dQ is stored (those with keys)
+    bool ok = true;
+    auto finish = [&](const WorkQ& w) {
+      const int64_t n = int64_t(w.qt) * BM + row;
+      const int64_t r = (int64_t(w.b) * a.H + w.h) * a.Nq + n;
+      __nv_bfloat16* o = dQ + w.b * a.dq.b + w.h * a.dq.h + n * a.dq.n;
+      float* po = part + (int64_t(w.split) * a.rows + r) * D;
+      const bool in = n < a.Nq;
+      if (w.nk > 0) {
+        if (!warp_wait(&bars->dqfull, done & 1, abort_flag)) return false;
+        ++done;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        if (w.nk > 0) {
+          tmem_ld_x32(t_dq + 32 * c, v);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0;
+        }
+        if (c == D / 32 - 1 && w.nk > 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->dqfree);
+        }
+        if (!in) continue;
+        if (a.splits > 1) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(__uint_as_float(v[e + k]) * a.scale);
+            store32(po + 32 * c + e, u, true);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 16) {
+            uint32_t u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              u[k] = pack_bf16(__uint_as_float(v[e + 2 * k]) * a.scale, __uint_as_float(v[e + 2 * k + 1]) * a.scale);
+            store32(o + 32 * c + e, u, wide != 0);
+          }
+        }
+      }
+      return true;
+    };
+    WorkQ prev;
+    bool have = false;
+    for (int64_t x = blockIdx.x; ok && x < a.total; x += gridDim.x) {
+      const WorkQ w = get_q(a, x);
+      if (w.nk > 0) {
+        const int64_t n = int64_t(w.qt) * BM + row;
+        float sum = 0.f;
+        if (n < a.Nq) {
+          const __nv_bfloat16* po = O + w.b * a.o.b + w.h * a.o.h + n * a.o.n;
+          const __nv_bfloat16* pg = dO + w.b * a.dout.b + w.h * a.dout.h + n * a.dout.n;
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+          for (int c = 0; c < D; c += 8) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(po + c)), v = __ldg(reinterpret_cast<const uint4*>(pg + c));
+            acc[0] += bf16lo(u.x) * bf16lo(v.x) + bf16hi(u.x) * bf16hi(v.x);
+            acc[1] += bf16lo(u.y) * bf16lo(v.y) + bf16hi(u.y) * bf16hi(v.y);
+            acc[2] += bf16lo(u.z) * bf16lo(v.z) + bf16hi(u.z) * bf16hi(v.z);
+            acc[3] += bf16lo(u.w) * bf16lo(v.w) + bf16hi(u.w) * bf16hi(v.w);
+          }
+          sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+          if (w.split == 0) delta[(int64_t(w.b) * a.H + w.h) * a.Nq + n] = sum;
+        }
+        // Buffer item & 1 was last read by the item two before, whose dQ this warp has stored.
+        d_sm[(item & 1) * BM + row] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->dready[item & 1]);
+        ++item;
+      }
+      if (have) ok = finish(prev);
+      prev = w;
+      have = true;
+    }
+    if (ok && have) finish(prev);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------------------------ dK, dV
+template <int DP>
+struct CfgK {
+  static constexpr uint32_t TILE = (DP / 64) * HALF;
+  static constexpr int QST = DP == 128 ? 2 : 4;   // Q tiles, and as many dO tiles
+  static constexpr uint32_t OFF_K = 0;
+  static constexpr uint32_t OFF_V = TILE;
+  static constexpr uint32_t OFF_Q = 2 * TILE;
+  static constexpr uint32_t OFF_G = OFF_Q + QST * TILE;
+  static constexpr uint32_t OFF_L = OFF_G + QST * TILE;   // [QST][2][128]: -lse log2(e), -D
+  static constexpr uint32_t OFF_BAR = OFF_L + QST * 2 * BM * 4;
+  static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;
+};
+static_assert(CfgK<128>::SMEM <= 232448 && CfgK<64>::SMEM <= 232448, "shared memory budget");
+
+template <int DP>
+struct BarsK {
+  uint64_t qfull[CfgK<DP>::QST], qempty[CfgK<DP>::QST];
+  uint64_t gfull[CfgK<DP>::QST], gempty[CfgK<DP>::QST];
+  uint64_t lfull[CfgK<DP>::QST], lempty[CfgK<DP>::QST];
+  uint64_t kfull, kempty, vfull, vempty;
+  uint64_t sfull, pready, dpfull, dsready, accfull, accfree, final_;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(BarsK<64>) <= 512, "barrier block too large");
+
+constexpr uint32_t K_S = 0, K_DP = 128, K_DV = 256, K_DK = 384;
+
+struct WorkK {
+  int64_t i;
+  int32_t b, h, kt, split;   // h: key head
+  int32_t t0, nq, keys;      // first query tile of the group, query tiles; 0: no keys in the tile
+};
+__device__ __forceinline__ WorkK get_k(const Args& a, int64_t i) {
+  WorkK w;
+  w.i = i;
+  uint32_t r = static_cast<uint32_t>(i);
+  const uint32_t q = r / static_cast<uint32_t>(a.tiles);
+  w.kt = static_cast<int32_t>(r - q * a.tiles);
+  r = q / static_cast<uint32_t>(a.splits);
+  w.split = static_cast<int32_t>(q - r * a.splits);
+  w.b = static_cast<int32_t>(r / static_cast<uint32_t>(a.Hkv));
+  w.h = static_cast<int32_t>(r - w.b * static_cast<uint32_t>(a.Hkv));
+  w.keys = a.count ? __ldg(a.count + w.b) : static_cast<int32_t>(a.Nk);
+  w.t0 = w.split * a.per;
+  const int32_t tiles = a.q_tiles * a.group - w.t0;
+  w.nq = tiles < a.per ? tiles : a.per;
+  if (w.nq < 0 || int64_t(w.kt) * BN >= w.keys) w.nq = 0;
+  return w;
+}
+__device__ __forceinline__ WorkK next_k(const Args& a, int64_t i) {
+  WorkK w;
+  w.nq = 0;
+  for (; i < a.total; i += gridDim.x) {
+    w = get_k(a, i);
+    if (w.nq > 0) return w;
+  }
+  w.i = a.total;
+  return w;
+}
+
+template <int DP, int D>
+__global__ void __launch_bounds__(THREADS, 1)
+dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
+           const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+           const __grid_constant__ Args a, const float* __restrict__ lse, const float* __restrict__ delta,
+           float* __restrict__ part_k, float* __restrict__ part_v) {
+  using C = CfgK<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1k(smem_raw);
+  BarsK<DP>* bars = reinterpret_cast<BarsK<DP>*>(smem + C::OFF_BAR);
+  const uint32_t sbase = smem_u32(smem);
+  float* l_sm = reinterpret_cast<float*>(smem + C::OFF_L);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bars->abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::QST; ++s) {
+      mbar_init(&bars->qfull[s], 1);
+      mbar_init(&bars->qempty[s], 1);
+      mbar_init(&bars->gfull[s], 1);
+      mbar_init(&bars->gempty[s], 1);
+      mbar_init(&bars->lfull[s], 4);
+      mbar_init(&bars->lempty[s], 8);
+    }
+    mbar_init(&bars->kfull, 1);
+    mbar_init(&bars->kempty, 1);
+    mbar_init(&bars->vfull, 1);
+    mbar_init(&bars->vempty, 1);
+    mbar_init(&bars->sfull, 1);
+    mbar_init(&bars->pready, 8);
+    mbar_init(&bars->dpfull, 1);
+    mbar_init(&bars->dsready, 8);
+    mbar_init(&bars->accfull, 1);
+    mbar_init(&bars->accfree, 8);
+    mbar_init(&bars->final_, 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 13) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (warp == 12 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmG);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  pdl_trigger();
+  pdl_wait();  // the gathered keys, and D from the dQ kernel
+
+  if (warp >= 12) {
+    regs_dec<REGS_CTRL>();
+    if (warp == 12 && lane == 0) {
+      // ---------------------------------------------------------- TMA producer
+      uint32_t qi = 0, items = 0;
+      uint32_t k_out = 0, v_out = 0;
+      bool ok = true;
+      for (WorkK w = next_k(a, blockIdx.x); ok && w.i < a.total; w = next_k(a, w.i + gridDim.x), ++items) {
+        if (!(ok = mbar_wait(&bars->kempty, (items & 1) ^ 1, abort_flag, LA_SLEEP_PROD))) break;
+        load_tile<DP>(smem + C::OFF_K, &tmK, w.kt * BN, w.h, w.b, &bars->kfull);
+        ++k_out;
+        for (int j = 0; ok && j < w.nq; ++j, ++qi) {
+          const int32_t it = w.t0 + j, hq = it / a.q_tiles;
+          const int32_t h = w.h * a.group + hq, n = (it - hq * a.q_tiles) * BM;
+          const uint32_t s = qi % C::QST, ph = ((qi / C::QST) & 1) ^ 1;
+          if (!(ok = mbar_wait(&bars->qempty[s], ph, abort_flag, LA_SLEEP_PROD))) break;
+          load_tile<DP>(smem + C::OFF_Q + s * C::TILE, &tmQ, n, h, w.b, &bars->qfull[s]);
+          if (j == 0) {
+            ok = mbar_wait(&bars->vempty, (items & 1) ^ 1, abort_flag, LA_SLEEP_PROD);
+            if (ok) {
+              load_tile<DP>(smem + C::OFF_V, &tmV, w.kt * BN, w.h, w.b, &bars->vfull);
+              ++v_out;
+            }
+          }
+          if (ok) ok = mbar_wait(&bars->gempty[s], ph, abort_flag, LA_SLEEP_PROD);
+          if (!ok) {
+            mbar_wait_drain(&bars->qfull[s], (qi / C::QST) & 1);
+            break;
+          }
+          load_tile<DP>(smem + C::OFF_G + s * C::TILE, &tmG, n, h, w.b, &bars->gfull[s]);
+        }
+        if (!ok) break;
+      }
+      if (*abort_flag) {
+        // Let every copy still in flight land before the CTA's shared memory goes away.
+        drain(bars->qfull, C::QST, qi);
+        drain(bars->gfull, C::QST, qi);
+        drain(&bars->kfull, 1, k_out);
+        drain(&bars->vfull, 1, v_out);
+      }
+    } else if (warp == 13 && lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      uint32_t i = 0, items = 0;
+      bool ok = true;
+      const uint32_t id_s = idesc_bf16_f32(BM, BN, false, false), id_d = idesc_bf16_f32(BM, DP, false, true);
+      auto issue_s = [&](bool first, bool last, uint32_t step, uint32_t item) {
+        const uint32_t s = step % C::QST;
+        if (first) ok = mbar_wait(&bars->kfull, item & 1, abort_flag);
+        if (ok) ok = mbar_wait(&bars->qfull[s], (step / C::QST) & 1, abort_flag);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t ka = sbase + C::OFF_K, qa = sbase + C::OFF_Q + s * C::TILE;
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)
+          mma_bf16(tmem + K_S, tile::desc_k(ka, kk), tile::desc_k(qa, kk), id_s, kk > 0);
+        mma_commit(&bars->sfull);
+        if (last) mma_commit(&bars->kempty);
+      };
+      auto issue_dp = [&](bool first, bool last, uint32_t step, uint32_t item) {
+        const uint32_t s = step % C::QST;
+        if (first) ok = mbar_wait(&bars->vfull, item & 1, abort_flag);
+        if (ok) ok = mbar_wait(&bars->gfull[s], (step / C::QST) & 1, abort_flag);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t va = sbase + C::OFF_V, ga = sbase + C::OFF_G + s * C::TILE;
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)
+          mma_bf16(tmem + K_DP, tile::desc_k(va, kk), tile::desc_k(ga, kk), id_s, kk > 0);
+        mma_commit(&bars->dpfull);
+        if (last) mma_commit(&bars->vempty);
+      };
+      // acc += A (tensor memory, two halves of 64 rows of the product's K) B (rows of a Q or dO tile)
+      auto issue_acc = [&](uint32_t acc, uint32_t at, uint32_t b, bool fresh) {
+#pragma unroll
+        for (int kk = 0; kk < BM / 16; ++kk)
+          mma_bf16_ts(tmem + acc, tmem + at + 8u * (kk & 3) + 64u * (kk >> 2), tile::desc_mn(b, kk), id_d,
+                      !fresh || kk > 0);
+      };
+      WorkK w = next_k(a, blockIdx.x);
+      if (w.i < a.total) {
+        issue_s(true, w.nq == 1, 0, 0);
+        if (ok) issue_dp(true, w.nq == 1, 0, 0);
+      }
+      while (ok && w.i < a.total) {
+        WorkK nx = w;
+        for (int j = 0; ok && j < w.nq; ++j, ++i) {
+          const bool last = j + 1 == w.nq;
+          if (last) nx = next_k(a, w.i + gridDim.x);
+          const bool more = !last || nx.i < a.total;
+          const uint32_t it2 = items + (last ? 1 : 0);
+          const bool last2 = last ? nx.nq == 1 : j + 2 == w.nq;
+          const uint32_t s = i % C::QST;
+          ok = mbar_wait(&bars->pready, i & 1, abort_flag);
+          if (ok && j == 0) ok = mbar_wait(&bars->accfree, (items & 1) ^ 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          issue_acc(K_DV, K_S, sbase + C::OFF_G + s * C::TILE, j == 0);
+          mma_commit(&bars->gempty[s]);
+          if (more) issue_s(last, last2, i + 1, it2);
+          if (ok) ok = mbar_wait(&bars->dsready, i & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          issue_acc(K_DK, K_DP, sbase + C::OFF_Q + s * C::TILE, j == 0);
+          mma_commit(&bars->qempty[s]);
+          if (last) mma_commit(&bars->accfull);
+          if (more) issue_dp(last, last2, i + 1, it2);
+        }
+        ++items;
+        w = nx;
+      }
+      mma_commit(&bars->final_);
+      mbar_wait_drain(&bars->final_, 0);
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ math: p, ds of half a key's row
+    regs_inc<REGS_MATH>();
+    const int hf = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t ts = t_row + K_S + 64u * hf, tp = t_row + K_DP + 64u * hf;
+    const uint64_t c2 = pk(a.c, a.c);
+    uint32_t i = 0, item = 0;
+    bool ok = true;
+    for (WorkK w = next_k(a, blockIdx.x); ok && w.i < a.total; w = next_k(a, w.i + gridDim.x), ++item) {
+      for (int j = 0; j < w.nq; ++j, ++i) {
+        const uint32_t s_l = i % C::QST;
+        const uint32_t la_ = sbase + C::OFF_L + (s_l * 2 * BM + 64 * hf) * 4, ld_ = la_ + BM * 4;
+        if (!(ok = warp_wait(&bars->lfull[s_l], (i / C::QST) & 1, abort_flag))) break;
+        if (!(ok = warp_wait(&bars->sfull, i & 1, abort_flag))) break;
+        tc_fence_after();
+        uint32_t s[2][32];
+        tmem_ld_x32(ts, s[0]);
+        tmem_ld_x32(ts + 32, s[1]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 nl = lds128f(la_ + (32 * q + e) * 4);
+            const float2 x = upk(fma2(pk(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), c2, pk(nl.x, nl.y)));
+            const float2 y = upk(fma2(pk(__uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3])), c2, pk(nl.z, nl.w)));
+            const float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y), p2 = exp2_approx(y.x), p3 = exp2_approx(y.y);
+            s[q][e] = __float_as_uint(p0);
+            s[q][e + 1] = __float_as_uint(p1);
+            s[q][e + 2] = __float_as_uint(p2);
+            s[q][e + 3] = __float_as_uint(p3);
+            p[e / 2] = pack_bf16(p0, p1);
+            p[e / 2 + 1] = pack_bf16(p2, p3);
+          }
+          tmem_st_x16(ts + 16 * q, p);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->pready);
+        if (!(ok = warp_wait(&bars->dpfull, i & 1, abort_flag))) break;
+        tc_fence_after();
+        uint32_t g[2][32];
+        tmem_ld_x32(tp, g[0]);
+        tmem_ld_x32(tp + 32, g[1]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t d[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 nd = lds128f(ld_ + (32 * q + e) * 4);
+            const float2 x = upk(mul2(add2(pk(__uint_as_float(g[q][e]), __uint_as_float(g[q][e + 1])), pk(nd.x, nd.y)),
+                                      pk(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]))));
+            const float2 y = upk(mul2(add2(pk(__uint_as_float(g[q][e + 2]), __uint_as_float(g[q][e + 3])), pk(nd.z, nd.w)),
+                                      pk(__uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3]))));
+            d[e / 2] = pack_bf16(x.x, x.y);
+            d[e / 2 + 1] = pack_bf16(y.x, y.y);
+          }
+          tmem_st_x16(tp + 16 * q, d);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars->dsready);
+          mbar_arrive(&bars->lempty[s_l]);
+        }
+      }
+      if (!ok) break;
+      // the item's sums: warps 0-3 store dV, warps 4-7 dK, a key per thread
+      if (!(ok = warp_wait(&bars->accfull, item & 1, abort_flag))) break;
+      tc_fence_after();
+      const int64_t n = int64_t(w.kt) * BN + row;
+      const float f = hf == 0 ? 1.f : a.scale;
+      float* out = (hf == 0 ? part_v : part_k) + (int64_t(w.split) * a.keys + (int64_t(w.b) * a.Hkv + w.h) * a.Nk + n) * D;
+      const uint32_t ta = t_row + (hf == 0 ? K_DV : K_DK);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld_x32(ta + 32 * c, v);
+        tmem_ld_wait();
+        if (n < w.keys) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(__uint_as_float(v[e + k]) * f);
+            store32(out + 32 * c + e, u, true);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->accfree);
+    }
+  } else {
+    // ------------------------------------------------------------ -lse log2(e) and -D of the queries
+    regs_dec<REGS_AUX>();
+    const int q = (warp & 3) * 32 + lane;
+    uint32_t i = 0;
+    bool ok = true;
+    for (WorkK w = next_k(a, blockIdx.x); ok && w.i < a.total; w = next_k(a, w.i + gridDim.x)) {
+      for (int j = 0; j < w.nq; ++j, ++i) {
+        const uint32_t s = i % C::QST;
+        const int32_t it = w.t0 + j, hq = it / a.q_tiles;
+        const int64_t n = int64_t(it - hq * a.q_tiles) * BM + q;
+        const int64_t r = (int64_t(w.b) * a.H + w.h * a.group + hq) * a.Nq + n;
+        // queries past the end: p = 2^-inf = 0
+        const float nl = n < a.Nq ? -lse[r] * LOG2E : xs::NEG_INF, nd = n < a.Nq ? -delta[r] : 0.f;
+        if (!(ok = warp_wait(&bars->lempty[s], ((i / C::QST) & 1) ^ 1, abort_flag, LA_SLEEP_PROD))) break;
+        l_sm[s * 2 * BM + q] = nl;
+        l_sm[s * 2 * BM + BM + q] = nd;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->lfull[s]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) tmem_dealloc(tmem, 512);
+}
+
+// dK and dV from the parts' sums, in order: key j of (b, h) is row place[b][j] of the parts (j itself
+// when nothing was gathered; 0 where it is not attended).  A thread has 2 channels; blockIdx.y
+// selects dK or dV.
+template <int D>
+__global__ void __launch_bounds__(256)
+sum_kernel(int64_t keys, int64_t Hkv, int64_t Nk, int splits, const float* __restrict__ part_k,
+           const float* __restrict__ part_v, const int32_t* __restrict__ place, __nv_bfloat16* __restrict__ dK,
+           __nv_bfloat16* __restrict__ dV, xs::Str sk, xs::Str sv) {
+  pdl_wait();
+  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t key = e / (D / 2);
+  const int c = static_cast<int>(e % (D / 2)) * 2;
+  if (key >= keys) return;
+  const int64_t n = key % Nk, bh = key / Nk, b = bh / Hkv;
+  const float* part = blockIdx.y == 0 ? part_k : part_v;
+  const xs::Str st = blockIdx.y == 0 ? sk : sv;
+  __nv_bfloat16* out = (blockIdx.y == 0 ? dK : dV) + b * st.b + (bh % Hkv) * st.h + n * st.n + c;
+  const int64_t at = place ? int64_t(place[b * Nk + n]) : n;
+  float2 v = make_float2(0.f, 0.f);
+  if (at >= 0) {
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float2 u = *reinterpret_cast<const float2*>(part + (int64_t(s) * keys + bh * Nk + at) * D + c);
+      v.x += u.x;
+      v.y += u.y;
+    }
+  }
+  *reinterpret_cast<uint32_t*>(out) = pack_bf16(v.x, v.y);
+}
+
+}  // namespace xb
+}  // namespace la
