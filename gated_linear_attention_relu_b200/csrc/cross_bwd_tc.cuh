@@ -123,11 +123,6 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* m, in
   if (DP == 128) tma_load_4d(dst + HALF, m, 64, n, h, b, bar);
 }
 
-// Instruction descriptor of a product with N columns (a multiple of 16).
-__device__ __forceinline__ uint32_t idesc_n(uint32_t n) {
-  return idesc_bf16_f32(BM, 16, false, false) - (2u << 17) + ((n >> 3) << 17);
-}
-
 // Drains the copies of a ring that were issued and may still be in flight.
 __device__ __forceinline__ void drain(uint64_t* full, uint32_t stages, uint32_t issued) {
   for (uint32_t j = issued > stages ? issued - stages : 0; j < issued; ++j)
@@ -147,7 +142,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
   BarsQ<DP>* bars = reinterpret_cast<BarsQ<DP>*>(smem + C::OFF_BAR);
   const uint32_t sbase = smem_u32(smem);
   float* d_sm = reinterpret_cast<float*>(smem + C::OFF_D);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_number(), lane = threadIdx.x & 31;
   volatile int* abort_flag = &bars->abort_flag;
 
   if (threadIdx.x == 0) {
@@ -180,7 +175,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bars->tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
   pdl_trigger();
   pdl_wait();  // the gathered keys and their counts
 
@@ -192,7 +187,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
       bool ok = true;
       auto load_q = [&](const CUtensorMap* m, const WorkQ& w) {
         const uint32_t s = qi % C::QST;
-        if (!mbar_wait(&bars->qempty[s], ((qi / C::QST) & 1) ^ 1, abort_flag, LA_SLEEP_PROD)) return false;
+        if (!mbar_wait_near(&bars->qempty[s], ((qi / C::QST) & 1) ^ 1, abort_flag)) return false;
         load_tile<DP>(smem + C::OFF_Q + s * C::TILE, m, w.qt * BM, w.h, w.b, &bars->qfull[s]);
         ++qi;
         return true;
@@ -203,10 +198,10 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
           const int32_t n = (w.k0 + j) * BN;
           if (j == 0 && !(ok = load_q(&tmQ, w))) break;
           const uint32_t sk = ki % C::KST, sv = ki % C::VST;
-          if (!(ok = mbar_wait(&bars->kempty[sk], ((ki / C::KST) & 1) ^ 1, abort_flag, LA_SLEEP_PROD))) break;
+          if (!(ok = mbar_wait_near(&bars->kempty[sk], ((ki / C::KST) & 1) ^ 1, abort_flag))) break;
           load_tile<DP>(smem + C::OFF_K + sk * C::TILE, &tmK, n, kh, w.b, &bars->kfull[sk]);
           if (j == 0) ok = load_q(&tmG, w);
-          if (ok) ok = mbar_wait(&bars->vempty[sv], ((ki / C::VST) & 1) ^ 1, abort_flag, LA_SLEEP_PROD);
+          if (ok) ok = mbar_wait_near(&bars->vempty[sv], ((ki / C::VST) & 1) ^ 1, abort_flag);
           if (!ok) {
             mbar_wait_drain(&bars->kfull[sk], (ki / C::KST) & 1);
             break;
@@ -220,40 +215,48 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         drain(bars->kfull, C::KST, ki);
         drain(bars->vfull, C::VST, ki);
       }
-    } else if (warp == 13 && lane == 0) {
-      // ---------------------------------------------------------- MMA issuer
+    } else if (warp == 13) {
+      // ---------------------------------------------------------- MMA issuer (the warp stays converged)
       uint32_t i = 0, items = 0;  // steps (key tiles) and items done
       bool ok = true;
       auto issue_s = [&](const WorkQ& w, int j, uint32_t step, uint32_t item) {
         const uint32_t qs = (2 * item) % C::QST, ks = step % C::KST;
-        ok = mbar_wait(&bars->kfull[ks], (step / C::KST) & 1, abort_flag);
-        if (ok && j == 0) ok = mbar_wait(&bars->qfull[qs], ((2 * item) / C::QST) & 1, abort_flag);
+        ok = warp_wait_near(&bars->kfull[ks], (step / C::KST) & 1, abort_flag);
+        if (j == 0) ok = ok && warp_wait_near(&bars->qfull[qs], ((2 * item) / C::QST) & 1, abort_flag);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t id = idesc_n(static_cast<uint32_t>((keys_of(w, j) + 15) & ~15));
-        const uint32_t qa = sbase + C::OFF_Q + qs * C::TILE, ka = sbase + C::OFF_K + ks * C::TILE;
+        const uint32_t id = xt::idesc_n(BM, static_cast<uint32_t>((keys_of(w, j) + 15) & ~15));
+        const uint64_t qd = tile::desc_k(sbase + C::OFF_Q + qs * C::TILE, 0);
+        const uint64_t kd = tile::desc_k(sbase + C::OFF_K + ks * C::TILE, 0);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)
-          mma_bf16(tmem + Q_S + 128u * (step & 1), tile::desc_k(qa, kk), tile::desc_k(ka, kk), id, kk > 0);
-        mma_commit(&bars->sfull[step & 1]);
-        if (j == w.nk - 1) mma_commit(&bars->qempty[qs]);
+          for (int kk = 0; kk < DP / 16; ++kk)
+            mma_bf16(tmem + Q_S + 128u * (step & 1), qd + tile::step_k(kk), kd + tile::step_k(kk), id, kk > 0);
+          mma_commit(&bars->sfull[step & 1]);
+          if (j == w.nk - 1) mma_commit(&bars->qempty[qs]);
+        }
+        __syncwarp();
       };
       auto issue_dp = [&](const WorkQ& w, int j, uint32_t step, uint32_t item) {
         const uint32_t gs = (2 * item + 1) % C::QST, vs = step % C::VST;
-        ok = mbar_wait(&bars->vfull[vs], (step / C::VST) & 1, abort_flag);
-        if (ok && j == 0) ok = mbar_wait(&bars->qfull[gs], ((2 * item + 1) / C::QST) & 1, abort_flag);
+        ok = warp_wait_near(&bars->vfull[vs], (step / C::VST) & 1, abort_flag);
+        if (j == 0) ok = ok && warp_wait_near(&bars->qfull[gs], ((2 * item + 1) / C::QST) & 1, abort_flag);
         // the math warps have read the last dP
-        if (ok) ok = mbar_wait(&bars->dpfree, (step & 1) ^ 1, abort_flag);
+        ok = ok && warp_wait_near(&bars->dpfree, (step & 1) ^ 1, abort_flag);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t id = idesc_n(static_cast<uint32_t>((keys_of(w, j) + 15) & ~15));
-        const uint32_t ga = sbase + C::OFF_Q + gs * C::TILE, va = sbase + C::OFF_V + vs * C::TILE;
+        const uint32_t id = xt::idesc_n(BM, static_cast<uint32_t>((keys_of(w, j) + 15) & ~15));
+        const uint64_t gd = tile::desc_k(sbase + C::OFF_Q + gs * C::TILE, 0);
+        const uint64_t vd = tile::desc_k(sbase + C::OFF_V + vs * C::TILE, 0);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)
-          mma_bf16(tmem + Q_DP, tile::desc_k(ga, kk), tile::desc_k(va, kk), id, kk > 0);
-        mma_commit(&bars->dpfull);
-        mma_commit(&bars->vempty[vs]);
-        if (j == w.nk - 1) mma_commit(&bars->qempty[gs]);
+          for (int kk = 0; kk < DP / 16; ++kk)
+            mma_bf16(tmem + Q_DP, gd + tile::step_k(kk), vd + tile::step_k(kk), id, kk > 0);
+          mma_commit(&bars->dpfull);
+          mma_commit(&bars->vempty[vs]);
+          if (j == w.nk - 1) mma_commit(&bars->qempty[gs]);
+        }
+        __syncwarp();
       };
       WorkQ w = next_q(a, blockIdx.x);
       if (w.i < a.total) {
@@ -271,24 +274,32 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             if (!ok) break;
           }
           // dQ += ds K
-          ok = mbar_wait(&bars->dsready[i & 1], (i >> 1) & 1, abort_flag);
-          if (ok && j == 0) ok = mbar_wait(&bars->dqfree, (items & 1) ^ 1, abort_flag);
+          ok = warp_wait_near(&bars->dsready[i & 1], (i >> 1) & 1, abort_flag);
+          if (j == 0) ok = ok && warp_wait_near(&bars->dqfree, (items & 1) ^ 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
           const int ksteps = (keys_of(w, j) + 15) >> 4;
-          const uint32_t ka = sbase + C::OFF_K + (i % C::KST) * C::TILE;
+          const uint32_t ks = i % C::KST;
+          const uint64_t kd = tile::desc_mn(sbase + C::OFF_K + ks * C::TILE, 0);
           const uint32_t ds = tmem + Q_S + 128u * (i & 1);
-          for (int kk = 0; kk < ksteps; ++kk)
-            mma_bf16_ts(tmem + Q_DQ, ds + 8u * (kk & 3) + 64u * (kk >> 2), tile::desc_mn(ka, kk),
-                        idesc_bf16_f32(BM, DP, false, true), j > 0 || kk > 0);
-          mma_commit(&bars->kempty[i % C::KST]);
-          if (last) mma_commit(&bars->dqfull);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+              if (kk < ksteps)
+                mma_bf16_ts(tmem + Q_DQ, ds + 8u * (kk & 3) + 64u * (kk >> 2), kd + tile::step_mn(kk),
+                            idesc_bf16_f32(BM, DP, false, true), j > 0 || kk > 0);
+            mma_commit(&bars->kempty[ks]);
+            if (last) mma_commit(&bars->dqfull);
+          }
+          __syncwarp();
         }
         ++items;
         w = nx;
       }
-      mma_commit(&bars->final_);
+      if (elect_one()) mma_commit(&bars->final_);
+      __syncwarp();
       mbar_wait_drain(&bars->final_, 0);
+      __syncwarp();
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ math: p, ds of half a row
@@ -301,13 +312,13 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     for (WorkQ w = next_q(a, blockIdx.x); ok && w.i < a.total; w = next_q(a, w.i + gridDim.x), ++item) {
       const int64_t n = int64_t(w.qt) * BM + row;
       const float nl = n < a.Nq ? -lse[(int64_t(w.b) * a.H + w.h) * a.Nq + n] * LOG2E : 0.f;
-      if (!(ok = warp_wait(&bars->dready[item & 1], (item >> 1) & 1, abort_flag))) break;
+      if (!(ok = warp_wait_near(&bars->dready[item & 1], (item >> 1) & 1, abort_flag))) break;
       const float nd = -d_sm[(item & 1) * BM + row];
       const uint64_t c2 = pk(a.c, a.c), nl2 = pk(nl, nl), nd2 = pk(nd, nd);
       for (int j = 0; j < w.nk; ++j, ++i) {
         const int nv = keys_of(w, j) - 64 * hf;  // keys of this half
         const uint32_t ts = t_row + Q_S + 128u * (i & 1);
-        if (!(ok = warp_wait(&bars->sfull[i & 1], (i >> 1) & 1, abort_flag))) break;
+        if (!(ok = warp_wait_near(&bars->sfull[i & 1], (i >> 1) & 1, abort_flag))) break;
         tc_fence_after();
         uint32_t s[2][32];
 #pragma unroll
@@ -329,7 +340,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
               if (e >= nv - 32 * q) s[q][e] = 0;
           }
         }
-        if (!(ok = warp_wait(&bars->dpfull, i & 1, abort_flag))) break;
+        if (!(ok = warp_wait_near(&bars->dpfull, i & 1, abort_flag))) break;
         tc_fence_after();
         uint32_t g[2][32];
 #pragma unroll
@@ -372,7 +383,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
       float* po = part + (int64_t(w.split) * a.rows + r) * D;
       const bool in = n < a.Nq;
       if (w.nk > 0) {
-        if (!warp_wait(&bars->dqfull, done & 1, abort_flag)) return false;
+        if (!warp_wait_near(&bars->dqfull, done & 1, abort_flag)) return false;
         ++done;
         tc_fence_after();
       }
@@ -526,7 +537,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
   BarsK<DP>* bars = reinterpret_cast<BarsK<DP>*>(smem + C::OFF_BAR);
   const uint32_t sbase = smem_u32(smem);
   float* l_sm = reinterpret_cast<float*>(smem + C::OFF_L);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_number(), lane = threadIdx.x & 31;
   volatile int* abort_flag = &bars->abort_flag;
 
   if (threadIdx.x == 0) {
@@ -565,7 +576,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bars->tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
   pdl_trigger();
   pdl_wait();  // the gathered keys, and D from the dQ kernel
 
@@ -577,23 +588,23 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       uint32_t k_out = 0, v_out = 0;
       bool ok = true;
       for (WorkK w = next_k(a, blockIdx.x); ok && w.i < a.total; w = next_k(a, w.i + gridDim.x), ++items) {
-        if (!(ok = mbar_wait(&bars->kempty, (items & 1) ^ 1, abort_flag, LA_SLEEP_PROD))) break;
+        if (!(ok = mbar_wait_near(&bars->kempty, (items & 1) ^ 1, abort_flag))) break;
         load_tile<DP>(smem + C::OFF_K, &tmK, w.kt * BN, w.h, w.b, &bars->kfull);
         ++k_out;
         for (int j = 0; ok && j < w.nq; ++j, ++qi) {
           const int32_t it = w.t0 + j, hq = it / a.q_tiles;
           const int32_t h = w.h * a.group + hq, n = (it - hq * a.q_tiles) * BM;
           const uint32_t s = qi % C::QST, ph = ((qi / C::QST) & 1) ^ 1;
-          if (!(ok = mbar_wait(&bars->qempty[s], ph, abort_flag, LA_SLEEP_PROD))) break;
+          if (!(ok = mbar_wait_near(&bars->qempty[s], ph, abort_flag))) break;
           load_tile<DP>(smem + C::OFF_Q + s * C::TILE, &tmQ, n, h, w.b, &bars->qfull[s]);
           if (j == 0) {
-            ok = mbar_wait(&bars->vempty, (items & 1) ^ 1, abort_flag, LA_SLEEP_PROD);
+            ok = mbar_wait_near(&bars->vempty, (items & 1) ^ 1, abort_flag);
             if (ok) {
               load_tile<DP>(smem + C::OFF_V, &tmV, w.kt * BN, w.h, w.b, &bars->vfull);
               ++v_out;
             }
           }
-          if (ok) ok = mbar_wait(&bars->gempty[s], ph, abort_flag, LA_SLEEP_PROD);
+          if (ok) ok = mbar_wait_near(&bars->gempty[s], ph, abort_flag);
           if (!ok) {
             mbar_wait_drain(&bars->qfull[s], (qi / C::QST) & 1);
             break;
@@ -609,43 +620,56 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         drain(&bars->kfull, 1, k_out);
         drain(&bars->vfull, 1, v_out);
       }
-    } else if (warp == 13 && lane == 0) {
-      // ---------------------------------------------------------- MMA issuer
+    } else if (warp == 13) {
+      // ---------------------------------------------------------- MMA issuer (the warp stays converged)
       uint32_t i = 0, items = 0;
       bool ok = true;
       const uint32_t id_s = idesc_bf16_f32(BM, BN, false, false), id_d = idesc_bf16_f32(BM, DP, false, true);
       auto issue_s = [&](bool first, bool last, uint32_t step, uint32_t item) {
         const uint32_t s = step % C::QST;
-        if (first) ok = mbar_wait(&bars->kfull, item & 1, abort_flag);
-        if (ok) ok = mbar_wait(&bars->qfull[s], (step / C::QST) & 1, abort_flag);
+        if (first) ok = warp_wait_near(&bars->kfull, item & 1, abort_flag);
+        ok = ok && warp_wait_near(&bars->qfull[s], (step / C::QST) & 1, abort_flag);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t ka = sbase + C::OFF_K, qa = sbase + C::OFF_Q + s * C::TILE;
+        const uint64_t kd = tile::desc_k(sbase + C::OFF_K, 0), qd = tile::desc_k(sbase + C::OFF_Q + s * C::TILE, 0);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)
-          mma_bf16(tmem + K_S, tile::desc_k(ka, kk), tile::desc_k(qa, kk), id_s, kk > 0);
-        mma_commit(&bars->sfull);
-        if (last) mma_commit(&bars->kempty);
+          for (int kk = 0; kk < DP / 16; ++kk)
+            mma_bf16(tmem + K_S, kd + tile::step_k(kk), qd + tile::step_k(kk), id_s, kk > 0);
+          mma_commit(&bars->sfull);
+          if (last) mma_commit(&bars->kempty);
+        }
+        __syncwarp();
       };
       auto issue_dp = [&](bool first, bool last, uint32_t step, uint32_t item) {
         const uint32_t s = step % C::QST;
-        if (first) ok = mbar_wait(&bars->vfull, item & 1, abort_flag);
-        if (ok) ok = mbar_wait(&bars->gfull[s], (step / C::QST) & 1, abort_flag);
+        if (first) ok = warp_wait_near(&bars->vfull, item & 1, abort_flag);
+        ok = ok && warp_wait_near(&bars->gfull[s], (step / C::QST) & 1, abort_flag);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t va = sbase + C::OFF_V, ga = sbase + C::OFF_G + s * C::TILE;
+        const uint64_t vd = tile::desc_k(sbase + C::OFF_V, 0), gd = tile::desc_k(sbase + C::OFF_G + s * C::TILE, 0);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)
-          mma_bf16(tmem + K_DP, tile::desc_k(va, kk), tile::desc_k(ga, kk), id_s, kk > 0);
-        mma_commit(&bars->dpfull);
-        if (last) mma_commit(&bars->vempty);
+          for (int kk = 0; kk < DP / 16; ++kk)
+            mma_bf16(tmem + K_DP, vd + tile::step_k(kk), gd + tile::step_k(kk), id_s, kk > 0);
+          mma_commit(&bars->dpfull);
+          if (last) mma_commit(&bars->vempty);
+        }
+        __syncwarp();
       };
-      // acc += A (tensor memory, two halves of 64 rows of the product's K) B (rows of a Q or dO tile)
-      auto issue_acc = [&](uint32_t acc, uint32_t at, uint32_t b, bool fresh) {
+      // acc += A (tensor memory, two halves of 64 rows of the product's K) B (rows of a Q or dO
+      // tile), then the tile is free (and, after an item's last product, its sums are complete).
+      auto issue_acc = [&](uint32_t acc, uint32_t at, uint32_t b, bool fresh, uint64_t* tile_free, uint64_t* full) {
+        const uint64_t bd = tile::desc_mn(b, 0);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < BM / 16; ++kk)
-          mma_bf16_ts(tmem + acc, tmem + at + 8u * (kk & 3) + 64u * (kk >> 2), tile::desc_mn(b, kk), id_d,
-                      !fresh || kk > 0);
+          for (int kk = 0; kk < BM / 16; ++kk)
+            mma_bf16_ts(tmem + acc, tmem + at + 8u * (kk & 3) + 64u * (kk >> 2), bd + tile::step_mn(kk), id_d,
+                        !fresh || kk > 0);
+          mma_commit(tile_free);
+          if (full) mma_commit(full);
+        }
+        __syncwarp();
       };
       WorkK w = next_k(a, blockIdx.x);
       if (w.i < a.total) {
@@ -661,26 +685,25 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
           const uint32_t it2 = items + (last ? 1 : 0);
           const bool last2 = last ? nx.nq == 1 : j + 2 == w.nq;
           const uint32_t s = i % C::QST;
-          ok = mbar_wait(&bars->pready, i & 1, abort_flag);
-          if (ok && j == 0) ok = mbar_wait(&bars->accfree, (items & 1) ^ 1, abort_flag);
+          ok = warp_wait_near(&bars->pready, i & 1, abort_flag);
+          if (j == 0) ok = ok && warp_wait_near(&bars->accfree, (items & 1) ^ 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          issue_acc(K_DV, K_S, sbase + C::OFF_G + s * C::TILE, j == 0);
-          mma_commit(&bars->gempty[s]);
+          issue_acc(K_DV, K_S, sbase + C::OFF_G + s * C::TILE, j == 0, &bars->gempty[s], nullptr);
           if (more) issue_s(last, last2, i + 1, it2);
-          if (ok) ok = mbar_wait(&bars->dsready, i & 1, abort_flag);
+          ok = ok && warp_wait_near(&bars->dsready, i & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          issue_acc(K_DK, K_DP, sbase + C::OFF_Q + s * C::TILE, j == 0);
-          mma_commit(&bars->qempty[s]);
-          if (last) mma_commit(&bars->accfull);
+          issue_acc(K_DK, K_DP, sbase + C::OFF_Q + s * C::TILE, j == 0, &bars->qempty[s], last ? &bars->accfull : nullptr);
           if (more) issue_dp(last, last2, i + 1, it2);
         }
         ++items;
         w = nx;
       }
-      mma_commit(&bars->final_);
+      if (elect_one()) mma_commit(&bars->final_);
+      __syncwarp();
       mbar_wait_drain(&bars->final_, 0);
+      __syncwarp();
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ math: p, ds of half a key's row
@@ -696,8 +719,8 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       for (int j = 0; j < w.nq; ++j, ++i) {
         const uint32_t s_l = i % C::QST;
         const uint32_t la_ = sbase + C::OFF_L + (s_l * 2 * BM + 64 * hf) * 4, ld_ = la_ + BM * 4;
-        if (!(ok = warp_wait(&bars->lfull[s_l], (i / C::QST) & 1, abort_flag))) break;
-        if (!(ok = warp_wait(&bars->sfull, i & 1, abort_flag))) break;
+        if (!(ok = warp_wait_near(&bars->lfull[s_l], (i / C::QST) & 1, abort_flag))) break;
+        if (!(ok = warp_wait_near(&bars->sfull, i & 1, abort_flag))) break;
         tc_fence_after();
         uint32_t s[2][32];
         tmem_ld_x32(ts, s[0]);
@@ -725,7 +748,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->pready);
-        if (!(ok = warp_wait(&bars->dpfull, i & 1, abort_flag))) break;
+        if (!(ok = warp_wait_near(&bars->dpfull, i & 1, abort_flag))) break;
         tc_fence_after();
         uint32_t g[2][32];
         tmem_ld_x32(tp, g[0]);
@@ -756,7 +779,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       }
       if (!ok) break;
       // the item's sums: warps 0-3 store dV, warps 4-7 dK, a key per thread
-      if (!(ok = warp_wait(&bars->accfull, item & 1, abort_flag))) break;
+      if (!(ok = warp_wait_near(&bars->accfull, item & 1, abort_flag))) break;
       tc_fence_after();
       const int64_t n = int64_t(w.kt) * BN + row;
       const float f = hf == 0 ? 1.f : a.scale;
@@ -795,7 +818,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         const int64_t r = (int64_t(w.b) * a.H + w.h * a.group + hq) * a.Nq + n;
         // queries past the end: p = 2^-inf = 0
         const float nl = n < a.Nq ? -lse[r] * LOG2E : xs::NEG_INF, nd = n < a.Nq ? -delta[r] : 0.f;
-        if (!(ok = warp_wait(&bars->lempty[s], ((i / C::QST) & 1) ^ 1, abort_flag, LA_SLEEP_PROD))) break;
+        if (!(ok = warp_wait_near(&bars->lempty[s], ((i / C::QST) & 1) ^ 1, abort_flag))) break;
         l_sm[s * 2 * BM + q] = nl;
         l_sm[s * 2 * BM + BM + q] = nd;
         __syncwarp();

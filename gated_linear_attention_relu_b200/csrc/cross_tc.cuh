@@ -75,6 +75,12 @@ struct Args {
   xs::Str o;
 };
 
+// Instruction descriptor of a product with M rows and n columns (a multiple of 16), both operands
+// K-major.
+__device__ __forceinline__ uint32_t idesc_n(uint32_t M, uint32_t n) {
+  return idesc_bf16_f32(M, 0, false, false) | ((n >> 3) << 17);
+}
+
 struct Work {
   int64_t i;
   int32_t b, h, pair, split;
@@ -152,7 +158,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   Bars<DP>* bars = reinterpret_cast<Bars<DP>*>(smem + C::OFF_BAR);
   const uint32_t sbase = smem_u32(smem);
   float* inv_l = reinterpret_cast<float*>(smem + C::OFF_L);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_number(), lane = threadIdx.x & 31;
   volatile int* abort_flag = &bars->abort_flag;
 
   if (threadIdx.x == 0) {
@@ -188,7 +194,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bars->tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
   pdl_trigger();
   pdl_wait();  // the gathered keys and their counts
 
@@ -200,7 +206,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       bool ok = true;
       auto load_kv = [&](const CUtensorMap* m, const Work& w, int j) {
         const uint32_t s = ki % C::KVST;
-        if (!mbar_wait(&bars->kvempty[s], ((ki / C::KVST) & 1) ^ 1, abort_flag, LA_SLEEP_PROD)) return false;
+        if (!mbar_wait_near(&bars->kvempty[s], ((ki / C::KVST) & 1) ^ 1, abort_flag)) return false;
         uint8_t* dst = smem + C::OFF_KV + s * C::TILE;
         mbar_arrive_expect_tx(&bars->kvfull[s], C::TILE);
         const int32_t n = (w.k0 + j) * BN, h = w.h / a.group;
@@ -212,7 +218,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       for (Work w = next_work(a, blockIdx.x); ok && w.i < a.total; w = next_work(a, w.i + gridDim.x)) {
         for (int t = 0; ok && t < w.nt; ++t) {
           const uint32_t s = qi % QST;
-          if (!(ok = mbar_wait(&bars->qempty[s], ((qi / QST) & 1) ^ 1, abort_flag, LA_SLEEP_PROD))) break;
+          if (!(ok = mbar_wait_near(&bars->qempty[s], ((qi / QST) & 1) ^ 1, abort_flag))) break;
           uint8_t* dst = smem + C::OFF_Q + s * C::TILE;
           mbar_arrive_expect_tx(&bars->qfull[s], C::TILE);
           const int32_t n = (w.pair * 2 + t) * BM;
@@ -232,31 +238,37 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         for (uint32_t j = (ki > C::KVST ? ki - C::KVST : 0); j < ki; ++j)
           mbar_wait_drain(&bars->kvfull[j % C::KVST], (j / C::KVST) & 1);
       }
-    } else if (warp == 13 && lane == 0) {
-      // ---------------------------------------------------------- MMA issuer
+    } else if (warp == 13) {
+      // ---------------------------------------------------------- MMA issuer (the warp stays converged)
       uint32_t qi = 0, ki = 0;                 // query tiles and key/value tiles consumed so far
       uint32_t steps[2] = {0, 0}, items[2] = {0, 0};
       bool ok = true;
-      // S_t of (w, j): its Q tile is number q of the ring, its K tile number k.
-      auto issue_s = [&](int t, const Work& w, int j, uint32_t q, uint32_t k) {
+      // S_t of (w, j): its Q tile is number q of the ring, its K tile number k; `free_k`: no other
+      // product of this K tile follows.
+      auto issue_s = [&](int t, const Work& w, int j, uint32_t q, uint32_t k, bool free_k) {
         const uint32_t n16 = static_cast<uint32_t>((tile_keys(w, j) + 15) & ~15);
-        const uint32_t id = idesc_bf16_f32(BM, 16, false, false) - (2u << 17) + ((n16 >> 3) << 17);
-        const uint32_t qa = sbase + C::OFF_Q + (q % QST) * C::TILE, ka = sbase + C::OFF_KV + (k % C::KVST) * C::TILE;
+        const uint32_t id = idesc_n(BM, n16);
+        const uint32_t qs = q % QST, ks = k % C::KVST;
+        const uint64_t qd = tile::desc_k(sbase + C::OFF_Q + qs * C::TILE, 0);
+        const uint64_t kd = tile::desc_k(sbase + C::OFF_KV + ks * C::TILE, 0);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)
-          mma_bf16(tmem + S_COL + 128u * t, tile::desc_k(qa, kk), tile::desc_k(ka, kk), id, kk > 0);
-        mma_commit(&bars->sfull[t]);
-        if (j == w.nk - 1) mma_commit(&bars->qempty[q % QST]);
+          for (int kk = 0; kk < DP / 16; ++kk)
+            mma_bf16(tmem + S_COL + 128u * t, qd + tile::step_k(kk), kd + tile::step_k(kk), id, kk > 0);
+          mma_commit(&bars->sfull[t]);
+          if (j == w.nk - 1) mma_commit(&bars->qempty[qs]);
+          if (free_k) mma_commit(&bars->kvempty[ks]);
+        }
+        __syncwarp();
       };
       Work w = next_work(a, blockIdx.x);
       if (w.i < a.total) {
-        ok = mbar_wait(&bars->kvfull[0], 0, abort_flag);
+        ok = warp_wait_near(&bars->kvfull[0], 0, abort_flag);
         for (int t = 0; ok && t < w.nt; ++t) {
-          ok = mbar_wait(&bars->qfull[t], 0, abort_flag);
+          ok = warp_wait_near(&bars->qfull[t], 0, abort_flag);
           tc_fence_after();
-          if (ok) issue_s(t, w, 0, t, 0);
+          if (ok) issue_s(t, w, 0, t, 0, t == w.nt - 1);
         }
-        if (ok) mma_commit(&bars->kvempty[0]);
         qi = w.nt;
         ki = 1;
       }
@@ -271,42 +283,49 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           if (more) ++ki;
           const int nt2 = more ? nx.nt : 0;
           const uint32_t q0 = last ? qi : qi - static_cast<uint32_t>(w.nt);
-          const int nv = tile_keys(w, j);
-          const int ksteps = (nv + 15) >> 4;
-          for (int t = 0; ok && t < (w.nt > nt2 ? w.nt : nt2); ++t) {
+          const int ksteps = (tile_keys(w, j) + 15) >> 4;
+          const uint32_t vs = v % C::KVST;
+          const uint64_t vd = tile::desc_mn(sbase + C::OFF_KV + vs * C::TILE, 0);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
             if (t < w.nt) {
               // O_t += P_t V (first of an item: the epilogue has read the last item's O_t)
-              if (t == 0) ok = mbar_wait(&bars->kvfull[v % C::KVST], (v / C::KVST) & 1, abort_flag);
-              if (ok && j == 0) ok = mbar_wait(&bars->ofree[t], (items[t] & 1) ^ 1, abort_flag);
-              ok = ok && mbar_wait(&bars->pready[t], steps[t] & 1, abort_flag);
+              if (t == 0) ok = ok && warp_wait_near(&bars->kvfull[vs], (v / C::KVST) & 1, abort_flag);
+              if (j == 0) ok = ok && warp_wait_near(&bars->ofree[t], (items[t] & 1) ^ 1, abort_flag);
+              ok = ok && warp_wait_near(&bars->pready[t], steps[t] & 1, abort_flag);
               if (!ok) break;
               tc_fence_after();
-              const uint32_t va = sbase + C::OFF_KV + (v % C::KVST) * C::TILE;
               const uint32_t id = idesc_bf16_f32(BM, DP, false, true);
-              for (int kk = 0; kk < ksteps; ++kk)
-                mma_bf16_ts(tmem + O_COL + 128u * t, tmem + S_COL + 128u * t + 8u * kk, tile::desc_mn(va, kk), id,
-                            j > 0 || kk > 0);
-              mma_commit(&bars->pvdone[t]);
-              if (last) mma_commit(&bars->ofull[t]);
+              if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk)
+                  if (kk < ksteps)
+                    mma_bf16_ts(tmem + O_COL + 128u * t, tmem + S_COL + 128u * t + 8u * kk, vd + tile::step_mn(kk), id,
+                                j > 0 || kk > 0);
+                mma_commit(&bars->pvdone[t]);
+                if (last) mma_commit(&bars->ofull[t]);
+                if (t == w.nt - 1) mma_commit(&bars->kvempty[vs]);
+              }
+              __syncwarp();
               ++steps[t];
               if (last) ++items[t];
-              if (t == w.nt - 1) mma_commit(&bars->kvempty[v % C::KVST]);
             }
             if (t < nt2) {
-              if (t == 0) ok = mbar_wait(&bars->kvfull[k % C::KVST], (k / C::KVST) & 1, abort_flag);
-              if (ok && last) ok = mbar_wait(&bars->qfull[(q0 + t) % QST], ((q0 + t) / QST) & 1, abort_flag);
+              if (t == 0) ok = warp_wait_near(&bars->kvfull[k % C::KVST], (k / C::KVST) & 1, abort_flag);
+              if (last) ok = ok && warp_wait_near(&bars->qfull[(q0 + t) % QST], ((q0 + t) / QST) & 1, abort_flag);
               if (!ok) break;
               tc_fence_after();
-              issue_s(t, nx, j2, q0 + t, k);
-              if (t == nt2 - 1) mma_commit(&bars->kvempty[k % C::KVST]);
+              issue_s(t, nx, j2, q0 + t, k, t == nt2 - 1);
             }
           }
         }
         if (nx.i < a.total) qi += nx.nt;
         w = nx;
       }
-      mma_commit(&bars->final_);
+      if (elect_one()) mma_commit(&bars->final_);
+      __syncwarp();
       mbar_wait_drain(&bars->final_, 0);
+      __syncwarp();
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax, one row per thread
@@ -323,7 +342,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       float m = 0.f, l = 0.f;
       for (int j = 0; j < w.nk; ++j, ++step) {
         const int nv = tile_keys(w, j);
-        if (!(ok = warp_wait(&bars->sfull[t], step & 1, abort_flag))) break;
+        if (!(ok = warp_wait_near(&bars->sfull[t], step & 1, abort_flag))) break;
         tc_fence_after();
         uint32_t s[4][32];
 #pragma unroll
@@ -351,7 +370,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           const float f = exp2_approx(m - m2);
           m = m2;
           l *= f;
-          if (!(ok = warp_wait(&bars->pvdone[t], (step - 1) & 1, abort_flag))) break;
+          if (!(ok = warp_wait_near(&bars->pvdone[t], (step - 1) & 1, abort_flag))) break;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < DP / 16; ++c) {
@@ -387,7 +406,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       }
       if (!ok) break;
       // the epilogue has read the last item's sums
-      if (!(ok = warp_wait(&bars->ofree[t], (item & 1) ^ 1, abort_flag))) break;
+      if (!(ok = warp_wait_near(&bars->ofree[t], (item & 1) ^ 1, abort_flag))) break;
       inv_l[t * BM + row] = 1.f / l;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->lready[t]);
@@ -419,7 +438,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const bool in = n < a.Nq;
         float inv = 0.f;
         if (w.nk > 0) {
-          ok = warp_wait(&bars->ofull[t], item[t] & 1, abort_flag) && warp_wait(&bars->lready[t], item[t] & 1, abort_flag);
+          ok = warp_wait_near(&bars->ofull[t], item[t] & 1, abort_flag) && warp_wait_near(&bars->lready[t], item[t] & 1, abort_flag);
           if (!ok) break;
           ++item[t];
           tc_fence_after();

@@ -140,6 +140,19 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
+// mbar_wait and warp_wait for waits that usually end within a few microseconds: a number of tests
+// (each of which pauses the thread in hardware for a while) come before the first look at the timer.
+__device__ __forceinline__ bool mbar_wait_near(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort_flag);
+}
+__device__ __forceinline__ bool warp_wait_near(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const bool ok = mbar_wait_near(bar, parity, abort_flag);
+  return __all_sync(0xffffffffu, ok);
+}
+
 // Same as mbar_wait, but ignores the abort flag (used while draining copies already in flight).
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -259,6 +272,22 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
                    smem_u32(bar))
                : "memory");
 }
+
+// One lane of a converged warp (the same one every time).  An MMA warp that stays converged and only
+// guards the tcgen05 instructions with this keeps its descriptors and addresses in uniform
+// registers, where those instructions want them; in a one-lane branch each of them is first moved
+// there, value by value.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+// The warp's number in its block, as a value that is uniform to the compiler too.
+__device__ __forceinline__ int warp_number() { return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0); }
 
 // Loads 32 consecutive fp32 columns of the calling thread's TMEM lane.
 __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {

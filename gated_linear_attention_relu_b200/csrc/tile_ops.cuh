@@ -20,6 +20,9 @@ __device__ __forceinline__ uint64_t desc_k(uint32_t base, int kk) {
 __device__ __forceinline__ uint64_t desc_mn(uint32_t base, int kk) {
   return smem_desc_sw128(base + static_cast<uint32_t>(kk) * 2048u, HALF, 1024);
 }
+// What K step kk adds to the descriptor of step 0 (addresses are in 16-byte units in its low bits).
+__device__ __forceinline__ constexpr uint64_t step_k(int kk) { return ((kk >> 2) * HALF + (kk & 3) * 32u) >> 4; }
+__device__ __forceinline__ constexpr uint64_t step_mn(int kk) { return (kk * 2048u) >> 4; }
 // Shared-memory address of 16-byte chunk ck (0..15) of row r in that layout.
 __device__ __forceinline__ uint32_t row_chunk(uint32_t base, int r, int ck) {
   return base + static_cast<uint32_t>(ck >> 3) * HALF + static_cast<uint32_t>(r) * 128u +
