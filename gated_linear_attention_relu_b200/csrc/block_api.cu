@@ -18,6 +18,7 @@
 #include "norm.cuh"
 #include "clip.cuh"
 #include "cross_simt.cuh"
+#include "cross_few.cuh"
 #include "cross_tc.cuh"
 #include "cross_bwd_tc.cuh"
 
@@ -122,7 +123,7 @@ struct Split {
 Split split_axis(int64_t tiles, int64_t blocks, int64_t want, int64_t least) {
   if (tiles <= 0 || blocks <= 0) return {1, static_cast<int>(std::max<int64_t>(tiles, 1))};
   int64_t parts = std::min(ceil_div(want, blocks), ceil_div(tiles, least));
-  parts = std::max<int64_t>(1, std::min<int64_t>(parts, 1024));
+  parts = std::max<int64_t>(1, std::min<int64_t>(parts, la::xs::MAX_SPLITS));
   const int64_t per = ceil_div(tiles, parts);
   return {static_cast<int>(ceil_div(tiles, per)), static_cast<int>(per)};
 }
@@ -146,6 +147,7 @@ Split split_waves(int64_t tiles, int64_t blocks, int64_t sm) {
 
 struct CrossPlan {
   bool tc;                       // tensor-core kernels (bf16)
+  bool few;                      // forward: few rows per key head
   int64_t rows, keys;            // B * H * Nq, B * Hkv * Nk
   int64_t q_tiles, k_tiles;      // per head
   int64_t pairs;                 // pairs of 128-query tiles per head (tensor cores)
@@ -169,7 +171,11 @@ CrossPlan cross_plan(const la_cross_problem& p, int sm) {
   c.tc = p.dtype == LA_BF16 && !(p.flags & LA_FLAG_FORCE_SIMT) && c.rows > 0 && c.keys > 0;
   c.pairs = ceil_div(p.Nq, 2 * la::xt::BM);
   c.pad = ceil_div(p.Nk, 16) * 16;
-  c.fwd = c.tc ? split_axis(ceil_div(p.Nk, la::xt::BN), p.B * p.H * c.pairs, sm, 4)
+  // A key head's rows in one block: one pass over the keys for all of them, where a tile of rows
+  // would be all but empty.
+  c.few = !(p.flags & LA_FLAG_FORCE_SIMT) && c.rows > 0 && c.keys > 0 && group * p.Nq <= la::xf::MAX_ROWS;
+  c.fwd = c.few ? split_axis(c.k_tiles, p.B * p.Hkv, 8 * int64_t(sm), 4)
+          : c.tc ? split_axis(ceil_div(p.Nk, la::xt::BN), p.B * p.H * c.pairs, sm, 4)
                : split_axis(c.k_tiles, p.B * p.H * c.q_tiles, want, 2);
   const int64_t q128 = ceil_div(p.Nq, la::xt::BM), k128 = ceil_div(p.Nk, la::xt::BN);
   c.dq = c.tc ? split_axis(k128, p.B * p.H * q128, sm, 4) : split_axis(c.k_tiles, p.B * p.H * c.q_tiles, want, 2);
@@ -236,8 +242,7 @@ int cross_forward_simt(const la_cross_problem& p, const CrossPlan& c, la::xs::Ar
     return LA_ERR_CUDA;
   ++*nl;
   if (c.fwd.parts > 1) {
-    if (launch_k(la::xs::join_kernel<D, T>, dim3(unsigned(ceil_div(c.rows, la::xs::THREADS / 32))), la::xs::THREADS, 0, st,
-                 true, a, part_o, part_ml, static_cast<T*>(O), lse))
+    if (launch_k(la::xs::join_kernel<D, T>, dim3(unsigned(c.rows)), 32 * la::xs::JOIN_WARPS, 0, st, true, a, part_o, part_ml, static_cast<T*>(O), lse))
       return LA_ERR_CUDA;
     ++*nl;
   }
@@ -365,6 +370,9 @@ int cross_forward_tc(const la_cross_problem& p, const CrossPlan& c, la::xs::Args
   t.splits = c.fwd.parts;
   t.per = c.fwd.per;
   t.total = p.B * p.H * c.pairs * c.fwd.parts;
+  t.fd_pairs = la::make_fastdiv(uint32_t(t.pairs));
+  t.fd_splits = la::make_fastdiv(uint32_t(t.splits));
+  t.fd_H = la::make_fastdiv(uint32_t(p.H));
   t.c = p.scale * la::xt::LOG2E;
   t.count = keys.count;
   t.o = a.o;
@@ -382,8 +390,7 @@ int cross_forward_tc(const la_cross_problem& p, const CrossPlan& c, la::xs::Args
   ++*nl;
   if (c.fwd.parts > 1) {
     use(a, c.fwd);
-    if (launch_k(la::xs::join_kernel<D, __nv_bfloat16>, dim3(unsigned(ceil_div(c.rows, la::xs::THREADS / 32))),
-                 la::xs::THREADS, 0, st, true, a, part_o, part_ml, static_cast<__nv_bfloat16*>(O), lse))
+    if (launch_k(la::xs::join_kernel<D, __nv_bfloat16>, dim3(unsigned(c.rows)), 32 * la::xs::JOIN_WARPS, 0, st, true, a, part_o, part_ml, static_cast<__nv_bfloat16*>(O), lse))
       return LA_ERR_CUDA;
     ++*nl;
   }
@@ -464,6 +471,28 @@ int with_type(const la_cross_problem& p, F&& f) {
     }
   };
   return p.dtype == LA_BF16 ? dim(__nv_bfloat16()) : dim(float());
+}
+
+template <int D, typename T, int R>
+int cross_few(const la_cross_problem& p, const CrossPlan& c, la::xs::Args a, const void* Q, const void* K, const void* V,
+              void* O, float* lse, uint8_t* ws, cudaStream_t st, int* nl) {
+  use(a, c.fwd);
+  float* part_o = reinterpret_cast<float*>(ws + c.off_o);
+  float2* part_ml = reinterpret_cast<float2*>(ws + c.off_ml);
+  const size_t smem = la::xf::smem_bytes<D, R>();
+  auto kern = la::xf::few_kernel<D, T, R>;
+  if (set_smem(kern, smem)) return LA_ERR_CUDA;
+  if (launch_k(kern, dim3(unsigned(p.B * p.Hkv * c.fwd.parts)), la::xf::THREADS, smem, st, false, a,
+               static_cast<const T*>(Q), static_cast<const T*>(K), static_cast<const T*>(V), static_cast<T*>(O), lse, part_o,
+               part_ml))
+    return LA_ERR_CUDA;
+  ++*nl;
+  if (c.fwd.parts > 1) {
+    if (launch_k(la::xs::join_kernel<D, T>, dim3(unsigned(c.rows)), 32 * la::xs::JOIN_WARPS, 0, st, true, a, part_o, part_ml, static_cast<T*>(O), lse))
+      return LA_ERR_CUDA;
+    ++*nl;
+  }
+  return LA_OK;
 }
 
 int need(const void* ptr, bool needed) {
@@ -811,7 +840,13 @@ int la_cross_forward(const la_cross_problem* p, const void* Q, const void* K, co
     const la::xs::Args a = cross_args(*p, c, kv_len, key_mask);
     rc = with_type(*p, [&](auto d, auto t) {
       constexpr int D = decltype(d)::value;
+      using T = decltype(t);
       uint8_t* w = static_cast<uint8_t*>(ws);
+      if (c.few) {
+        const int64_t r = p->H / p->Hkv * p->Nq;
+        auto f = r <= 1 ? cross_few<D, T, 1> : r <= 2 ? cross_few<D, T, 2> : r <= 4 ? cross_few<D, T, 4> : cross_few<D, T, 8>;
+        return f(*p, c, a, Q, K, V, O, lse, w, stream, &nl);
+      }
       if constexpr (sizeof(t) == 2) {
         if (c.tc) return cross_forward_tc<D>(*p, c, a, Q, K, V, O, lse, w, sm, stream, &nl);
       }

@@ -291,38 +291,71 @@ forward_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T*
   }
 }
 
-// Joins the splits' partial results, one warp per row: with M the largest maximum,
-// o = sum_s e^(m_s - M) o_s / sum_s e^(m_s - M) l_s.
+// Joins the splits' partial results, one block per row: with M the largest maximum,
+// o = sum_s e^(m_s - M) o_s / sum_s e^(m_s - M) l_s.  A warp adds every JOIN_WARPS-th part, and the
+// warps' sums are added in order.
+constexpr int JOIN_WARPS = 4, MAX_SPLITS = 1024;
+
 template <int D, typename T>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(32 * JOIN_WARPS)
 join_kernel(const __grid_constant__ Args a, const float* __restrict__ part_o, const float2* __restrict__ part_ml,
             T* __restrict__ O, float* __restrict__ lse) {
+  __shared__ float f[MAX_SPLITS];
+  __shared__ float red[JOIN_WARPS], sums[JOIN_WARPS][D];
   pdl_wait();
-  const int64_t row = int64_t(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= a.rows) return;
-  float M = NEG_INF;
-  for (int s = 0; s < a.splits; ++s) M = fmaxf(M, part_ml[int64_t(s) * a.rows + row].x);
+  const int64_t row = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float top = NEG_INF;
+  for (int s = threadIdx.x; s < a.splits; s += 32 * JOIN_WARPS) {
+    f[s] = part_ml[int64_t(s) * a.rows + row].x;
+    top = fmaxf(top, f[s]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) red[warp] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float M = top == NEG_INF ? 0.f : top;  // (nothing attended: every factor is 0)
+  __syncthreads();
+  float L = 0.f;
+  for (int s = threadIdx.x; s < a.splits; s += 32 * JOIN_WARPS) {
+    const float m = f[s];
+    f[s] = m == NEG_INF ? 0.f : expf(m - M);
+    L += f[s] * part_ml[int64_t(s) * a.rows + row].y;
+  }
+  L = ln::warp_sum(L);
+  if (lane == 0) red[warp] = L;
+  __syncthreads();
+  L = (red[0] + red[1]) + (red[2] + red[3]);
   constexpr int C = D / 32;
-  float acc[C], L = 0.f;
+  float acc[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) acc[c] = 0.f;
-  if (M > NEG_INF)
-    for (int s = 0; s < a.splits; ++s) {
-      const int64_t slot = int64_t(s) * a.rows + row;
-      const float2 ml = part_ml[slot];
-      if (ml.x == NEG_INF) continue;
-      const float f = expf(ml.x - M);
-      L += f * ml.y;
+  const float* po = part_o + row * D + lane;
+  int s = warp;
+  for (; s + 7 * JOIN_WARPS < a.splits; s += 8 * JOIN_WARPS) {  // (a part without keys has sums of 0)
+    float v[8][C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] += f * part_o[slot * D + lane + 32 * c];
-    }
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int c = 0; c < C; ++c) v[k][c] = po[int64_t(s + k * JOIN_WARPS) * a.rows * D + 32 * c];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] += f[s + k * JOIN_WARPS] * v[k][c];
+  }
+  for (; s < a.splits; s += JOIN_WARPS)
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] += f[s] * po[int64_t(s) * a.rows * D + 32 * c];
+#pragma unroll
+  for (int c = 0; c < C; ++c) sums[warp][lane + 32 * c] = acc[c];
+  __syncthreads();
   const int64_t n = row % a.Nq, bh = row / a.Nq;
   T* o = O + (bh / a.H) * a.o.b + (bh % a.H) * a.o.h + n * a.o.n;
   const float inv = L > 0.f ? 1.f / L : 0.f;
-#pragma unroll
-  for (int c = 0; c < C; ++c) ln::put(o[lane + 32 * c], acc[c] * inv);
-  if (lse && lane == 0) lse[row] = L > 0.f ? M + logf(L) : NEG_INF;
+  for (int c = threadIdx.x; c < D; c += 32 * JOIN_WARPS)
+    ln::put(o[c], ((sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c])) * inv);
+  if (lse && threadIdx.x == 0) lse[row] = L > 0.f ? M + logf(L) : NEG_INF;
 }
 
 // D_i = dO_i . O_i for every query row, one warp per row.

@@ -7,7 +7,7 @@
 // keep its running maximum and sum in registers and write P = 2^(S c - m) back to tensor memory as
 // bf16 (rounded once; the sum takes the unrounded values), and O += P V with P as the operand in
 // tensor memory.  The two query tiles alternate, so that the tensor cores work on one while the
-// exponentials of the other are computed.  With c = scale log2(e) and a reference maximum m that is
+// exponentials of the other are computed: their warps on a scheduler take turns at those.  With c = scale log2(e) and a reference maximum m that is
 // only raised when a row's maximum has grown by more than 2^8 (then O and the sum are rescaled),
 // the accumulator is hardly ever touched between the first and the last key tile.
 // The last key tile is cut to a multiple of 16 keys in both products and to a multiple of 32 in the
@@ -17,7 +17,8 @@
 // keys where there are too few items):
 //   0-3, 4-7   softmax of query tile 0 / 1 (thread = row)
 //   8-11       epilogue: O / sum to global memory, a row per thread in 32-byte stores
-//   12, 13     TMA producer, MMA issuer (14, 15 complete the warpgroup)
+//   12         TMA producer
+//   13, 14     MMA issuers of query tile 0 / 1 (15 completes the warpgroup)
 // Tensor memory: S (and P) of the two tiles in columns [0, 256), O in [256, 512).
 // Every wait is bounded (mbar_wait).
 #pragma once
@@ -50,15 +51,16 @@ static_assert(Cfg<128>::SMEM <= 232448 && Cfg<64>::SMEM <= 232448, "shared memor
 
 constexpr uint32_t S_COL = 0, O_COL = 256;  // + 128 t
 // Registers: 128 a thread at launch (the host checks that), handed on to the softmax warps.
-constexpr uint32_t REGS_LAUNCH = 128, REGS_SOFTMAX = 184, REGS_EPI = 80, REGS_CTRL = 64;
+constexpr uint32_t REGS_LAUNCH = 128, REGS_SOFTMAX = 176, REGS_EPI = 104, REGS_CTRL = 56;
 static_assert(256 * REGS_SOFTMAX + 128 * REGS_EPI + 128 * REGS_CTRL <= THREADS * REGS_LAUNCH, "register split");
 
 template <int DP>
 struct Bars {
   uint64_t qfull[QST], qempty[QST];
   uint64_t kvfull[Cfg<DP>::KVST], kvempty[Cfg<DP>::KVST];
+  uint64_t order[2][4];
   uint64_t sfull[2], pready[2], pvdone[2], ofull[2], ofree[2], lready[2];
-  uint64_t final_;
+  uint64_t final_[2];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -70,6 +72,7 @@ struct Args {
   int32_t pairs;          // pairs of query tiles per head
   int32_t group;          // query heads per key head
   int32_t splits, per;    // parts of the keys, key tiles per part
+  FastDiv fd_pairs, fd_splits, fd_H;
   float c;                // scale * log2(e)
   const int32_t* count;   // keys per batch row (gathered), or null: Nk
   xs::Str o;
@@ -93,11 +96,11 @@ __device__ __forceinline__ Work get_work(const Args& a, int64_t i) {
   Work w;
   w.i = i;
   uint32_t r = static_cast<uint32_t>(i);
-  const uint32_t q = r / static_cast<uint32_t>(a.pairs);
+  const uint32_t q = fdiv(r, a.fd_pairs);
   w.pair = static_cast<int32_t>(r - q * a.pairs);
-  r = q / static_cast<uint32_t>(a.splits);
+  r = fdiv(q, a.fd_splits);
   w.split = static_cast<int32_t>(q - r * a.splits);
-  w.b = static_cast<int32_t>(r / static_cast<uint32_t>(a.H));
+  w.b = static_cast<int32_t>(fdiv(r, a.fd_H));
   w.h = static_cast<int32_t>(r - w.b * static_cast<uint32_t>(a.H));
   w.keys = a.count ? __ldg(a.count + w.b) : static_cast<int32_t>(a.Nk);
   const int32_t tiles = (w.keys + BN - 1) / BN;
@@ -125,6 +128,17 @@ __device__ __forceinline__ int tile_keys(const Work& w, int j) {
   return left < BN ? left : BN;
 }
 
+// A position in a ring of n stages and the parity of its round.
+struct Ring {
+  uint32_t s, ph;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++s == n) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+};
+
 template <uint32_t R>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
@@ -143,6 +157,35 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8], bool wi
     reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
   }
+}
+
+// The running maximum over up to 32 scores (n of them attended).
+__device__ __forceinline__ void row_max(uint32_t (&s)[32], int n, float (&mx)[4]) {
+  if (n < 32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i >= n) s[i] = __float_as_uint(xs::NEG_INF);
+  }
+#pragma unroll
+  for (int i = 0; i < 32; i += 2)
+    mx[(i / 2) & 3] = max3(mx[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+}
+// p = 2^(s c - m) of 32 scores (0 past the n-th), as bf16 to tensor memory; adds to the sums.
+__device__ __forceinline__ void row_exp(uint32_t (&s)[32], int n, uint64_t c2, uint64_t m2, uint64_t (&sum)[2], uint32_t to) {
+  if (n < 32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i >= n) s[i] = __float_as_uint(xs::NEG_INF);
+  }
+  uint32_t p[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint64_t x2 = fma2(pk(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, m2);
+    const float2 x = upk(x2), e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+    sum[i & 1] = add2(sum[i & 1], pk(e.x, e.y));
+    p[i] = pack_bf16(e.x, e.y);
+  }
+  tmem_st_x16(to, p);
 }
 
 // DP: channels as the tensor cores see them (64 or 128); D: channels of the tensors (32 runs as 64
@@ -168,17 +211,18 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     }
     for (int s = 0; s < C::KVST; ++s) {
       mbar_init(&bars->kvfull[s], 1);
-      mbar_init(&bars->kvempty[s], 1);
+      mbar_init(&bars->kvempty[s], 2);  // both issuers
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->sfull[t], 1);
       mbar_init(&bars->pready[t], 4);
+      for (int q = 0; q < 4; ++q) mbar_init(&bars->order[t][q], 1);
       mbar_init(&bars->pvdone[t], 1);
       mbar_init(&bars->ofull[t], 1);
       mbar_init(&bars->ofree[t], 4);
       mbar_init(&bars->lready[t], 4);
+      mbar_init(&bars->final_[t], 1);
     }
-    mbar_init(&bars->final_, 1);
     bars->abort_flag = 0;
     fence_mbar_init();
   }
@@ -238,93 +282,116 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         for (uint32_t j = (ki > C::KVST ? ki - C::KVST : 0); j < ki; ++j)
           mbar_wait_drain(&bars->kvfull[j % C::KVST], (j / C::KVST) & 1);
       }
-    } else if (warp == 13) {
-      // ---------------------------------------------------------- MMA issuer (the warp stays converged)
-      uint32_t qi = 0, ki = 0;                 // query tiles and key/value tiles consumed so far
-      uint32_t steps[2] = {0, 0}, items[2] = {0, 0};
+    } else if (warp == 13 || warp == 14) {
+      // ---------------------------------------------------------- MMA issuers, one for each query tile
+      // (so that one's waits and bookkeeping hide behind the other's products).  The warp stays
+      // converged; what does not depend on P is waited for and computed before P is.
+      const int t = warp - 13;
+      Ring k = {0, 0}, q = {0, 0};  // K and V tiles (they share a ring), Q tiles
+      uint32_t step = 0, item = 0;
       bool ok = true;
-      // S_t of (w, j): its Q tile is number q of the ring, its K tile number k; `free_k`: no other
-      // product of this K tile follows.
-      auto issue_s = [&](int t, const Work& w, int j, uint32_t q, uint32_t k, bool free_k) {
-        const uint32_t n16 = static_cast<uint32_t>((tile_keys(w, j) + 15) & ~15);
-        const uint32_t id = idesc_n(BM, n16);
-        const uint32_t qs = q % QST, ks = k % C::KVST;
-        const uint64_t qd = tile::desc_k(sbase + C::OFF_Q + qs * C::TILE, 0);
-        const uint64_t kd = tile::desc_k(sbase + C::OFF_KV + ks * C::TILE, 0);
-        if (elect_one()) {
+      const uint32_t ps = tmem + S_COL + 128u * t, po = tmem + O_COL + 128u * t;
+      constexpr uint32_t id_o = idesc_bf16_f32(BM, DP, false, true);
+      auto id_s = [&](const Work& w, int j) { return idesc_n(BM, static_cast<uint32_t>((tile_keys(w, j) + 15) & ~15)); };
+      auto s_mma = [&](uint64_t qd, uint64_t kd, uint32_t id) {
 #pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk)
-            mma_bf16(tmem + S_COL + 128u * t, qd + tile::step_k(kk), kd + tile::step_k(kk), id, kk > 0);
-          mma_commit(&bars->sfull[t]);
-          if (j == w.nk - 1) mma_commit(&bars->qempty[qs]);
-          if (free_k) mma_commit(&bars->kvempty[ks]);
+        for (int kk = 0; kk < DP / 16; ++kk) mma_bf16(ps, qd + tile::step_k(kk), kd + tile::step_k(kk), id, kk > 0);
+        mma_commit(&bars->sfull[t]);
+      };
+      // The slot of this issuer's Q tile of an item; the ring moves past all of the item's.
+      auto q_slot = [&](const Work& w) {
+        Ring mine = q;
+        q.next(QST);
+        if (w.nt == 2) {
+          if (t == 1) mine = q;
+          q.next(QST);
         }
-        __syncwarp();
+        return mine;
       };
       Work w = next_work(a, blockIdx.x);
+      uint32_t qs = 0;
       if (w.i < a.total) {
         ok = warp_wait_near(&bars->kvfull[0], 0, abort_flag);
-        for (int t = 0; ok && t < w.nt; ++t) {
-          ok = warp_wait_near(&bars->qfull[t], 0, abort_flag);
+        const Ring mine = q_slot(w);
+        qs = mine.s;
+        if (t < w.nt) {
+          ok = ok && warp_wait_near(&bars->qfull[qs], mine.ph, abort_flag);
           tc_fence_after();
-          if (ok) issue_s(t, w, 0, t, 0, t == w.nt - 1);
+          if (ok && elect_one()) {
+            s_mma(tile::desc_k(sbase + C::OFF_Q + qs * C::TILE, 0), tile::desc_k(sbase + C::OFF_KV, 0), id_s(w, 0));
+            if (w.nk == 1) mma_commit(&bars->qempty[qs]);
+            mma_commit(&bars->kvempty[0]);
+          }
+          __syncwarp();
+        } else if (ok && lane == 0) {
+          mbar_arrive(&bars->kvempty[0]);
         }
-        qi = w.nt;
-        ki = 1;
+        k.next(C::KVST);
       }
       while (ok && w.i < a.total) {
-        Work nx = w;
+        const Work nx = next_work(a, w.i + gridDim.x);
         for (int j = 0; ok && j < w.nk; ++j) {
           const bool last = j + 1 == w.nk;
-          if (last) nx = next_work(a, w.i + gridDim.x);
-          const bool more = !last || nx.i < a.total;
-          const int j2 = last ? 0 : j + 1;
-          const uint32_t v = ki++, k = ki;
-          if (more) ++ki;
-          const int nt2 = more ? nx.nt : 0;
-          const uint32_t q0 = last ? qi : qi - static_cast<uint32_t>(w.nt);
-          const int ksteps = (tile_keys(w, j) + 15) >> 4;
-          const uint32_t vs = v % C::KVST;
-          const uint64_t vd = tile::desc_mn(sbase + C::OFF_KV + vs * C::TILE, 0);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (t < w.nt) {
-              // O_t += P_t V (first of an item: the epilogue has read the last item's O_t)
-              if (t == 0) ok = ok && warp_wait_near(&bars->kvfull[vs], (v / C::KVST) & 1, abort_flag);
-              if (j == 0) ok = ok && warp_wait_near(&bars->ofree[t], (items[t] & 1) ^ 1, abort_flag);
-              ok = ok && warp_wait_near(&bars->pready[t], steps[t] & 1, abort_flag);
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t id = idesc_bf16_f32(BM, DP, false, true);
-              if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                  if (kk < ksteps)
-                    mma_bf16_ts(tmem + O_COL + 128u * t, tmem + S_COL + 128u * t + 8u * kk, vd + tile::step_mn(kk), id,
-                                j > 0 || kk > 0);
-                mma_commit(&bars->pvdone[t]);
-                if (last) mma_commit(&bars->ofull[t]);
-                if (t == w.nt - 1) mma_commit(&bars->kvempty[vs]);
-              }
-              __syncwarp();
-              ++steps[t];
-              if (last) ++items[t];
-            }
-            if (t < nt2) {
-              if (t == 0) ok = warp_wait_near(&bars->kvfull[k % C::KVST], (k / C::KVST) & 1, abort_flag);
-              if (last) ok = ok && warp_wait_near(&bars->qfull[(q0 + t) % QST], ((q0 + t) / QST) & 1, abort_flag);
-              if (!ok) break;
-              tc_fence_after();
-              issue_s(t, nx, j2, q0 + t, k, t == nt2 - 1);
+          const bool more = !last || nx.i < a.total;       // a K tile follows
+          const bool now = t < w.nt, then = last ? more && t < nx.nt : now;  // this tile takes part
+          const Ring v = k;
+          k.next(C::KVST);
+          const Ring k2 = k;
+          if (more) k.next(C::KVST);
+          ok = warp_wait_near(&bars->kvfull[v.s], v.ph, abort_flag);
+          if (more) ok = ok && warp_wait_near(&bars->kvfull[k2.s], k2.ph, abort_flag);
+          if (last && more) {
+            const Ring mine = q_slot(nx);
+            if (then) {
+              qs = mine.s;
+              ok = ok && warp_wait_near(&bars->qfull[mine.s], mine.ph, abort_flag);
             }
           }
+          const uint64_t vd = tile::desc_mn(sbase + C::OFF_KV + v.s * C::TILE, 0);
+          const uint64_t kd = tile::desc_k(sbase + C::OFF_KV + k2.s * C::TILE, 0);
+          const uint64_t qd = tile::desc_k(sbase + C::OFF_Q + qs * C::TILE, 0);
+          const int ksteps = (tile_keys(w, j) + 15) >> 4;
+          const uint32_t ids = last ? id_s(nx, 0) : id_s(w, j + 1);
+          const bool q_done = last ? nx.nk == 1 : j + 2 == w.nk;  // the next S is the last one of its Q tile
+          if (now) {
+            // O_t += P_t V (first of an item: the epilogue has read the last item's O_t)
+            if (j == 0) ok = ok && warp_wait_near(&bars->ofree[t], (item & 1) ^ 1, abort_flag);
+            ok = ok && warp_wait_near(&bars->pready[t], step & 1, abort_flag);
+          }
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (now) {
+#pragma unroll
+              for (int kk = 0; kk < BN / 16; ++kk)
+                if (kk < ksteps) mma_bf16_ts(po, ps + 8u * kk, vd + tile::step_mn(kk), id_o, j > 0 || kk > 0);
+              mma_commit(&bars->pvdone[t]);
+            }
+            if (then) s_mma(qd, kd, ids);
+            if (now) {
+              if (last) mma_commit(&bars->ofull[t]);
+              mma_commit(&bars->kvempty[v.s]);
+            } else {
+              mbar_arrive(&bars->kvempty[v.s]);
+            }
+            if (then) {
+              if (q_done) mma_commit(&bars->qempty[qs]);
+              mma_commit(&bars->kvempty[k2.s]);
+            } else if (more) {
+              mbar_arrive(&bars->kvempty[k2.s]);
+            }
+          }
+          __syncwarp();
+          if (now) {
+            ++step;
+            if (last) ++item;
+          }
         }
-        if (nx.i < a.total) qi += nx.nt;
         w = nx;
       }
-      if (elect_one()) mma_commit(&bars->final_);
+      if (elect_one()) mma_commit(&bars->final_[t]);
       __syncwarp();
-      mbar_wait_drain(&bars->final_, 0);
+      mbar_wait_drain(&bars->final_[t], 0);
       __syncwarp();
     }
   } else if (warp < 8) {
@@ -335,33 +402,33 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + S_COL + 128u * t + lane_bits;
     const uint32_t to = tmem + O_COL + 128u * t + lane_bits;
-    uint32_t step = 0, item = 0;
+    uint32_t step = 0, item = 0, turn = 0;
     bool ok = true;
-    for (Work w = next_work(a, blockIdx.x); ok && w.i < a.total; w = next_work(a, w.i + gridDim.x)) {
+    Work nx = next_work(a, blockIdx.x);
+    while (ok && nx.i < a.total) {
+      const Work w = nx;
+      nx = next_work(a, w.i + gridDim.x);
       if (t >= w.nt) continue;
       float m = 0.f, l = 0.f;
       for (int j = 0; j < w.nk; ++j, ++step) {
         const int nv = tile_keys(w, j);
         if (!(ok = warp_wait_near(&bars->sfull[t], step & 1, abort_flag))) break;
         tc_fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (32 * c < nv) tmem_ld_x32(ts + 32 * c, s[c]);
-        tmem_ld_wait();
+        // Two passes over the row in chunks of 32 scores, by small loops: the code stays within the
+        // instruction cache, and a row needs 64 registers instead of 128.
+        const int nc = (nv + 31) >> 5;
         float mx[4] = {xs::NEG_INF, xs::NEG_INF, xs::NEG_INF, xs::NEG_INF};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (32 * c >= nv) break;
-          if (nv - 32 * c < 32) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i >= nv - 32 * c) s[c][i] = __float_as_uint(xs::NEG_INF);
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[c][i]));
+        uint32_t s0[32], s1[32];
+#pragma unroll 1
+        for (int c = 0; c < nc; c += 2) {
+          tmem_ld_x32(ts + 32 * c, s0);
+          if (c + 1 < nc) tmem_ld_x32(ts + 32 * c + 32, s1);
+          tmem_ld_wait();
+          row_max(s0, nv - 32 * c, mx);
+          if (c + 1 < nc) row_max(s1, nv - 32 * c - 32, mx);
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
+        tmem_ld_x32(ts, s0);
         if (j == 0) {
           m = top;
         } else if (__any_sync(0xffffffffu, top > m + RESCALE)) {
@@ -384,25 +451,30 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
         const uint64_t c2 = pk(a.c, a.c), m2 = pk(-m, -m);
         uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (32 * c >= nv) break;
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 x = upk(fma2(pk(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), c2, m2));
-            const float e0 = exp2_approx(x.x), e1 = exp2_approx(x.y);
-            sum[i & 1] = add2(sum[i & 1], pk(e0, e1));
-            p[i] = pack_bf16(e0, e1);
+        // The two tiles' warps on a scheduler take turns at the exponentials: one tile's run while the
+        // other's products do, instead of both at once at half the rate.
+        if (w.nt == 2 && !(ok = warp_wait_near(&bars->order[t][quarter], t == 0 ? (turn & 1) ^ 1 : turn & 1, abort_flag))) break;
+#pragma unroll 1
+        for (int c = 0; c < nc; c += 2) {
+          tmem_ld_wait();
+          if (c + 1 < nc) tmem_ld_x32(ts + 32 * c + 32, s1);
+          row_exp(s0, nv - 32 * c, c2, m2, sum, ts + 16 * c);
+          if (c + 1 < nc) {
+            tmem_ld_wait();
+            if (c + 2 < nc) tmem_ld_x32(ts + 32 * c + 64, s0);
+            row_exp(s1, nv - 32 * c - 32, c2, m2, sum, ts + 16 * c + 16);
           }
-          tmem_st_x16(ts + 16 * c, p);
+        }
+        if (w.nt == 2) {
+          if (lane == 0) mbar_arrive(&bars->order[t ^ 1][quarter]);
+          ++turn;
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->pready[t]);
-        const float2 s0 = upk(sum[0]), s1 = upk(sum[1]);
-        l += (s0.x + s0.y) + (s1.x + s1.y);
+        const float2 u0 = upk(sum[0]), u1 = upk(sum[1]);
+        l += (u0.x + u0.y) + (u1.x + u1.y);
       }
       if (!ok) break;
       // the epilogue has read the last item's sums
@@ -428,6 +500,11 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
     uint32_t item[2] = {0, 0};
     bool ok = true;
+    auto release = [&](int t) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->ofree[t]);
+    };
     for (int64_t i = blockIdx.x; ok && i < a.total; i += gridDim.x) {
       const Work w = get_work(a, i);
       for (int t = 0; t < w.nt; ++t) {
@@ -449,23 +526,16 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           else if (lse)
             lse[r] = xs::NEG_INF;
         }
+        const uint32_t ot = tmem + O_COL + 128u * t + lane_bits;
+        if (a.splits > 1) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t v[32];
-          if (w.nk > 0) {
-            tmem_ld_x32(tmem + O_COL + 128u * t + lane_bits + 32 * c, v);
-            tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = 0;
-          }
-          if (c == D / 32 - 1 && w.nk > 0) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->ofree[t]);
-          }
-          if (!in) continue;
-          if (a.splits > 1) {
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32] = {};
+            if (w.nk > 0) {
+              tmem_ld_x32(ot + 32 * c, v);
+              tmem_ld_wait();
+            }
+            if (!in) continue;
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
               uint32_t u[8];
@@ -473,15 +543,27 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
               for (int k = 0; k < 8; ++k) u[k] = v[e + k];
               store32(po + 32 * c + e, u, true);
             }
-          } else {
+          }
+          if (w.nk > 0) release(t);
+        } else {
+          // the row to registers as bf16, O_t back to the tensor cores, then the stores
+          uint32_t u[D / 16][8] = {};
+          if (w.nk > 0) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 16) {
-              uint32_t u[8];
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld_x32(ot + 32 * c, v);
+              tmem_ld_wait();
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                u[k] = pack_bf16(__uint_as_float(v[e + 2 * k]) * inv, __uint_as_float(v[e + 2 * k + 1]) * inv);
-              store32(o + 32 * c + e, u, wide != 0);
+              for (int k = 0; k < 16; ++k)
+                u[2 * c + k / 8][k % 8] =
+                    pack_bf16(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv);
             }
+            release(t);
+          }
+          if (in) {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) store32(o + 16 * c, u[c], wide != 0);
           }
         }
       }
