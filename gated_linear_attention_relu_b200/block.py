@@ -9,8 +9,9 @@ call allocates (outputs that are not given, a workspace that is not given) belon
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -46,7 +47,7 @@ def _lib():
     global _declared
     lib = load()
     if not _declared:
-        C, N, G = (ctypes.POINTER(t) for t in (LaCrossProblem, LaNormProblem, LaGrad))
+        C = N = G = _VP  # structs, by reference or as packed bytes
         i64, f32 = ctypes.c_int64, ctypes.c_float
         for name, res, args in (
             ("la_cross_workspace_bytes", _SIZE, [C]),
@@ -68,70 +69,81 @@ def _lib():
     return lib
 
 
-def _ok(rc: int, where: str):
-    if rc != 0:
-        raise LaError(rc, where)
-
-
 def _torch_dtype(name: str):
     import torch
 
     return torch.bfloat16 if name == "bf16" else torch.float32
 
 
-def _want(t, name: str, shape, dtype, device, dense: bool = False):
-    """Raises ValueError unless ``t`` is a CUDA tensor of this shape, type and device."""
+def _wrong(t, name, shape, dtype, device, dense):
+    """Raises the ValueError that says what is wrong with a tensor."""
     if t.device != device or device.type != "cuda":
         raise ValueError(f"{name}: on {t.device}, expected {device} (a CUDA device)")
     if t.dtype is not dtype:
         raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dense and not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
+    raise ValueError(f"{name}: must be contiguous" if dense else f"{name}: the elements of a row must be contiguous")
+
+
+def _want(t, name: str, shape, dtype, device):
+    """A contiguous CUDA tensor of this shape, type and device, or ValueError."""
+    if not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda and t.is_contiguous()):
+        _wrong(t, name, shape, dtype, device, True)
+
+
+def _rows(t, name, shape, dtype, device):
+    """The same, but only the last dimension need be contiguous.  Returns the strides."""
+    st = t.stride()
+    if not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda and
+            (st[-1] == 1 or shape[-1] <= 1 or t.numel() == 0)):
+        _wrong(t, name, shape, dtype, device, False)
+    return st
 
 
 def _p(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _out(t, name: str, shape, dtype, device, dense: bool = False):
-    """``t`` checked, or a new tensor."""
-    import torch
+class _On:
+    """Makes ``device`` and ``stream`` current, so that the library's device queries and the caching
+    allocator see them; ``handle`` is the stream's.  (A class: entering it costs less than a
+    generator.)"""
 
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _want(t, name, shape, dtype, device, dense)
-    return t
+    __slots__ = ("handle", "guard")
+
+    def __init__(self, device, stream):
+        import torch
+
+        self.guard = None
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream: on {stream.device}, the tensors are on {device}")
+            self.guard = torch.cuda.stream(stream)
+        else:
+            if torch.cuda.current_device() != device.index:
+                self.guard = torch.cuda.device(device)
+            stream = torch.cuda.current_stream(device)
+        self.handle = stream.cuda_stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            return self.guard.__exit__(*exc)
+        return None
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """Makes ``device`` and ``stream`` current, so that the library's device queries and the
-    caching allocator see them; gives the stream's handle."""
-    import torch
-
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream: on {stream.device}, the tensors are on {device}")
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
-    elif torch.cuda.current_device() == device.index:
-        yield torch.cuda.current_stream().cuda_stream
-    else:
-        with torch.cuda.device(device):
-            yield torch.cuda.current_stream().cuda_stream
-
-
-def _workspace(ws, device, nbytes):
-    """(tensor, size): the given workspace, or a new one of ``nbytes()`` bytes."""
+def _workspace(ws, device, query, *args):
+    """(tensor, size): the given workspace, or a new one of the size that ``query(*args)`` says."""
     import torch
 
     if ws is None:
-        n = nbytes()
+        n = query(*args)
         return torch.empty(max(n, 16), dtype=torch.uint8, device=device), n
-    if isinstance(ws, tuple):  # what cross_workspace() and its like return
-        ws = ws[0]
     if ws.device != device or ws.dtype is not torch.uint8 or not ws.is_contiguous():
         raise ValueError(f"ws: a contiguous uint8 tensor on {device} is expected")
     return ws, ws.numel()
@@ -157,22 +169,36 @@ class CrossProblem:
     def kv_heads(self) -> int:
         return self.H if self.Hkv is None else self.Hkv
 
-    def c(self, **tensors) -> LaCrossProblem:
-        """The C struct; a tensor that is not given counts as dense."""
+    @functools.cached_property
+    def _head(self) -> bytes:
+        """The struct up to the strides."""
         scale = self.d ** -0.5 if self.scale is None else self.scale
-        c = LaCrossProblem(self.B, self.H, self.kv_heads, self.Nq, self.Nk, self.d,
+        return struct.pack("=5q2ifI", self.B, self.H, self.kv_heads, self.Nq, self.Nk, self.d,
                            LA_BF16 if self.dtype == "bf16" else LA_F32, float(scale),
                            LA_FLAG_FORCE_SIMT if self.force_simt else 0)
-        for name in ("q", "k", "v", "o", "dout", "dq", "dk", "dv"):
-            t = tensors.get(name)
-            if t is None:
-                keys = name in ("k", "v", "dk", "dv")
-                n = self.Nk if keys else self.Nq
-                s = ((self.kv_heads if keys else self.H) * n * self.d, n * self.d, self.d)
-            else:
-                s = t.stride()
-            setattr(c, name, LaStrides(*s[:3]))
-        return c
+
+    @functools.cached_property
+    def _shapes(self):
+        return (self.B, self.H, self.Nq, self.d), (self.B, self.kv_heads, self.Nk, self.d)
+
+    def c(self, q=None, k=None, v=None, o=None, dout=None, dq=None, dk=None, dv=None) -> LaCrossProblem:
+        """The C struct, from the tensors' strides; None counts as dense."""
+        dq_ = (self.H * self.Nq * self.d, self.Nq * self.d, self.d, 1)
+        dk_ = (self.kv_heads * self.Nk * self.d, self.Nk * self.d, self.d, 1)
+        return LaCrossProblem.from_buffer_copy(self._packed(q or dq_, k or dk_, v or dk_, o or dq_, dout or dq_, dq or dq_,
+                                                            dk or dk_, dv or dk_))
+
+    def _packed(self, q, k, v, o, *grads) -> bytes:
+        """The struct's bytes, from the strides of four or eight tensors."""
+        if not grads:
+            return self._head + _STRIDES4(*q[:3], *k[:3], *v[:3], *o[:3]) + _NO_STRIDES
+        g, dq, dk, dv = grads
+        return (self._head + _STRIDES4(*q[:3], *k[:3], *v[:3], *o[:3]) +
+                _STRIDES4(*g[:3], *dq[:3], *dk[:3], *dv[:3]))
+
+
+_STRIDES4 = struct.Struct("=12q").pack
+_NO_STRIDES = bytes(96)
 
 
 def cross_workspace_bytes(p: CrossProblem, sm_count: Optional[int] = None) -> int:
@@ -192,21 +218,15 @@ def cross_workspace(p: CrossProblem, device="cuda"):
         return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
-def _rows(t, name, shape, dtype, device):
-    _want(t, name, shape, dtype, device)
-    if t.numel() and shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the channels of a row must be contiguous")
-
-
 def _cross_masks(p: CrossProblem, kv_len, key_mask, device):
     import torch
 
     if kv_len is not None:
-        _want(kv_len, "kv_len", (p.B,), torch.int32, device, dense=True)
+        _want(kv_len, "kv_len", (p.B,), torch.int32, device)
     if key_mask is not None:
         if key_mask.dtype not in (torch.bool, torch.uint8):
             raise ValueError(f"key_mask: {key_mask.dtype}, expected torch.bool or torch.uint8")
-        _want(key_mask, "key_mask", (p.B, p.Nk), key_mask.dtype, device, dense=True)
+        _want(key_mask, "key_mask", (p.B, p.Nk), key_mask.dtype, device)
 
 
 def cross_forward(p: CrossProblem, Q, K, V, kv_len=None, key_mask=None, O=None, lse=None, return_lse=False,
@@ -218,22 +238,27 @@ def cross_forward(p: CrossProblem, Q, K, V, kv_len=None, key_mask=None, O=None, 
     import torch
 
     dt, dev = _torch_dtype(p.dtype), Q.device
-    qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.kv_heads, p.Nk, p.d)
-    _rows(Q, "Q", qs, dt, dev)
-    _rows(K, "K", ks, dt, dev)
-    _rows(V, "V", ks, dt, dev)
-    _cross_masks(p, kv_len, key_mask, dev)
-    with _on(dev, stream) as st:
+    qs, ks = p._shapes
+    sq = _rows(Q, "Q", qs, dt, dev)
+    sk = _rows(K, "K", ks, dt, dev)
+    sv = _rows(V, "V", ks, dt, dev)
+    if kv_len is not None or key_mask is not None:
+        _cross_masks(p, kv_len, key_mask, dev)
+    lib = _lib()
+    with _On(dev, stream) as st:
         if O is None:
             O = torch.empty_like(Q)
-        _rows(O, "O", qs, dt, dev)
-        if lse is not None or return_lse:
-            lse = _out(lse, "lse", qs[:3], torch.float32, dev, dense=True)
-        c = p.c(q=Q, k=K, v=V, o=O)
-        lib = _lib()
-        ws, nbytes = _workspace(ws, dev, lambda: lib.la_cross_workspace_bytes(ctypes.byref(c)))
-        _ok(lib.la_cross_forward(ctypes.byref(c), _p(Q), _p(K), _p(V), _p(kv_len), _p(key_mask), _p(O), _p(lse),
-                                 _p(ws), nbytes, st), "la_cross_forward")
+        so = _rows(O, "O", qs, dt, dev)
+        if lse is not None:
+            _want(lse, "lse", qs[:3], torch.float32, dev)
+        elif return_lse:
+            lse = torch.empty(qs[:3], dtype=torch.float32, device=dev)
+        c = p._packed(sq, sk, sv, so)
+        ws, nbytes = _workspace(ws, dev, lib.la_cross_workspace_bytes, c)
+        rc = lib.la_cross_forward(c, Q.data_ptr(), K.data_ptr(), V.data_ptr(), _p(kv_len), _p(key_mask), O.data_ptr(),
+                                  _p(lse), ws.data_ptr(), nbytes, st)
+    if rc:
+        raise LaError(rc, "la_cross_forward")
     return (O, lse) if return_lse else O
 
 
@@ -242,20 +267,26 @@ def cross_backward(p: CrossProblem, Q, K, V, O, lse, dO, kv_len=None, key_mask=N
     import torch
 
     dt, dev = _torch_dtype(p.dtype), Q.device
-    qs, ks = (p.B, p.H, p.Nq, p.d), (p.B, p.kv_heads, p.Nk, p.d)
-    for t, name, shape in ((Q, "Q", qs), (K, "K", ks), (V, "V", ks), (O, "O", qs), (dO, "dO", qs)):
-        _rows(t, name, shape, dt, dev)
-    _want(lse, "lse", qs[:3], torch.float32, dev, dense=True)
-    _cross_masks(p, kv_len, key_mask, dev)
-    with _on(dev, stream) as st:
+    qs, ks = p._shapes
+    sq = _rows(Q, "Q", qs, dt, dev)
+    sk = _rows(K, "K", ks, dt, dev)
+    sv = _rows(V, "V", ks, dt, dev)
+    so = _rows(O, "O", qs, dt, dev)
+    sg = _rows(dO, "dO", qs, dt, dev)
+    _want(lse, "lse", qs[:3], torch.float32, dev)
+    if kv_len is not None or key_mask is not None:
+        _cross_masks(p, kv_len, key_mask, dev)
+    lib = _lib()
+    with _On(dev, stream) as st:
         dQ, dK, dV = grads if grads is not None else (torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V))
-        for t, name, shape in ((dQ, "dQ", qs), (dK, "dK", ks), (dV, "dV", ks)):
-            _rows(t, name, shape, dt, dev)
-        c = p.c(q=Q, k=K, v=V, o=O, dout=dO, dq=dQ, dk=dK, dv=dV)
-        lib = _lib()
-        ws, nbytes = _workspace(ws, dev, lambda: lib.la_cross_workspace_bytes(ctypes.byref(c)))
-        _ok(lib.la_cross_backward(ctypes.byref(c), _p(Q), _p(K), _p(V), _p(kv_len), _p(key_mask), _p(O), _p(lse),
-                                  _p(dO), _p(dQ), _p(dK), _p(dV), _p(ws), nbytes, st), "la_cross_backward")
+        c = p._packed(sq, sk, sv, so, sg, _rows(dQ, "dQ", qs, dt, dev), _rows(dK, "dK", ks, dt, dev),
+                      _rows(dV, "dV", ks, dt, dev))
+        ws, nbytes = _workspace(ws, dev, lib.la_cross_workspace_bytes, c)
+        rc = lib.la_cross_backward(c, Q.data_ptr(), K.data_ptr(), V.data_ptr(), _p(kv_len), _p(key_mask), O.data_ptr(),
+                                   lse.data_ptr(), dO.data_ptr(), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(),
+                                   ws.data_ptr(), nbytes, st)
+    if rc:
+        raise LaError(rc, "la_cross_backward")
     return dQ, dK, dV
 
 
@@ -271,10 +302,16 @@ class NormProblem:
     eps: float = 1e-6
     dtype: str = "bf16"
 
-    def c(self, x=None, y=None, dy=None, dx=None) -> LaNormProblem:
-        s = [self.cols if t is None else t.stride(0) for t in (x, y, dy, dx)]
-        return LaNormProblem(self.rows, self.cols, self.groups, *s, float(self.eps),
-                             LA_BF16 if self.dtype == "bf16" else LA_F32, 0)
+    def _packed(self, sx: int, sy: int, sdy: int, sdx: int) -> bytes:
+        return _NORM(self.rows, self.cols, self.groups, sx, sy, sdy, sdx, self.eps,
+                     LA_BF16 if self.dtype == "bf16" else LA_F32, 0)
+
+    def c(self) -> LaNormProblem:
+        """The C struct for dense tensors."""
+        return LaNormProblem.from_buffer_copy(self._packed(self.cols, self.cols, self.cols, self.cols))
+
+
+_NORM = struct.Struct("=7qfiI4x").pack
 
 
 def layernorm_workspace_bytes(p: NormProblem, sm_count: Optional[int] = None) -> int:
@@ -292,19 +329,12 @@ def layernorm_workspace(p: NormProblem, device="cuda"):
         return torch.empty(max(layernorm_workspace_bytes(p), 16), dtype=torch.uint8, device=device)
 
 
-def _cols(t, name, p: NormProblem, dev):
-    _want(t, name, (p.rows, p.cols), _torch_dtype(p.dtype), dev)
-    if t.numel() and p.cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the columns of a row must be contiguous")
-
-
 def _param(t, name, p: NormProblem, dev):
     import torch
 
     if t is not None:
-        if t.dim() == 1 and p.groups == 1:
-            t = t[None]
-        _want(t, name, (p.groups, p.cols), torch.float32, dev, dense=True)
+        shape = (p.cols,) if t.dim() == 1 and p.groups == 1 else (p.groups, p.cols)
+        _want(t, name, shape, torch.float32, dev)
 
 
 def layernorm_forward(p: NormProblem, x, weight=None, bias=None, y=None, mean=None, rstd=None, return_stats=False,
@@ -314,20 +344,25 @@ def layernorm_forward(p: NormProblem, x, weight=None, bias=None, y=None, mean=No
     Returns y, or (y, mean, rstd) ([rows] fp32) with ``return_stats``."""
     import torch
 
-    dev = x.device
-    _cols(x, "x", p, dev)
+    dev, dt, shape = x.device, _torch_dtype(p.dtype), (p.rows, p.cols)
+    sx = _rows(x, "x", shape, dt, dev)
     _param(weight, "weight", p, dev)
     _param(bias, "bias", p, dev)
-    with _on(dev, stream) as st:
+    lib = _lib()
+    with _On(dev, stream) as st:
         if y is None:
-            y = torch.empty((p.rows, p.cols), dtype=x.dtype, device=dev)
-        _cols(y, "y", p, dev)
+            y = torch.empty(shape, dtype=dt, device=dev)
+        sy = _rows(y, "y", shape, dt, dev)
+        for t, name in ((mean, "mean"), (rstd, "rstd")):
+            if t is not None:
+                _want(t, name, (p.rows,), torch.float32, dev)
         if return_stats or mean is not None or rstd is not None:
-            mean = _out(mean, "mean", (p.rows,), torch.float32, dev, dense=True)
-            rstd = _out(rstd, "rstd", (p.rows,), torch.float32, dev, dense=True)
-        c = p.c(x=x, y=y)
-        _ok(_lib().la_layernorm_forward(ctypes.byref(c), _p(x), _p(weight), _p(bias), _p(y), _p(mean), _p(rstd), st),
-            "la_layernorm_forward")
+            mean = torch.empty(p.rows, dtype=torch.float32, device=dev) if mean is None else mean
+            rstd = torch.empty(p.rows, dtype=torch.float32, device=dev) if rstd is None else rstd
+        rc = lib.la_layernorm_forward(p._packed(sx[0], sy[0], 0, 0), x.data_ptr(), _p(weight), _p(bias), y.data_ptr(),
+                                      _p(mean), _p(rstd), st)
+    if rc:
+        raise LaError(rc, "la_layernorm_forward")
     return (y, mean, rstd) if return_stats else y
 
 
@@ -337,71 +372,97 @@ def layernorm_backward(p: NormProblem, x, dy, mean, rstd, weight=None, dx=None, 
     None with ``param_grads`` False (then only those given are computed).  ``dx`` may be ``dy``."""
     import torch
 
-    dev = x.device
-    _cols(x, "x", p, dev)
-    _cols(dy, "dy", p, dev)
-    _param(weight, "weight", p, dev)
-    _want(mean, "mean", (p.rows,), torch.float32, dev, dense=True)
-    _want(rstd, "rstd", (p.rows,), torch.float32, dev, dense=True)
-    with _on(dev, stream) as st:
+    dev, dt, shape = x.device, _torch_dtype(p.dtype), (p.rows, p.cols)
+    sx = _rows(x, "x", shape, dt, dev)
+    sdy = _rows(dy, "dy", shape, dt, dev)
+    _want(mean, "mean", (p.rows,), torch.float32, dev)
+    _want(rstd, "rstd", (p.rows,), torch.float32, dev)
+    for t, name in ((weight, "weight"), (dweight, "dweight"), (dbias, "dbias")):
+        _param(t, name, p, dev)
+    lib = _lib()
+    with _On(dev, stream) as st:
         if dx is None:
-            dx = torch.empty((p.rows, p.cols), dtype=x.dtype, device=dev)
-        _cols(dx, "dx", p, dev)
-        for t, name in ((dweight, "dweight"), (dbias, "dbias")):
-            _param(t, name, p, dev)
+            dx = torch.empty(shape, dtype=dt, device=dev)
+        sdx = _rows(dx, "dx", shape, dt, dev)
         if param_grads:
-            shape = (p.groups, p.cols)
-            dweight = torch.empty(shape, dtype=torch.float32, device=dev) if dweight is None else dweight
-            dbias = torch.empty(shape, dtype=torch.float32, device=dev) if dbias is None else dbias
-        c = p.c(x=x, dy=dy, dx=dx)
-        lib = _lib()
-        ws, nbytes = _workspace(ws, dev, lambda: lib.la_layernorm_workspace_bytes(ctypes.byref(c)))
-        _ok(lib.la_layernorm_backward(ctypes.byref(c), _p(x), _p(dy), _p(weight), _p(mean), _p(rstd), _p(dx),
-                                      _p(dweight), _p(dbias), _p(ws), nbytes, st), "la_layernorm_backward")
+            gs = (p.groups, p.cols)
+            dweight = torch.empty(gs, dtype=torch.float32, device=dev) if dweight is None else dweight
+            dbias = torch.empty(gs, dtype=torch.float32, device=dev) if dbias is None else dbias
+        c = p._packed(sx[0], 0, sdy[0], sdx[0])
+        ws, nbytes = _workspace(ws, dev, lib.la_layernorm_workspace_bytes, p._packed(p.cols, p.cols, p.cols, p.cols))
+        rc = lib.la_layernorm_backward(c, x.data_ptr(), dy.data_ptr(), _p(weight), mean.data_ptr(), rstd.data_ptr(),
+                                       dx.data_ptr(), _p(dweight), _p(dbias), ws.data_ptr(), nbytes, st)
+    if rc:
+        raise LaError(rc, "la_layernorm_backward")
     return dx, dweight, dbias
 
 
 # ------------------------------------------------------------------------------- gradient clipping
+def _grad_fields(tensors, what):
+    """(pointers, element counts, la_dtypes, device index) of a list of contiguous CUDA tensors.
+    One pass in C per property: lists have hundreds of tensors, and a call may be short."""
+    import torch
+
+    T = torch.Tensor
+    kinds = {torch.bfloat16: LA_BF16, torch.float32: LA_F32}
+    types = [kinds.get(t.dtype) for t in tensors]
+    if None in types:
+        i = types.index(None)
+        raise ValueError(f"{what} {i}: {tensors[i].dtype}, expected torch.bfloat16 or torch.float32")
+    devices = list(map(T.get_device, tensors))
+    if min(devices) != max(devices) or devices[0] < 0:
+        i = next(i for i, d in enumerate(devices) if d != devices[0] or d < 0)
+        raise ValueError(f"{what} {i}: on {tensors[i].device}, expected one CUDA device for all")
+    if not all(map(T.is_contiguous, tensors)):
+        i = [t.is_contiguous() for t in tensors].index(False)
+        raise ValueError(f"{what} {i}: must be contiguous")
+    return list(map(T.data_ptr, tensors)), list(map(T.numel, tensors)), types, devices[0]
+
+
 def _grad_list(tensors, out):
+    """The C array of a list (as a numpy array of the struct's layout), its length and its device."""
+    import numpy as np
     import torch
 
     n = len(tensors)
     if out is not None and len(out) != n:
         raise ValueError(f"out: {len(out)} tensors for {n} gradients")
-    kinds = {torch.bfloat16: LA_BF16, torch.float32: LA_F32}
-    arr = (LaGrad * max(n, 1))()
-    dev = tensors[0].device if n else None
-    for i, t in enumerate(tensors):
-        o = t if out is None else out[i]
-        kind = kinds.get(t.dtype)
-        if kind is None:
-            raise ValueError(f"gradient {i}: {t.dtype}, expected torch.bfloat16 or torch.float32")
-        if t.device != dev or dev.type != "cuda":
-            raise ValueError(f"gradient {i}: on {t.device}, expected {dev} (a CUDA device)")
-        if not t.is_contiguous():
-            raise ValueError(f"gradient {i}: must be contiguous")
-        if o is not t and (o.dtype is not t.dtype or o.device != dev or o.shape != t.shape or not o.is_contiguous()):
-            raise ValueError(f"out {i}: must be a contiguous tensor like its gradient")
-        g = arr[i]
-        g.in_, g.out, g.numel, g.dtype = t.data_ptr(), o.data_ptr(), t.numel(), kind
-    return arr, n, dev
+    arr = np.zeros(max(n, 1), dtype=[("in", "u8"), ("out", "u8"), ("numel", "i8"), ("dtype", "i4"), ("reserved", "i4")])
+    if n == 0:
+        return arr, 0, None
+    ptr, numel, types, dev = _grad_fields(tensors, "gradient")
+    arr["in"], arr["numel"], arr["dtype"] = ptr, numel, types
+    if out is None:
+        arr["out"] = arr["in"]
+    else:
+        optr, onumel, otypes, odev = _grad_fields(out, "out")
+        if onumel != numel or otypes != types or odev != dev:
+            i = next((i for i in range(n) if onumel[i] != numel[i] or otypes[i] != types[i]), 0)
+            raise ValueError(f"out {i}: must have its gradient's size, type and device")
+        arr["out"] = optr
+    return arr, n, torch.device("cuda", dev)
 
 
 def _norm_call(tensors, max_norm, out, norm, ws, stream):
     import torch
 
     tensors = list(tensors)
-    arr, n, dev = _grad_list(tensors, out)
+    arr, n, dev = _grad_list(tensors, None if out is None else list(out))
     if dev is None:
         dev = norm.device if norm is not None else torch.device("cuda", torch.cuda.current_device())
-    with _on(dev, stream) as st:
-        norm = _out(norm, "norm", (), torch.float32, dev)
-        lib = _lib()
-        ws, nbytes = _workspace(ws, dev, lambda: lib.la_clip_workspace_bytes(n))
+    lib = _lib()
+    with _On(dev, stream) as st:
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=dev)
+        elif norm.numel() != 1 or norm.dtype is not torch.float32 or norm.device != dev:
+            raise ValueError(f"norm: one fp32 element on {dev} is expected")
+        ws, nbytes = _workspace(ws, dev, lib.la_clip_workspace_bytes, n)
         if max_norm is None:
-            _ok(lib.la_grad_norm(arr, n, _p(norm), _p(ws), nbytes, st), "la_grad_norm")
+            rc = lib.la_grad_norm(arr.ctypes.data, n, norm.data_ptr(), ws.data_ptr(), nbytes, st)
         else:
-            _ok(lib.la_clip_grad_norm(arr, n, float(max_norm), _p(norm), _p(ws), nbytes, st), "la_clip_grad_norm")
+            rc = lib.la_clip_grad_norm(arr.ctypes.data, n, float(max_norm), norm.data_ptr(), ws.data_ptr(), nbytes, st)
+    if rc:
+        raise LaError(rc, "la_grad_norm" if max_norm is None else "la_clip_grad_norm")
     return norm
 
 

@@ -432,6 +432,12 @@ int cross_backward_tc(const la_cross_problem& p, const CrossPlan& c, la::xs::Arg
   t.splits = c.dq.parts;
   t.per = c.dq.per;
   t.total = p.B * p.H * int64_t(t.tiles) * t.splits;
+  auto divisions = [&](int64_t heads) {
+    t.fd_tiles = la::make_fastdiv(uint32_t(t.tiles));
+    t.fd_splits = la::make_fastdiv(uint32_t(t.splits));
+    t.fd_heads = la::make_fastdiv(uint32_t(heads));
+  };
+  divisions(p.H);
   if (launch_k(kq, dim3(unsigned(std::min<int64_t>(t.total, sm))), la::xb::THREADS, mq, st, keys.count != nullptr, tq, tg,
                keys.k, keys.v, t, static_cast<const T*>(O), static_cast<const T*>(dO), lse, delta, static_cast<T*>(dQ), part,
                int(wide)))
@@ -448,6 +454,7 @@ int cross_backward_tc(const la_cross_problem& p, const CrossPlan& c, la::xs::Arg
   t.splits = c.dkv.parts;
   t.per = c.dkv.per;
   t.total = p.B * p.Hkv * int64_t(t.tiles) * t.splits;
+  divisions(p.Hkv);
   float* part_v = part + int64_t(c.dkv.parts) * c.keys * D;
   if (launch_k(kk, dim3(unsigned(std::min<int64_t>(t.total, sm))), la::xb::THREADS, mk, st, true, tq, tg, keys.k, keys.v, t,
                lse, delta, part, part_v))

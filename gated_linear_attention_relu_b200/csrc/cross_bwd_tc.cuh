@@ -18,7 +18,7 @@
 //
 // Warps: 0-7 math (warps 0-3 the first 64 columns of a tile, 4-7 the others; thread = row);
 // 8-11 dq: D_i of the next query tile, dQ to memory; dkv: lse and D of the query tiles to come;
-// 12 TMA producer, 13 MMA issuer.  One CTA per SM, persistent.  Every wait is bounded.
+// 12 TMA producer; 13, 14 MMA issuers.  One CTA per SM, persistent.  Every wait is bounded.
 #pragma once
 #include "cross_tc.cuh"
 
@@ -32,9 +32,10 @@ using xt::LOG2E;
 using xt::regs_dec;
 using xt::regs_inc;
 using xt::store32;
+using xt::store_row32;
 
 constexpr int THREADS = 512;
-constexpr uint32_t REGS_LAUNCH = 128, REGS_MATH = 184, REGS_AUX = 80, REGS_CTRL = 64;
+constexpr uint32_t REGS_LAUNCH = 128, REGS_MATH = 176, REGS_AUX = 104, REGS_CTRL = 56;
 static_assert(256 * REGS_MATH + 128 * REGS_AUX + 128 * REGS_CTRL <= THREADS * REGS_LAUNCH, "register split");
 
 struct Args {
@@ -44,6 +45,7 @@ struct Args {
   int32_t q_tiles;        // query tiles per head
   int32_t group;
   int32_t splits, per;    // dq: parts of the keys; dkv: parts of the group's query tiles
+  FastDiv fd_tiles, fd_splits, fd_heads;  // tiles, splits, H (dq) or Hkv (dkv)
   float c, scale;         // scale * log2(e), scale
   const int32_t* count;
   xs::Str o, dout, dq;
@@ -71,7 +73,7 @@ struct BarsQ {
   uint64_t kfull[CfgQ<DP>::KST], kempty[CfgQ<DP>::KST];
   uint64_t vfull[CfgQ<DP>::VST], vempty[CfgQ<DP>::VST];
   uint64_t sfull[2], dsready[2], dready[2];
-  uint64_t dpfull, dpfree, dqfull, dqfree, final_;
+  uint64_t dpfull, dpfree, dqfull, dqfree, final_[2];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -88,11 +90,11 @@ __device__ __forceinline__ WorkQ get_q(const Args& a, int64_t i) {
   WorkQ w;
   w.i = i;
   uint32_t r = static_cast<uint32_t>(i);
-  const uint32_t q = r / static_cast<uint32_t>(a.tiles);
+  const uint32_t q = fdiv(r, a.fd_tiles);
   w.qt = static_cast<int32_t>(r - q * a.tiles);
-  r = q / static_cast<uint32_t>(a.splits);
+  r = fdiv(q, a.fd_splits);
   w.split = static_cast<int32_t>(q - r * a.splits);
-  w.b = static_cast<int32_t>(r / static_cast<uint32_t>(a.H));
+  w.b = static_cast<int32_t>(fdiv(r, a.fd_heads));
   w.h = static_cast<int32_t>(r - w.b * static_cast<uint32_t>(a.H));
   w.keys = a.count ? __ldg(a.count + w.b) : static_cast<int32_t>(a.Nk);
   w.k0 = w.split * a.per;
@@ -158,7 +160,8 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     mbar_init(&bars->dpfree, 8);
     mbar_init(&bars->dqfull, 1);
     mbar_init(&bars->dqfree, 4);
-    mbar_init(&bars->final_, 1);
+    mbar_init(&bars->final_[0], 1);
+    mbar_init(&bars->final_[1], 1);
     bars->abort_flag = 0;
     fence_mbar_init();
   }
@@ -216,18 +219,19 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         drain(bars->vfull, C::VST, ki);
       }
     } else if (warp == 13) {
-      // ---------------------------------------------------------- MMA issuer (the warp stays converged)
+      // ---------------------------------------------------------- MMA issuer of S and dQ
+      // (the issuers' warps stay converged; one's waits hide behind the other's products)
       uint32_t i = 0, items = 0;  // steps (key tiles) and items done
       bool ok = true;
       auto issue_s = [&](const WorkQ& w, int j, uint32_t step, uint32_t item) {
         const uint32_t qs = (2 * item) % C::QST, ks = step % C::KST;
+        const uint32_t id = xt::idesc_n(BM, static_cast<uint32_t>((keys_of(w, j) + 15) & ~15));
+        const uint64_t qd = tile::desc_k(sbase + C::OFF_Q + qs * C::TILE, 0);
+        const uint64_t kd = tile::desc_k(sbase + C::OFF_K + ks * C::TILE, 0);
         ok = warp_wait_near(&bars->kfull[ks], (step / C::KST) & 1, abort_flag);
         if (j == 0) ok = ok && warp_wait_near(&bars->qfull[qs], ((2 * item) / C::QST) & 1, abort_flag);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t id = xt::idesc_n(BM, static_cast<uint32_t>((keys_of(w, j) + 15) & ~15));
-        const uint64_t qd = tile::desc_k(sbase + C::OFF_Q + qs * C::TILE, 0);
-        const uint64_t kd = tile::desc_k(sbase + C::OFF_K + ks * C::TILE, 0);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < DP / 16; ++kk)
@@ -237,51 +241,25 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         }
         __syncwarp();
       };
-      auto issue_dp = [&](const WorkQ& w, int j, uint32_t step, uint32_t item) {
-        const uint32_t gs = (2 * item + 1) % C::QST, vs = step % C::VST;
-        ok = warp_wait_near(&bars->vfull[vs], (step / C::VST) & 1, abort_flag);
-        if (j == 0) ok = ok && warp_wait_near(&bars->qfull[gs], ((2 * item + 1) / C::QST) & 1, abort_flag);
-        // the math warps have read the last dP
-        ok = ok && warp_wait_near(&bars->dpfree, (step & 1) ^ 1, abort_flag);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t id = xt::idesc_n(BM, static_cast<uint32_t>((keys_of(w, j) + 15) & ~15));
-        const uint64_t gd = tile::desc_k(sbase + C::OFF_Q + gs * C::TILE, 0);
-        const uint64_t vd = tile::desc_k(sbase + C::OFF_V + vs * C::TILE, 0);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk)
-            mma_bf16(tmem + Q_DP, gd + tile::step_k(kk), vd + tile::step_k(kk), id, kk > 0);
-          mma_commit(&bars->dpfull);
-          mma_commit(&bars->vempty[vs]);
-          if (j == w.nk - 1) mma_commit(&bars->qempty[gs]);
-        }
-        __syncwarp();
-      };
       WorkQ w = next_q(a, blockIdx.x);
-      if (w.i < a.total) {
-        issue_s(w, 0, 0, 0);
-        if (ok) issue_dp(w, 0, 0, 0);
-      }
+      if (w.i < a.total) issue_s(w, 0, 0, 0);
       while (ok && w.i < a.total) {
-        WorkQ nx = w;
+        const WorkQ nx = next_q(a, w.i + gridDim.x);
         for (int j = 0; ok && j < w.nk; ++j, ++i) {
           const bool last = j + 1 == w.nk;
-          if (last) nx = next_q(a, w.i + gridDim.x);
-          if (!last || nx.i < a.total) {
-            issue_s(nx, last ? 0 : j + 1, i + 1, items + (last ? 1 : 0));
-            if (ok) issue_dp(nx, last ? 0 : j + 1, i + 1, items + (last ? 1 : 0));
-            if (!ok) break;
-          }
+          if (!last)
+            issue_s(w, j + 1, i + 1, items);
+          else if (nx.i < a.total)
+            issue_s(nx, 0, i + 1, items + 1);
           // dQ += ds K
-          ok = warp_wait_near(&bars->dsready[i & 1], (i >> 1) & 1, abort_flag);
-          if (j == 0) ok = ok && warp_wait_near(&bars->dqfree, (items & 1) ^ 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
           const int ksteps = (keys_of(w, j) + 15) >> 4;
           const uint32_t ks = i % C::KST;
           const uint64_t kd = tile::desc_mn(sbase + C::OFF_K + ks * C::TILE, 0);
           const uint32_t ds = tmem + Q_S + 128u * (i & 1);
+          if (j == 0) ok = ok && warp_wait_near(&bars->dqfree, (items & 1) ^ 1, abort_flag);
+          ok = ok && warp_wait_near(&bars->dsready[i & 1], (i >> 1) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk)
@@ -296,9 +274,41 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         ++items;
         w = nx;
       }
-      if (elect_one()) mma_commit(&bars->final_);
+      if (elect_one()) mma_commit(&bars->final_[0]);
       __syncwarp();
-      mbar_wait_drain(&bars->final_, 0);
+      mbar_wait_drain(&bars->final_[0], 0);
+      __syncwarp();
+    } else if (warp == 14) {
+      // ---------------------------------------------------------- MMA issuer of dP
+      uint32_t i = 0, item = 0;
+      bool ok = true;
+      for (WorkQ w = next_q(a, blockIdx.x); ok && w.i < a.total; w = next_q(a, w.i + gridDim.x), ++item) {
+        const uint32_t gs = (2 * item + 1) % C::QST;
+        const uint64_t gd = tile::desc_k(sbase + C::OFF_Q + gs * C::TILE, 0);
+        for (int j = 0; j < w.nk; ++j, ++i) {
+          const uint32_t vs = i % C::VST;
+          const uint32_t id = xt::idesc_n(BM, static_cast<uint32_t>((keys_of(w, j) + 15) & ~15));
+          const uint64_t vd = tile::desc_k(sbase + C::OFF_V + vs * C::TILE, 0);
+          if (j == 0) ok = warp_wait_near(&bars->qfull[gs], ((2 * item + 1) / C::QST) & 1, abort_flag);
+          ok = ok && warp_wait_near(&bars->vfull[vs], (i / C::VST) & 1, abort_flag);
+          // the math warps have read the last dP
+          ok = ok && warp_wait_near(&bars->dpfree, (i & 1) ^ 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; ++kk)
+              mma_bf16(tmem + Q_DP, gd + tile::step_k(kk), vd + tile::step_k(kk), id, kk > 0);
+            mma_commit(&bars->dpfull);
+            mma_commit(&bars->vempty[vs]);
+            if (j == w.nk - 1) mma_commit(&bars->qempty[gs]);
+          }
+          __syncwarp();
+        }
+      }
+      if (elect_one()) mma_commit(&bars->final_[1]);
+      __syncwarp();
+      mbar_wait_drain(&bars->final_[1], 0);
       __syncwarp();
     }
   } else if (warp < 8) {
@@ -320,48 +330,54 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         const uint32_t ts = t_row + Q_S + 128u * (i & 1);
         if (!(ok = warp_wait_near(&bars->sfull[i & 1], (i >> 1) & 1, abort_flag))) break;
         tc_fence_after();
-        uint32_t s[2][32];
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (32 * q < nv) tmem_ld_x32(ts + 32 * q, s[q]);
-        tmem_ld_wait();
-#pragma unroll
+        // 32 columns at a time, by a loop: unrolled over the row, the kernel's code outgrows the
+        // instruction cache (and the warps wait for instructions, not for data).
+        uint32_t s[32];
+        if (nv > 0) tmem_ld_x32(ts, s);
+#pragma unroll 1
         for (int q = 0; q < 2; ++q) {
-          if (32 * q >= nv) break;
+          const int n = nv - 32 * q;
+          if (n > 0) {
+            tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 x = upk(fma2(pk(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), c2, nl2));
-            s[q][e] = __float_as_uint(exp2_approx(x.x));
-            s[q][e + 1] = __float_as_uint(exp2_approx(x.y));
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x = upk(fma2(pk(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, nl2));
+              s[e] = __float_as_uint(exp2_approx(x.x));
+              s[e + 1] = __float_as_uint(exp2_approx(x.y));
+            }
+            if (n < 32) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e >= n) s[e] = 0;
+            }
           }
-          if (nv - 32 * q < 32) {
+          if (q == 0) {
+            if (!(ok = warp_wait_near(&bars->dpfull, i & 1, abort_flag))) break;
+            tc_fence_after();
+          }
+          uint32_t g[32];
+          if (n > 0) {
+            tmem_ld_x32(t_row + Q_DP + 32 * q, g);
+            tmem_ld_wait();
+          }
+          if (q == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->dpfree);
+          }
+          if (n > 0) {
+            uint32_t d[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (e >= nv - 32 * q) s[q][e] = 0;
+            for (int e = 0; e < 16; ++e) {
+              const uint64_t x = add2(pk(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1])), nd2);
+              const float2 y = upk(mul2(x, pk(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]))));
+              d[e] = pack_bf16(y.x, y.y);
+            }
+            if (n > 32 && q == 0) tmem_ld_x32(ts + 32, s);
+            tmem_st_x16(ts + 16 * q, d);
           }
         }
-        if (!(ok = warp_wait_near(&bars->dpfull, i & 1, abort_flag))) break;
-        tc_fence_after();
-        uint32_t g[2][32];
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (32 * q < nv) tmem_ld_x32(t_row + Q_DP + 32 * q, g[q]);
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->dpfree);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (32 * q >= nv) break;
-          uint32_t d[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint64_t x = add2(pk(__uint_as_float(g[q][2 * e]), __uint_as_float(g[q][2 * e + 1])), nd2);
-            const float2 y = upk(mul2(x, pk(__uint_as_float(s[q][2 * e]), __uint_as_float(s[q][2 * e + 1]))));
-            d[e] = pack_bf16(y.x, y.y);
-          }
-          tmem_st_x16(ts + 16 * q, d);
-        }
+        if (!ok) break;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -387,40 +403,19 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         ++done;
         tc_fence_after();
       }
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
-        uint32_t v[32];
+        uint32_t v[32] = {};
         if (w.nk > 0) {
           tmem_ld_x32(t_dq + 32 * c, v);
           tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0;
         }
-        if (c == D / 32 - 1 && w.nk > 0) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->dqfree);
-        }
-        if (!in) continue;
-        if (a.splits > 1) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t u[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(__uint_as_float(v[e + k]) * a.scale);
-            store32(po + 32 * c + e, u, true);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; e += 16) {
-            uint32_t u[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              u[k] = pack_bf16(__uint_as_float(v[e + 2 * k]) * a.scale, __uint_as_float(v[e + 2 * k + 1]) * a.scale);
-            store32(o + 32 * c + e, u, wide != 0);
-          }
-        }
+        if (in) store_row32(o + 32 * c, po + 32 * c, v, a.scale, a.splits > 1, wide != 0);
+      }
+      if (w.nk > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->dqfree);
       }
       return true;
     };
@@ -429,28 +424,57 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     for (int64_t x = blockIdx.x; ok && x < a.total; x += gridDim.x) {
       const WorkQ w = get_q(a, x);
       if (w.nk > 0) {
-        const int64_t n = int64_t(w.qt) * BM + row;
-        float sum = 0.f;
-        if (n < a.Nq) {
-          const __nv_bfloat16* po = O + w.b * a.o.b + w.h * a.o.h + n * a.o.n;
-          const __nv_bfloat16* pg = dO + w.b * a.dout.b + w.h * a.dout.h + n * a.dout.n;
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-          for (int c = 0; c < D; c += 8) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(po + c)), v = __ldg(reinterpret_cast<const uint4*>(pg + c));
-            acc[0] += bf16lo(u.x) * bf16lo(v.x) + bf16hi(u.x) * bf16hi(v.x);
-            acc[1] += bf16lo(u.y) * bf16lo(v.y) + bf16hi(u.y) * bf16hi(v.y);
-            acc[2] += bf16lo(u.z) * bf16lo(v.z) + bf16hi(u.z) * bf16hi(v.z);
-            acc[3] += bf16lo(u.w) * bf16lo(v.w) + bf16hi(u.w) * bf16hi(v.w);
+        // A row is read by LPR neighbouring lanes, 16 bytes each, GRP rows of the warp's 32 at a time.
+        constexpr int LPR = D / 8, RPI = 32 / LPR, GRP = 4;
+        const int64_t n0 = int64_t(w.qt) * BM + quarter * 32;
+        const int r_in = lane / LPR, ch = (lane % LPR) * 8;
+        const __nv_bfloat16* po = O + w.b * a.o.b + w.h * a.o.h + ch;
+        const __nv_bfloat16* pg = dO + w.b * a.dout.b + w.h * a.dout.h + ch;
+        float* gd = delta + (int64_t(w.b) * a.H + w.h) * a.Nq;
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32; r0 += GRP * RPI) {
+          uint4 u[GRP], v[GRP];
+#pragma unroll
+          for (int k = 0; k < GRP; ++k) {
+            const int64_t n = n0 + r0 + k * RPI + r_in;
+            u[k] = v[k] = make_uint4(0, 0, 0, 0);
+            if (n < a.Nq) {
+              u[k] = __ldg(reinterpret_cast<const uint4*>(po + n * a.o.n));
+              v[k] = __ldg(reinterpret_cast<const uint4*>(pg + n * a.dout.n));
+            }
           }
-          sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-          if (w.split == 0) delta[(int64_t(w.b) * a.H + w.h) * a.Nq + n] = sum;
+#pragma unroll
+          for (int k = 0; k < GRP; ++k) {
+            float x = (bf16lo(u[k].x) * bf16lo(v[k].x) + bf16hi(u[k].x) * bf16hi(v[k].x)) +
+                      (bf16lo(u[k].y) * bf16lo(v[k].y) + bf16hi(u[k].y) * bf16hi(v[k].y));
+            x += (bf16lo(u[k].z) * bf16lo(v[k].z) + bf16hi(u[k].z) * bf16hi(v[k].z)) +
+                 (bf16lo(u[k].w) * bf16lo(v[k].w) + bf16hi(u[k].w) * bf16hi(v[k].w));
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            const int r = r0 + k * RPI + r_in;
+            // Buffer item & 1 was last read by the item two before, whose dQ this warp has stored.
+            if (ch == 0) {
+              d_sm[(item & 1) * BM + quarter * 32 + r] = x;
+              if (w.split == 0 && n0 + r < a.Nq) gd[n0 + r] = x;
+            }
+          }
         }
-        // Buffer item & 1 was last read by the item two before, whose dQ this warp has stored.
-        d_sm[(item & 1) * BM + row] = sum;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->dready[item & 1]);
         ++item;
+      }
+      if (x + gridDim.x < a.total) {  // the next item's rows on their way to L2 (a line per lane and step)
+        const WorkQ y = get_q(a, x + gridDim.x);
+        constexpr int LINES = (D * 2 + 127) / 128;
+#pragma unroll
+        for (int k = 0; k < LINES; ++k) {
+          const int e = k * 32 + lane;
+          const int64_t n = int64_t(y.qt) * BM + quarter * 32 + e / LINES;
+          if (y.nk > 0 && n < a.Nq) {
+            prefetch_l2(O + y.b * a.o.b + y.h * a.o.h + n * a.o.n + (e % LINES) * 64);
+            prefetch_l2(dO + y.b * a.dout.b + y.h * a.dout.h + n * a.dout.n + (e % LINES) * 64);
+          }
+        }
       }
       if (have) ok = finish(prev);
       prev = w;
@@ -484,7 +508,7 @@ struct BarsK {
   uint64_t gfull[CfgK<DP>::QST], gempty[CfgK<DP>::QST];
   uint64_t lfull[CfgK<DP>::QST], lempty[CfgK<DP>::QST];
   uint64_t kfull, kempty, vfull, vempty;
-  uint64_t sfull, pready, dpfull, dsready, accfull, accfree, final_;
+  uint64_t sfull, pready, dpfull, dsready, accfull, accfree, final_[2];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -501,11 +525,11 @@ __device__ __forceinline__ WorkK get_k(const Args& a, int64_t i) {
   WorkK w;
   w.i = i;
   uint32_t r = static_cast<uint32_t>(i);
-  const uint32_t q = r / static_cast<uint32_t>(a.tiles);
+  const uint32_t q = fdiv(r, a.fd_tiles);
   w.kt = static_cast<int32_t>(r - q * a.tiles);
-  r = q / static_cast<uint32_t>(a.splits);
+  r = fdiv(q, a.fd_splits);
   w.split = static_cast<int32_t>(q - r * a.splits);
-  w.b = static_cast<int32_t>(r / static_cast<uint32_t>(a.Hkv));
+  w.b = static_cast<int32_t>(fdiv(r, a.fd_heads));
   w.h = static_cast<int32_t>(r - w.b * static_cast<uint32_t>(a.Hkv));
   w.keys = a.count ? __ldg(a.count + w.b) : static_cast<int32_t>(a.Nk);
   w.t0 = w.split * a.per;
@@ -543,9 +567,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::QST; ++s) {
       mbar_init(&bars->qfull[s], 1);
-      mbar_init(&bars->qempty[s], 1);
+      mbar_init(&bars->qempty[s], 2);  // both issuers
       mbar_init(&bars->gfull[s], 1);
-      mbar_init(&bars->gempty[s], 1);
+      mbar_init(&bars->gempty[s], 2);
       mbar_init(&bars->lfull[s], 4);
       mbar_init(&bars->lempty[s], 8);
     }
@@ -557,9 +581,10 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     mbar_init(&bars->pready, 8);
     mbar_init(&bars->dpfull, 1);
     mbar_init(&bars->dsready, 8);
-    mbar_init(&bars->accfull, 1);
+    mbar_init(&bars->accfull, 2);
     mbar_init(&bars->accfree, 8);
-    mbar_init(&bars->final_, 1);
+    mbar_init(&bars->final_[0], 1);
+    mbar_init(&bars->final_[1], 1);
     bars->abort_flag = 0;
     fence_mbar_init();
   }
@@ -620,89 +645,72 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         drain(&bars->kfull, 1, k_out);
         drain(&bars->vfull, 1, v_out);
       }
-    } else if (warp == 13) {
-      // ---------------------------------------------------------- MMA issuer (the warp stays converged)
+    } else if (warp == 13 || warp == 14) {
+      // ---------------------------------------------------------- MMA issuers (converged warps)
+      // 13: S^T and dV, 14: dP^T and dK.  Each walks the same steps: the product of this step's p (ds)
+      // first, then the scores (dP) of the next step, which overwrite it.
+      const bool sv = warp == 13;
       uint32_t i = 0, items = 0;
       bool ok = true;
       const uint32_t id_s = idesc_bf16_f32(BM, BN, false, false), id_d = idesc_bf16_f32(BM, DP, false, true);
-      auto issue_s = [&](bool first, bool last, uint32_t step, uint32_t item) {
-        const uint32_t s = step % C::QST;
-        if (first) ok = warp_wait_near(&bars->kfull, item & 1, abort_flag);
-        ok = ok && warp_wait_near(&bars->qfull[s], (step / C::QST) & 1, abort_flag);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t kd = tile::desc_k(sbase + C::OFF_K, 0), qd = tile::desc_k(sbase + C::OFF_Q + s * C::TILE, 0);
-        if (elect_one()) {
+      const uint32_t t_in = tmem + (sv ? K_S : K_DP), t_acc = tmem + (sv ? K_DV : K_DK);
+      const uint32_t fixed = sbase + (sv ? C::OFF_K : C::OFF_V);          // the item's K (V) tile
+      const uint32_t in = sbase + (sv ? C::OFF_Q : C::OFF_G);             // ... times Q (dO) tiles
+      const uint32_t out = sbase + (sv ? C::OFF_G : C::OFF_Q);            // p dO (ds Q)
+      uint64_t* in_full = sv ? bars->qfull : bars->gfull;
+      uint64_t* in_empty = sv ? bars->qempty : bars->gempty;
+      uint64_t* out_empty = sv ? bars->gempty : bars->qempty;
+      uint64_t* fixed_full = sv ? &bars->kfull : &bars->vfull;
+      uint64_t* fixed_empty = sv ? &bars->kempty : &bars->vempty;
+      uint64_t* in_done = sv ? &bars->sfull : &bars->dpfull;
+      uint64_t* ready = sv ? &bars->pready : &bars->dsready;
+      const uint64_t fd = tile::desc_k(fixed, 0);
+      auto issue_in = [&](bool last, uint32_t s) {
+        const uint64_t id = tile::desc_k(in + s * C::TILE, 0);
 #pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk)
-            mma_bf16(tmem + K_S, kd + tile::step_k(kk), qd + tile::step_k(kk), id_s, kk > 0);
-          mma_commit(&bars->sfull);
-          if (last) mma_commit(&bars->kempty);
-        }
-        __syncwarp();
-      };
-      auto issue_dp = [&](bool first, bool last, uint32_t step, uint32_t item) {
-        const uint32_t s = step % C::QST;
-        if (first) ok = warp_wait_near(&bars->vfull, item & 1, abort_flag);
-        ok = ok && warp_wait_near(&bars->gfull[s], (step / C::QST) & 1, abort_flag);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t vd = tile::desc_k(sbase + C::OFF_V, 0), gd = tile::desc_k(sbase + C::OFF_G + s * C::TILE, 0);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk)
-            mma_bf16(tmem + K_DP, vd + tile::step_k(kk), gd + tile::step_k(kk), id_s, kk > 0);
-          mma_commit(&bars->dpfull);
-          if (last) mma_commit(&bars->vempty);
-        }
-        __syncwarp();
-      };
-      // acc += A (tensor memory, two halves of 64 rows of the product's K) B (rows of a Q or dO
-      // tile), then the tile is free (and, after an item's last product, its sums are complete).
-      auto issue_acc = [&](uint32_t acc, uint32_t at, uint32_t b, bool fresh, uint64_t* tile_free, uint64_t* full) {
-        const uint64_t bd = tile::desc_mn(b, 0);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < BM / 16; ++kk)
-            mma_bf16_ts(tmem + acc, tmem + at + 8u * (kk & 3) + 64u * (kk >> 2), bd + tile::step_mn(kk), id_d,
-                        !fresh || kk > 0);
-          mma_commit(tile_free);
-          if (full) mma_commit(full);
-        }
-        __syncwarp();
+        for (int kk = 0; kk < DP / 16; ++kk) mma_bf16(t_in, fd + tile::step_k(kk), id + tile::step_k(kk), id_s, kk > 0);
+        mma_commit(in_done);
+        mma_commit(&in_empty[s]);
+        if (last) mma_commit(fixed_empty);
       };
       WorkK w = next_k(a, blockIdx.x);
       if (w.i < a.total) {
-        issue_s(true, w.nq == 1, 0, 0);
-        if (ok) issue_dp(true, w.nq == 1, 0, 0);
+        ok = warp_wait_near(fixed_full, 0, abort_flag) && warp_wait_near(&in_full[0], 0, abort_flag);
+        tc_fence_after();
+        if (ok && elect_one()) issue_in(w.nq == 1, 0);
+        __syncwarp();
       }
       while (ok && w.i < a.total) {
-        WorkK nx = w;
+        const WorkK nx = next_k(a, w.i + gridDim.x);
         for (int j = 0; ok && j < w.nq; ++j, ++i) {
-          const bool last = j + 1 == w.nq;
-          if (last) nx = next_k(a, w.i + gridDim.x);
-          const bool more = !last || nx.i < a.total;
-          const uint32_t it2 = items + (last ? 1 : 0);
+          const bool last = j + 1 == w.nq, more = !last || nx.i < a.total;
           const bool last2 = last ? nx.nq == 1 : j + 2 == w.nq;
-          const uint32_t s = i % C::QST;
-          ok = warp_wait_near(&bars->pready, i & 1, abort_flag);
+          const uint32_t s = i % C::QST, s2 = (i + 1) % C::QST;
+          const uint64_t od = tile::desc_mn(out + s * C::TILE, 0);
+          if (more) {
+            if (last) ok = warp_wait_near(fixed_full, (items + 1) & 1, abort_flag);
+            ok = ok && warp_wait_near(&in_full[s2], ((i + 1) / C::QST) & 1, abort_flag);
+          }
           if (j == 0) ok = ok && warp_wait_near(&bars->accfree, (items & 1) ^ 1, abort_flag);
+          ok = ok && warp_wait_near(ready, i & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          issue_acc(K_DV, K_S, sbase + C::OFF_G + s * C::TILE, j == 0, &bars->gempty[s], nullptr);
-          if (more) issue_s(last, last2, i + 1, it2);
-          ok = ok && warp_wait_near(&bars->dsready, i & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          issue_acc(K_DK, K_DP, sbase + C::OFF_Q + s * C::TILE, j == 0, &bars->qempty[s], last ? &bars->accfull : nullptr);
-          if (more) issue_dp(last, last2, i + 1, it2);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < BM / 16; ++kk)
+              mma_bf16_ts(t_acc, t_in + 8u * (kk & 3) + 64u * (kk >> 2), od + tile::step_mn(kk), id_d, j > 0 || kk > 0);
+            mma_commit(&out_empty[s]);
+            if (last) mma_commit(&bars->accfull);
+            if (more) issue_in(last2, s2);
+          }
+          __syncwarp();
         }
         ++items;
         w = nx;
       }
-      if (elect_one()) mma_commit(&bars->final_);
+      if (elect_one()) mma_commit(&bars->final_[warp - 13]);
       __syncwarp();
-      mbar_wait_drain(&bars->final_, 0);
+      mbar_wait_drain(&bars->final_[warp - 13], 0);
       __syncwarp();
     }
   } else if (warp < 8) {

@@ -188,6 +188,28 @@ __device__ __forceinline__ void row_exp(uint32_t (&s)[32], int n, uint64_t c2, u
   tmem_st_x16(to, p);
 }
 
+// 32 fp32 channels of a row, times f: as bf16 to o, or (part) as they are to po.
+__device__ __forceinline__ void store_row32(__nv_bfloat16* o, float* po, const uint32_t (&v)[32], float f, bool part, bool wide) {
+  if (part) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+      uint32_t u[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(__uint_as_float(v[e + k]) * f);
+      store32(po + e, u, true);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; e += 16) {
+      uint32_t u[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        u[k] = pack_bf16(__uint_as_float(v[e + 2 * k]) * f, __uint_as_float(v[e + 2 * k + 1]) * f);
+      store32(o + e, u, wide);
+    }
+  }
+}
+
 // DP: channels as the tensor cores see them (64 or 128); D: channels of the tensors (32 runs as 64
 // with zeros, which the loads fill in).
 template <int DP, int D>
@@ -500,11 +522,6 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
     uint32_t item[2] = {0, 0};
     bool ok = true;
-    auto release = [&](int t) {
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->ofree[t]);
-    };
     for (int64_t i = blockIdx.x; ok && i < a.total; i += gridDim.x) {
       const Work w = get_work(a, i);
       for (int t = 0; t < w.nt; ++t) {
@@ -527,44 +544,20 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             lse[r] = xs::NEG_INF;
         }
         const uint32_t ot = tmem + O_COL + 128u * t + lane_bits;
-        if (a.splits > 1) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32] = {};
-            if (w.nk > 0) {
-              tmem_ld_x32(ot + 32 * c, v);
-              tmem_ld_wait();
-            }
-            if (!in) continue;
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t u[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) u[k] = v[e + k];
-              store32(po + 32 * c + e, u, true);
-            }
-          }
-          if (w.nk > 0) release(t);
-        } else {
-          // the row to registers as bf16, O_t back to the tensor cores, then the stores
-          uint32_t u[D / 16][8] = {};
+        // (by a loop: the kernel's code has to stay within the instruction cache)
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32] = {};
           if (w.nk > 0) {
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t v[32];
-              tmem_ld_x32(ot + 32 * c, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                u[2 * c + k / 8][k % 8] =
-                    pack_bf16(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv);
-            }
-            release(t);
+            tmem_ld_x32(ot + 32 * c, v);
+            tmem_ld_wait();
           }
-          if (in) {
-#pragma unroll
-            for (int c = 0; c < D / 16; ++c) store32(o + 16 * c, u[c], wide != 0);
-          }
+          if (in) store_row32(o + 32 * c, po + 32 * c, v, a.splits > 1 ? 1.f : inv, a.splits > 1, wide != 0);
+        }
+        if (w.nk > 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->ofree[t]);
         }
       }
     }
