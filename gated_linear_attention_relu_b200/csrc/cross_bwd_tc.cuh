@@ -103,14 +103,20 @@ __device__ __forceinline__ WorkQ get_q(const Args& a, int64_t i) {
   if (w.nk < 0) w.nk = 0;
   return w;
 }
-__device__ __forceinline__ WorkQ next_q(const Args& a, int64_t i) {
+// The item before this CTA's first, and the next one with work.
+__device__ __forceinline__ WorkQ before_first_q() {
   WorkQ w;
+  w.i = int64_t(blockIdx.x) - gridDim.x;
   w.nk = 0;
-  for (; i < a.total; i += gridDim.x) {
-    w = get_q(a, i);
-    if (w.nk > 0) return w;
-  }
-  w.i = a.total;
+  return w;
+}
+__device__ __forceinline__ WorkQ next_q(const Args& a, WorkQ w) {
+#pragma unroll 1
+  do {
+    w.i += gridDim.x;
+    if (w.i >= a.total) break;
+    w = get_q(a, w.i);
+  } while (w.nk == 0);
   return w;
 }
 __device__ __forceinline__ int keys_of(const WorkQ& w, int j) {
@@ -195,7 +201,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         ++qi;
         return true;
       };
-      for (WorkQ w = next_q(a, blockIdx.x); ok && w.i < a.total; w = next_q(a, w.i + gridDim.x)) {
+      for (WorkQ w = before_first_q(); ok && (w = next_q(a, w)).i < a.total;) {
         const int32_t kh = w.h / a.group;
         for (int j = 0; ok && j < w.nk; ++j, ++ki) {
           const int32_t n = (w.k0 + j) * BN;
@@ -233,24 +239,22 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         if (!ok) return;
         tc_fence_after();
         if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk)
-            mma_bf16(tmem + Q_S + 128u * (step & 1), qd + tile::step_k(kk), kd + tile::step_k(kk), id, kk > 0);
+          tile::mma_kk<DP>(tmem + Q_S + 128u * (step & 1), qd, kd, id);
           mma_commit(&bars->sfull[step & 1]);
           if (j == w.nk - 1) mma_commit(&bars->qempty[qs]);
         }
         __syncwarp();
       };
-      WorkQ w = next_q(a, blockIdx.x);
-      if (w.i < a.total) issue_s(w, 0, 0, 0);
-      while (ok && w.i < a.total) {
-        const WorkQ nx = next_q(a, w.i + gridDim.x);
-        for (int j = 0; ok && j < w.nk; ++j, ++i) {
-          const bool last = j + 1 == w.nk;
-          if (!last)
-            issue_s(w, j + 1, i + 1, items);
-          else if (nx.i < a.total)
-            issue_s(nx, 0, i + 1, items + 1);
+      WorkQ w, nx = before_first_q();
+      for (int first = 1; ok && nx.i < a.total; first = 0) {
+        w = nx;
+        nx = next_q(a, w);
+        // Step -1 of the first turn issues the very first S; every other step the next one's.
+        for (int j = -first; ok && j < w.nk; ++j) {
+          const bool last = j + 1 >= w.nk;
+          const WorkQ& v = last ? nx : w;
+          if (v.i < a.total) issue_s(v, last ? 0 : j + 1, i + (1 - first), items + (last && !first ? 1 : 0));
+          if (first) break;
           // dQ += ds K
           const int ksteps = (keys_of(w, j) + 15) >> 4;
           const uint32_t ks = i % C::KST;
@@ -261,18 +265,17 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)
-              if (kk < ksteps)
-                mma_bf16_ts(tmem + Q_DQ, ds + 8u * (kk & 3) + 64u * (kk >> 2), kd + tile::step_mn(kk),
-                            idesc_bf16_f32(BM, DP, false, true), j > 0 || kk > 0);
+#pragma unroll 1
+            for (int kk = 0; kk < ksteps; ++kk)
+              mma_bf16_ts(tmem + Q_DQ, ds + 8u * (kk & 3) + 64u * (kk >> 2), kd + tile::step_mn(kk),
+                          idesc_bf16_f32(BM, DP, false, true), j > 0 || kk > 0);
             mma_commit(&bars->kempty[ks]);
             if (last) mma_commit(&bars->dqfull);
           }
           __syncwarp();
+          ++i;
         }
-        ++items;
-        w = nx;
+        if (!first) ++items;
       }
       if (elect_one()) mma_commit(&bars->final_[0]);
       __syncwarp();
@@ -282,7 +285,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
       // ---------------------------------------------------------- MMA issuer of dP
       uint32_t i = 0, item = 0;
       bool ok = true;
-      for (WorkQ w = next_q(a, blockIdx.x); ok && w.i < a.total; w = next_q(a, w.i + gridDim.x), ++item) {
+      for (WorkQ w = before_first_q(); ok && (w = next_q(a, w)).i < a.total; ++item) {
         const uint32_t gs = (2 * item + 1) % C::QST;
         const uint64_t gd = tile::desc_k(sbase + C::OFF_Q + gs * C::TILE, 0);
         for (int j = 0; j < w.nk; ++j, ++i) {
@@ -296,9 +299,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < DP / 16; ++kk)
-              mma_bf16(tmem + Q_DP, gd + tile::step_k(kk), vd + tile::step_k(kk), id, kk > 0);
+            tile::mma_kk<DP>(tmem + Q_DP, gd, vd, id);
             mma_commit(&bars->dpfull);
             mma_commit(&bars->vempty[vs]);
             if (j == w.nk - 1) mma_commit(&bars->qempty[gs]);
@@ -319,7 +320,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 64u * hf;
     uint32_t i = 0, item = 0;
     bool ok = true;
-    for (WorkQ w = next_q(a, blockIdx.x); ok && w.i < a.total; w = next_q(a, w.i + gridDim.x), ++item) {
+    for (WorkQ w = before_first_q(); ok && (w = next_q(a, w)).i < a.total; ++item) {
       const int64_t n = int64_t(w.qt) * BM + row;
       const float nl = n < a.Nq ? -lse[(int64_t(w.b) * a.H + w.h) * a.Nq + n] * LOG2E : 0.f;
       if (!(ok = warp_wait_near(&bars->dready[item & 1], (item >> 1) & 1, abort_flag))) break;
@@ -538,14 +539,20 @@ __device__ __forceinline__ WorkK get_k(const Args& a, int64_t i) {
   if (w.nq < 0 || int64_t(w.kt) * BN >= w.keys) w.nq = 0;
   return w;
 }
-__device__ __forceinline__ WorkK next_k(const Args& a, int64_t i) {
+// The item before this CTA's first, and the next one with work.
+__device__ __forceinline__ WorkK before_first_k() {
   WorkK w;
+  w.i = int64_t(blockIdx.x) - gridDim.x;
   w.nq = 0;
-  for (; i < a.total; i += gridDim.x) {
-    w = get_k(a, i);
-    if (w.nq > 0) return w;
-  }
-  w.i = a.total;
+  return w;
+}
+__device__ __forceinline__ WorkK next_k(const Args& a, WorkK w) {
+#pragma unroll 1
+  do {
+    w.i += gridDim.x;
+    if (w.i >= a.total) break;
+    w = get_k(a, w.i);
+  } while (w.nq == 0);
   return w;
 }
 
@@ -612,7 +619,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       uint32_t qi = 0, items = 0;
       uint32_t k_out = 0, v_out = 0;
       bool ok = true;
-      for (WorkK w = next_k(a, blockIdx.x); ok && w.i < a.total; w = next_k(a, w.i + gridDim.x), ++items) {
+      for (WorkK w = before_first_k(); ok && (w = next_k(a, w)).i < a.total; ++items) {
         if (!(ok = mbar_wait_near(&bars->kempty, (items & 1) ^ 1, abort_flag))) break;
         load_tile<DP>(smem + C::OFF_K, &tmK, w.kt * BN, w.h, w.b, &bars->kfull);
         ++k_out;
@@ -666,22 +673,23 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       uint64_t* ready = sv ? &bars->pready : &bars->dsready;
       const uint64_t fd = tile::desc_k(fixed, 0);
       auto issue_in = [&](bool last, uint32_t s) {
-        const uint64_t id = tile::desc_k(in + s * C::TILE, 0);
-#pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk) mma_bf16(t_in, fd + tile::step_k(kk), id + tile::step_k(kk), id_s, kk > 0);
+        tile::mma_kk<DP>(t_in, fd, tile::desc_k(in + s * C::TILE, 0), id_s);
         mma_commit(in_done);
         mma_commit(&in_empty[s]);
         if (last) mma_commit(fixed_empty);
       };
-      WorkK w = next_k(a, blockIdx.x);
-      if (w.i < a.total) {
-        ok = warp_wait_near(fixed_full, 0, abort_flag) && warp_wait_near(&in_full[0], 0, abort_flag);
-        tc_fence_after();
-        if (ok && elect_one()) issue_in(w.nq == 1, 0);
-        __syncwarp();
-      }
-      while (ok && w.i < a.total) {
-        const WorkK nx = next_k(a, w.i + gridDim.x);
+      WorkK w, nx = before_first_k();
+      for (int first = 1; ok && nx.i < a.total; first = 0) {
+        w = nx;
+        nx = next_k(a, w);
+        if (first) {  // the first scores; the others follow the product before them
+          if (nx.i >= a.total) break;
+          ok = warp_wait_near(fixed_full, 0, abort_flag) && warp_wait_near(&in_full[0], 0, abort_flag);
+          tc_fence_after();
+          if (ok && elect_one()) issue_in(nx.nq == 1, 0);
+          __syncwarp();
+          continue;
+        }
         for (int j = 0; ok && j < w.nq; ++j, ++i) {
           const bool last = j + 1 == w.nq, more = !last || nx.i < a.total;
           const bool last2 = last ? nx.nq == 1 : j + 2 == w.nq;
@@ -706,7 +714,6 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
           __syncwarp();
         }
         ++items;
-        w = nx;
       }
       if (elect_one()) mma_commit(&bars->final_[warp - 13]);
       __syncwarp();
@@ -723,7 +730,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     const uint64_t c2 = pk(a.c, a.c);
     uint32_t i = 0, item = 0;
     bool ok = true;
-    for (WorkK w = next_k(a, blockIdx.x); ok && w.i < a.total; w = next_k(a, w.i + gridDim.x), ++item) {
+    for (WorkK w = before_first_k(); ok && (w = next_k(a, w)).i < a.total; ++item) {
       for (int j = 0; j < w.nq; ++j, ++i) {
         const uint32_t s_l = i % C::QST;
         const uint32_t la_ = sbase + C::OFF_L + (s_l * 2 * BM + 64 * hf) * 4, ld_ = la_ + BM * 4;
@@ -793,20 +800,12 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       const float f = hf == 0 ? 1.f : a.scale;
       float* out = (hf == 0 ? part_v : part_k) + (int64_t(w.split) * a.keys + (int64_t(w.b) * a.Hkv + w.h) * a.Nk + n) * D;
       const uint32_t ta = t_row + (hf == 0 ? K_DV : K_DK);
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
         tmem_ld_x32(ta + 32 * c, v);
         tmem_ld_wait();
-        if (n < w.keys) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t u[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(__uint_as_float(v[e + k]) * f);
-            store32(out + 32 * c + e, u, true);
-          }
-        }
+        if (n < w.keys) store_row32(nullptr, out + 32 * c, v, f, true, true);
       }
       tc_fence_before();
       __syncwarp();
@@ -818,7 +817,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     const int q = (warp & 3) * 32 + lane;
     uint32_t i = 0;
     bool ok = true;
-    for (WorkK w = next_k(a, blockIdx.x); ok && w.i < a.total; w = next_k(a, w.i + gridDim.x)) {
+    for (WorkK w = before_first_k(); ok && (w = next_k(a, w)).i < a.total;) {
       for (int j = 0; j < w.nq; ++j, ++i) {
         const uint32_t s = i % C::QST;
         const int32_t it = w.t0 + j, hq = it / a.q_tiles;

@@ -110,16 +110,21 @@ __device__ __forceinline__ Work get_work(const Args& a, int64_t i) {
   w.nt = int64_t(w.pair) * 2 * BM + BM < a.Nq ? 2 : 1;
   return w;
 }
-// The first item at or after i (in this CTA's steps) that has keys; i >= total: none.
-__device__ __forceinline__ Work next_work(const Args& a, int64_t i) {
+// The item before this CTA's first, and the next one that has keys (i >= total: none).  (The roles
+// call next_work in one place each: its code is inlined at every call.)
+__device__ __forceinline__ Work before_first() {
   Work w;
-  w.i = i;
-  w.nk = 0;
-  for (; i < a.total; i += gridDim.x) {
-    w = get_work(a, i);
-    if (w.nk > 0) return w;
-  }
-  w.i = a.total;
+  w.i = int64_t(blockIdx.x) - gridDim.x;
+  w.nk = w.nt = 0;
+  return w;
+}
+__device__ __forceinline__ Work next_work(const Args& a, Work w) {
+#pragma unroll 1
+  do {
+    w.i += gridDim.x;
+    if (w.i >= a.total) break;
+    w = get_work(a, w.i);
+  } while (w.nk == 0);
   return w;
 }
 // Attended keys in key tile j of an item.
@@ -281,21 +286,26 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         ++ki;
         return true;
       };
-      for (Work w = next_work(a, blockIdx.x); ok && w.i < a.total; w = next_work(a, w.i + gridDim.x)) {
-        for (int t = 0; ok && t < w.nt; ++t) {
-          const uint32_t s = qi % QST;
-          if (!(ok = mbar_wait_near(&bars->qempty[s], ((qi / QST) & 1) ^ 1, abort_flag))) break;
-          uint8_t* dst = smem + C::OFF_Q + s * C::TILE;
-          mbar_arrive_expect_tx(&bars->qfull[s], C::TILE);
-          const int32_t n = (w.pair * 2 + t) * BM;
-          tma_load_4d(dst, &tmQ, 0, n, w.h, w.b, &bars->qfull[s]);
-          if (DP == 128) tma_load_4d(dst + HALF, &tmQ, 64, n, w.h, w.b, &bars->qfull[s]);
-          ++qi;
-          if (t == 0 && !(ok = load_kv(&tmK, w, 0))) break;
-        }
-        for (int j = 0; ok && j < w.nk; ++j) {
-          ok = load_kv(&tmV, w, j);
-          if (ok && j + 1 < w.nk) ok = load_kv(&tmK, w, j + 1);
+      Work w = before_first();
+      while (ok && (w = next_work(a, w)).i < a.total) {
+        // Q0, K0, Q1, V0, then K and V of the other key tiles in turn
+        const int loads = w.nt + 2 * w.nk;
+#pragma unroll 1
+        for (int e = 0, t = 0, x = 0; ok && e < loads; ++e) {
+          if (t < w.nt && (e == 0 || e == 2)) {
+            const uint32_t s = qi % QST;
+            if (!(ok = mbar_wait_near(&bars->qempty[s], ((qi / QST) & 1) ^ 1, abort_flag))) break;
+            uint8_t* dst = smem + C::OFF_Q + s * C::TILE;
+            mbar_arrive_expect_tx(&bars->qfull[s], C::TILE);
+            const int32_t n = (w.pair * 2 + t) * BM;
+            tma_load_4d(dst, &tmQ, 0, n, w.h, w.b, &bars->qfull[s]);
+            if (DP == 128) tma_load_4d(dst + HALF, &tmQ, 64, n, w.h, w.b, &bars->qfull[s]);
+            ++qi;
+            ++t;
+          } else {
+            ok = load_kv((x & 1) ? &tmV : &tmK, w, x >> 1);
+            ++x;
+          }
         }
       }
       if (*abort_flag) {
@@ -316,8 +326,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       constexpr uint32_t id_o = idesc_bf16_f32(BM, DP, false, true);
       auto id_s = [&](const Work& w, int j) { return idesc_n(BM, static_cast<uint32_t>((tile_keys(w, j) + 15) & ~15)); };
       auto s_mma = [&](uint64_t qd, uint64_t kd, uint32_t id) {
-#pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk) mma_bf16(ps, qd + tile::step_k(kk), kd + tile::step_k(kk), id, kk > 0);
+        tile::mma_kk<DP>(ps, qd, kd, id);
         mma_commit(&bars->sfull[t]);
       };
       // The slot of this issuer's Q tile of an item; the ring moves past all of the item's.
@@ -330,28 +339,32 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
         return mine;
       };
-      Work w = next_work(a, blockIdx.x);
+      Work w, nx = before_first();
       uint32_t qs = 0;
-      if (w.i < a.total) {
-        ok = warp_wait_near(&bars->kvfull[0], 0, abort_flag);
-        const Ring mine = q_slot(w);
-        qs = mine.s;
-        if (t < w.nt) {
-          ok = ok && warp_wait_near(&bars->qfull[qs], mine.ph, abort_flag);
-          tc_fence_after();
-          if (ok && elect_one()) {
-            s_mma(tile::desc_k(sbase + C::OFF_Q + qs * C::TILE, 0), tile::desc_k(sbase + C::OFF_KV, 0), id_s(w, 0));
-            if (w.nk == 1) mma_commit(&bars->qempty[qs]);
-            mma_commit(&bars->kvempty[0]);
+      for (bool first = true; ok; first = false) {
+        w = nx;
+        if (w.i >= a.total) break;
+        nx = next_work(a, w);
+        if (first) {  // the first S; the others follow the product before them
+          if (nx.i >= a.total) break;
+          ok = warp_wait_near(&bars->kvfull[0], 0, abort_flag);
+          const Ring mine = q_slot(nx);
+          qs = mine.s;
+          if (t < nx.nt) {
+            ok = ok && warp_wait_near(&bars->qfull[qs], mine.ph, abort_flag);
+            tc_fence_after();
+            if (ok && elect_one()) {
+              s_mma(tile::desc_k(sbase + C::OFF_Q + qs * C::TILE, 0), tile::desc_k(sbase + C::OFF_KV, 0), id_s(nx, 0));
+              if (nx.nk == 1) mma_commit(&bars->qempty[qs]);
+              mma_commit(&bars->kvempty[0]);
+            }
+            __syncwarp();
+          } else if (ok && lane == 0) {
+            mbar_arrive(&bars->kvempty[0]);
           }
-          __syncwarp();
-        } else if (ok && lane == 0) {
-          mbar_arrive(&bars->kvempty[0]);
+          k.next(C::KVST);
+          continue;
         }
-        k.next(C::KVST);
-      }
-      while (ok && w.i < a.total) {
-        const Work nx = next_work(a, w.i + gridDim.x);
         for (int j = 0; ok && j < w.nk; ++j) {
           const bool last = j + 1 == w.nk;
           const bool more = !last || nx.i < a.total;       // a K tile follows
@@ -384,9 +397,8 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           tc_fence_after();
           if (elect_one()) {
             if (now) {
-#pragma unroll
-              for (int kk = 0; kk < BN / 16; ++kk)
-                if (kk < ksteps) mma_bf16_ts(po, ps + 8u * kk, vd + tile::step_mn(kk), id_o, j > 0 || kk > 0);
+#pragma unroll 1
+              for (int kk = 0; kk < ksteps; ++kk) mma_bf16_ts(po, ps + 8u * kk, vd + tile::step_mn(kk), id_o, j > 0 || kk > 0);
               mma_commit(&bars->pvdone[t]);
             }
             if (then) s_mma(qd, kd, ids);
@@ -409,7 +421,6 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             if (last) ++item;
           }
         }
-        w = nx;
       }
       if (elect_one()) mma_commit(&bars->final_[t]);
       __syncwarp();
@@ -426,11 +437,11 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const uint32_t to = tmem + O_COL + 128u * t + lane_bits;
     uint32_t step = 0, item = 0, turn = 0;
     bool ok = true;
-    Work nx = next_work(a, blockIdx.x);
+    Work nx = before_first();
     while (ok && nx.i < a.total) {
       const Work w = nx;
-      nx = next_work(a, w.i + gridDim.x);
-      if (t >= w.nt) continue;
+      nx = next_work(a, w);
+      if (t >= w.nt) continue;  // (also before the first)
       float m = 0.f, l = 0.f;
       for (int j = 0; j < w.nk; ++j, ++step) {
         const int nv = tile_keys(w, j);

@@ -140,13 +140,23 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
-// mbar_wait and warp_wait for waits that usually end within a few microseconds: a number of tests
-// (each of which pauses the thread in hardware for a while) come before the first look at the timer.
+// mbar_wait and warp_wait for kernels of many roles, whose code has to stay within the instruction
+// cache: a few instructions at every wait, and a limit on the tests (each of which the hardware
+// lets last up to some microseconds) instead of one on the time.
+#ifndef LA_WAIT_TESTS
+#define LA_WAIT_TESTS (1u << 22)
+#endif
 __device__ __forceinline__ bool mbar_wait_near(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  uint32_t i = 0;
+  bool ok;
 #pragma unroll 1
-  for (int i = 0; i < 32; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, abort_flag);
+  while (!(ok = mbar_try_wait(bar, parity)) && !*abort_flag) {
+    if (++i == LA_WAIT_TESTS) {
+      *abort_flag = 1;
+      atomicOr(&g_la_error, ERR_WAIT_TIMEOUT);
+    }
+  }
+  return ok;
 }
 __device__ __forceinline__ bool warp_wait_near(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   const bool ok = mbar_wait_near(bar, parity, abort_flag);

@@ -22,7 +22,18 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t base, int kk) {
 }
 // What K step kk adds to the descriptor of step 0 (addresses are in 16-byte units in its low bits).
 __device__ __forceinline__ constexpr uint64_t step_k(int kk) { return ((kk >> 2) * HALF + (kk & 3) * 32u) >> 4; }
-__device__ __forceinline__ constexpr uint64_t step_mn(int kk) { return (kk * 2048u) >> 4; }
+__device__ __forceinline__ constexpr uint64_t step_mn(int kk) { return (static_cast<uint32_t>(kk) * 2048u) >> 4; }
+// D = A B, both K-major tiles of D channels, by a loop (kernels of many roles are bound by the
+// instruction cache before they are by the few instructions that a loop adds).
+template <int CH>
+__device__ __forceinline__ void mma_kk(uint32_t d, uint64_t a, uint64_t b, uint32_t id) {
+#pragma unroll 1
+  for (uint32_t h = 0; h < CH / 64; ++h) {
+    const uint64_t at = h * (HALF >> 4);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) mma_bf16(d, a + at + step_k(kk), b + at + step_k(kk), id, (h | kk) != 0);
+  }
+}
 // Shared-memory address of 16-byte chunk ck (0..15) of row r in that layout.
 __device__ __forceinline__ uint32_t row_chunk(uint32_t base, int r, int ck) {
   return base + static_cast<uint32_t>(ck >> 3) * HALF + static_cast<uint32_t>(r) * 128u +
