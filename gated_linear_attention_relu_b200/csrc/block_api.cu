@@ -542,14 +542,6 @@ bool norm_alias_ok(const la_norm_problem& p, const void* in, int64_t si, const v
   return d >= p.cols * e && d <= s - p.cols * e;
 }
 
-// Blocks (and slots of dweight and dbias) per group of the backward kernel: enough to fill the
-// machine, each with at least 8 steps over its rows.
-struct NormPlan {
-  int wpr;          // warps per row
-  int parts;
-  size_t total;
-};
-
 template <typename T>
 bool norm_vec(const la_norm_problem& p, int n, const void* const* ptr, const int64_t* stride) {
   const int64_t vec = 16 / int64_t(sizeof(T));
@@ -559,57 +551,81 @@ bool norm_vec(const la_norm_problem& p, int n, const void* const* ptr, const int
   return true;
 }
 
-// Per-thread elements are bounded by the registers (16 in the backward pass, which holds the row,
-// its weight and two sums for each; 128 bytes' worth of packs in the forward pass).
-int backward_wpr(int64_t cols, int64_t vec) {
-  const int64_t warp = vec == 1 ? 8 : 16;  // elements per lane of a row that one warp holds
-  if (cols <= 32 * warp) return 1;
-  return cols <= 4096 ? 8 : 16;
+// Blocks per group (in the backward pass also slots of dweight and dbias): enough to fill the
+// machine, each with at least 8 steps over its rows.
+int norm_parts(const la_norm_problem& p, int sm, int per_sm) {
+  const int64_t parts = int64_t(sm) * per_sm / std::max<int64_t>(p.groups, 1);
+  return static_cast<int>(std::max<int64_t>(1, std::min(parts, ceil_div(p.rows / p.groups, 8))));
+}
+// Backward blocks that share an SM, by the registers of 16 elements a thread (a row, its weight and
+// two sums for each): 2 blocks of 256 threads at 4096 columns, and in proportion.
+int norm_backward_per_sm(int64_t cols) {
+  return cols <= 512 ? 8 : cols <= 1024 ? 6 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1;
 }
 
-NormPlan norm_plan(const la_norm_problem& p, int sm) {
-  NormPlan n;
-  // The slots do not depend on the rows' alignment: both paths fit.
-  const int64_t blocks = int64_t(sm) * 4;
-  int64_t parts = blocks / std::max<int64_t>(p.groups, 1);
-  const int64_t per_group = p.rows / p.groups;
-  n.wpr = 0;
-  n.parts = static_cast<int>(std::max<int64_t>(1, std::min(parts, ceil_div(per_group, 8))));
-  n.total = n.parts > 1 ? align256(2 * size_t(p.groups) * size_t(n.parts) * size_t(p.cols) * 4) : 0;
-  return n;
+// The slots' bytes (they do not depend on the rows' alignment: every path fits).
+size_t norm_slots(const la_norm_problem& p, int sm) {
+  const int parts = norm_parts(p, sm, norm_backward_per_sm(p.cols));
+  return parts > 1 ? align256(2 * size_t(p.groups) * size_t(parts) * size_t(p.cols) * 4) : 0;
 }
 
-template <typename T, int VEC, int NV, int WPR>
-int norm_forward(const la::ln::Args& a, const void* x, const float* w, const float* b, void* y, float* mean, float* rstd,
-                 cudaStream_t st) {
-  constexpr int THREADS = 32 * (WPR == 1 ? la::ln::WARP_ROWS : WPR);
-  const int64_t grid = WPR == 1 ? ceil_div(a.rows, la::ln::WARP_ROWS) : a.rows;
-  return launch_k(la::ln::forward_kernel<T, VEC, NV, WPR>, dim3(unsigned(grid)), THREADS, 0, st, false, a,
-                  static_cast<const T*>(x), w, b, static_cast<T*>(y), mean, rstd);
+// Ring stages: what lets as many blocks share an SM as there are, at least 1 and at most 4.
+int norm_stages(size_t stage_bytes, int per_sm) {
+  const size_t budget = (size_t(220) << 10) / size_t(per_sm);
+  return static_cast<int>(std::max<size_t>(1, std::min<size_t>(4, budget / stage_bytes)));
+}
+
+struct NormForward {
+  const void* x;
+  const float *w, *b;
+  void* y;
+  float *mean, *rstd;
+};
+
+template <typename T, int VEC, int NV, int LPR, int U>
+int norm_forward_short(const la_norm_problem&, const la::ln::Args& a, int, const NormForward& f, cudaStream_t st) {
+  const int64_t rows = la::ln::WARPS * U * (32 / LPR);
+  return launch_k(la::ln::forward_short<T, VEC, NV, LPR, U>, dim3(unsigned(ceil_div(a.rows, rows))), 32 * la::ln::WARPS, 0, st,
+                  false, a, static_cast<const T*>(f.x), f.w, f.b, static_cast<T*>(f.y), f.mean, f.rstd);
+}
+
+template <typename T, int VEC, int NV, int WPR, bool RING>
+int norm_forward_long(const la_norm_problem& p, const la::ln::Args& a, int sm, const NormForward& f, cudaStream_t st) {
+  auto kern = la::ln::forward_long<T, VEC, NV, WPR, RING>;
+  const int per_sm = WPR <= 8 ? 4 : 2;
+  const int parts = norm_parts(p, sm, per_sm);
+  const size_t row = size_t(p.cols) * sizeof(T);
+  const int stages = RING ? norm_stages(row, per_sm) : 0;
+  if (RING && set_smem(kern, stages * row)) return LA_ERR_CUDA;
+  return launch_k(kern, dim3(unsigned(p.groups * parts)), 32 * WPR, stages * row, st, false, a, parts, stages,
+                  static_cast<const T*>(f.x), f.w, f.b, static_cast<T*>(f.y), f.mean, f.rstd);
 }
 
 template <typename T>
-int norm_forward_any(const la_norm_problem& p, const la::ln::Args& a, const void* x, const float* w, const float* b, void* y,
-                     float* mean, float* rstd, cudaStream_t st) {
-  const void* ptr[2] = {x, y};
+int norm_forward_any(const la_norm_problem& p, const la::ln::Args& a, int sm, const NormForward& f, cudaStream_t st) {
+  const void* ptr[2] = {f.x, f.y};
   const int64_t str[2] = {p.sx, p.sy};
   const int64_t c = p.cols;
   if (norm_vec<T>(p, 2, ptr, str)) {
     constexpr int V = 16 / int(sizeof(T));
-    if (c <= 32 * V) return norm_forward<T, V, 1, 1>(a, x, w, b, y, mean, rstd, st);
-    if (c <= 64 * V) return norm_forward<T, V, 2, 1>(a, x, w, b, y, mean, rstd, st);
-    if (c <= 128 * V) return norm_forward<T, V, 4, 1>(a, x, w, b, y, mean, rstd, st);
-    if (c <= 256 * V) return norm_forward<T, V, 8, 1>(a, x, w, b, y, mean, rstd, st);
-    if (c <= 512 * V) return norm_forward<T, V, 16, 1>(a, x, w, b, y, mean, rstd, st);
-    if (c <= 1024 * V) return norm_forward<T, V, 4, 8>(a, x, w, b, y, mean, rstd, st);
-    if (c <= 2048 * V) return norm_forward<T, V, 4, 16>(a, x, w, b, y, mean, rstd, st);
-    return norm_forward<T, V, 8, 16>(a, x, w, b, y, mean, rstd, st);
+    if (c <= 8 * V) return norm_forward_short<T, V, 1, 8, 4>(p, a, sm, f, st);
+    if (c <= 16 * V) return norm_forward_short<T, V, 1, 16, 4>(p, a, sm, f, st);
+    if (c <= 32 * V) return norm_forward_short<T, V, 1, 32, 4>(p, a, sm, f, st);
+    if (c <= 64 * V) return norm_forward_short<T, V, 2, 32, 2>(p, a, sm, f, st);
+    if (c <= 128 * V) return norm_forward_short<T, V, 4, 32, 1>(p, a, sm, f, st);
+    if (c <= 256 * V) return norm_forward_short<T, V, 8, 32, 1>(p, a, sm, f, st);
+    if (c <= 512 * V) return norm_forward_short<T, V, 16, 32, 1>(p, a, sm, f, st);
+    if (c <= 1024 * V) return norm_forward_long<T, V, 2, 16, true>(p, a, sm, f, st);
+    if (c <= 2048 * V) return norm_forward_long<T, V, 4, 16, true>(p, a, sm, f, st);
+    return norm_forward_long<T, V, 8, 16, true>(p, a, sm, f, st);
   }
-  if (c <= 32 * 4) return norm_forward<T, 1, 4, 1>(a, x, w, b, y, mean, rstd, st);
-  if (c <= 32 * 16) return norm_forward<T, 1, 16, 1>(a, x, w, b, y, mean, rstd, st);
-  if (c <= 256 * 8) return norm_forward<T, 1, 8, 8>(a, x, w, b, y, mean, rstd, st);
-  if (c <= 512 * 16) return norm_forward<T, 1, 16, 16>(a, x, w, b, y, mean, rstd, st);
-  return norm_forward<T, 1, 32, 16>(a, x, w, b, y, mean, rstd, st);
+  if (c <= 8 * 4) return norm_forward_short<T, 1, 4, 8, 2>(p, a, sm, f, st);
+  if (c <= 32 * 4) return norm_forward_short<T, 1, 4, 32, 2>(p, a, sm, f, st);
+  if (c <= 32 * 16) return norm_forward_short<T, 1, 16, 32, 1>(p, a, sm, f, st);
+  if (c <= 32 * 32) return norm_forward_short<T, 1, 32, 32, 1>(p, a, sm, f, st);
+  if (c <= 256 * 16) return norm_forward_long<T, 1, 16, 8, false>(p, a, sm, f, st);
+  if (c <= 512 * 16) return norm_forward_long<T, 1, 16, 16, false>(p, a, sm, f, st);
+  return norm_forward_long<T, 1, 32, 16, false>(p, a, sm, f, st);
 }
 
 struct NormGrads {
@@ -619,13 +635,23 @@ struct NormGrads {
   float *dw, *db;  // or the slots
 };
 
-template <typename T, int VEC, int NV, int WPR>
-int norm_backward(const la::ln::Args& a, int64_t groups, int parts, const NormGrads& g, cudaStream_t st) {
-  constexpr int THREADS = 32 * (WPR == 1 ? la::ln::WARP_ROWS : WPR);
-  const size_t smem = WPR == 1 && (g.dw || g.db) ? size_t(la::ln::WARP_ROWS) * size_t(a.cols) * 4 : 0;
-  return launch_k(la::ln::backward_kernel<T, VEC, NV, WPR>, dim3(unsigned(groups * parts)), THREADS, smem, st, false, a,
-                  parts, static_cast<const T*>(g.x), static_cast<const T*>(g.dy), g.w, g.mean, g.rstd,
+template <typename T, int VEC, int NV, int LPR, int U>
+int norm_backward_short(const la::ln::Args& a, int64_t groups, int parts, const NormGrads& g, cudaStream_t st) {
+  const size_t smem = g.dw || g.db ? size_t(la::ln::WARPS) * (32 / LPR) * size_t(a.cols) * 4 : 0;
+  return launch_k(la::ln::backward_short<T, VEC, NV, LPR, U>, dim3(unsigned(groups * parts)), 32 * la::ln::WARPS, smem, st,
+                  false, a, parts, static_cast<const T*>(g.x), static_cast<const T*>(g.dy), g.w, g.mean, g.rstd,
                   static_cast<T*>(g.dx), g.dw, g.db);
+}
+
+template <typename T, int VEC, int NV, int WPR, bool RING>
+int norm_backward_long(const la::ln::Args& a, int64_t groups, int parts, const NormGrads& g, cudaStream_t st) {
+  auto kern = la::ln::backward_long<T, VEC, NV, WPR, RING>;
+  const size_t stage = 2 * size_t(a.cols) * sizeof(T);
+  const int stages = RING ? norm_stages(stage, norm_backward_per_sm(a.cols)) : 0;
+  if (RING && set_smem(kern, stages * stage)) return LA_ERR_CUDA;
+  return launch_k(kern, dim3(unsigned(groups * parts)), 32 * WPR, stages * stage, st, false, a, parts, stages,
+                  static_cast<const T*>(g.x), static_cast<const T*>(g.dy), g.w, g.mean, g.rstd, static_cast<T*>(g.dx), g.dw,
+                  g.db);
 }
 
 template <typename T>
@@ -635,18 +661,22 @@ int norm_backward_any(const la_norm_problem& p, const la::ln::Args& a, int parts
   const int64_t c = p.cols, n = p.groups;
   if (norm_vec<T>(p, 3, ptr, str)) {
     constexpr int V = 16 / int(sizeof(T));
-    if (c <= 32 * V) return norm_backward<T, V, 1, 1>(a, n, parts, g, st);
-    if (c <= 512) return norm_backward<T, V, 16 / V, 1>(a, n, parts, g, st);
-    if (c <= 2048) return norm_backward<T, V, 8 / V, 8>(a, n, parts, g, st);
-    if (c <= 4096) return norm_backward<T, V, 16 / V, 8>(a, n, parts, g, st);
-    if (c <= 8192) return norm_backward<T, V, 16 / V, 16>(a, n, parts, g, st);
-    return norm_backward<T, V, 32 / V, 16>(a, n, parts, g, st);
+    if (c <= 8 * V) return norm_backward_short<T, V, 1, 8, 2>(a, n, parts, g, st);
+    if (c <= 16 * V) return norm_backward_short<T, V, 1, 16, 2>(a, n, parts, g, st);
+    if (c <= 32 * V) return norm_backward_short<T, V, 1, 32, 2>(a, n, parts, g, st);
+    if (c <= 512) return norm_backward_short<T, V, 16 / V, 32, 1>(a, n, parts, g, st);
+    if (c <= 1024) return norm_backward_long<T, V, 16 / V, 2, true>(a, n, parts, g, st);
+    if (c <= 2048) return norm_backward_long<T, V, 16 / V, 4, true>(a, n, parts, g, st);
+    if (c <= 4096) return norm_backward_long<T, V, 16 / V, 8, true>(a, n, parts, g, st);
+    if (c <= 8192) return norm_backward_long<T, V, 16 / V, 16, true>(a, n, parts, g, st);
+    return norm_backward_long<T, V, 32 / V, 16, true>(a, n, parts, g, st);
   }
-  if (c <= 32 * 8) return norm_backward<T, 1, 8, 1>(a, n, parts, g, st);
-  if (c <= 256 * 8) return norm_backward<T, 1, 8, 8>(a, n, parts, g, st);
-  if (c <= 256 * 16) return norm_backward<T, 1, 16, 8>(a, n, parts, g, st);
-  if (c <= 512 * 16) return norm_backward<T, 1, 16, 16>(a, n, parts, g, st);
-  return norm_backward<T, 1, 32, 16>(a, n, parts, g, st);
+  if (c <= 8 * 4) return norm_backward_short<T, 1, 4, 8, 1>(a, n, parts, g, st);
+  if (c <= 32 * 8) return norm_backward_short<T, 1, 8, 32, 1>(a, n, parts, g, st);
+  if (c <= 256 * 8) return norm_backward_long<T, 1, 8, 8, false>(a, n, parts, g, st);
+  if (c <= 256 * 16) return norm_backward_long<T, 1, 16, 8, false>(a, n, parts, g, st);
+  if (c <= 512 * 16) return norm_backward_long<T, 1, 16, 16, false>(a, n, parts, g, st);
+  return norm_backward_long<T, 1, 32, 16, false>(a, n, parts, g, st);
 }
 
 la::ln::Args norm_args(const la_norm_problem& p) {
@@ -906,7 +936,7 @@ int la_cross_backward(const la_cross_problem* p, const void* Q, const void* K, c
 
 size_t la_layernorm_workspace_bytes_for(const la_norm_problem* p, int sm_count) {
   if (validate(p, false) != LA_OK || sm_count <= 0) return 0;
-  return std::max<size_t>(norm_plan(*p, sm_count).total, 16);
+  return std::max<size_t>(norm_slots(*p, sm_count), 16);
 }
 
 size_t la_layernorm_workspace_bytes(const la_norm_problem* p) {
@@ -926,9 +956,11 @@ int la_layernorm_forward(const la_norm_problem* p, const void* x, const float* w
   if (!aligned16(weight) || !aligned16(bias) || !aligned16(mean) || !aligned16(rstd)) return LA_ERR_ALIGN;
   if (has && !norm_alias_ok(*p, x, p->sx, y, p->sy)) return LA_ERR_SHAPE;
   if (has) {
+    int sm = 0;
+    if ((rc = current_sm_count(&sm))) return rc;
     const la::ln::Args a = norm_args(*p);
-    rc = p->dtype == LA_BF16 ? norm_forward_any<__nv_bfloat16>(*p, a, x, weight, bias, y, mean, rstd, stream)
-                             : norm_forward_any<float>(*p, a, x, weight, bias, y, mean, rstd, stream);
+    const NormForward f = {x, weight, bias, y, mean, rstd};
+    rc = p->dtype == LA_BF16 ? norm_forward_any<__nv_bfloat16>(*p, a, sm, f, stream) : norm_forward_any<float>(*p, a, sm, f, stream);
     if (rc) return rc;
   }
   g_last_launches = has ? 1 : 0;
@@ -950,9 +982,10 @@ int la_layernorm_backward(const la_norm_problem* p, const void* x, const void* d
   if (has && (!norm_alias_ok(*p, x, p->sx, dx, p->sdx) || !norm_alias_ok(*p, dy, p->sdy, dx, p->sdx))) return LA_ERR_SHAPE;
   int sm = 0;
   if ((rc = current_sm_count(&sm))) return rc;
-  const NormPlan n = norm_plan(*p, sm);
+  const size_t need_bytes = norm_slots(*p, sm);
+  const int parts = norm_parts(*p, sm, norm_backward_per_sm(p->cols));
   const bool grads = dweight || dbias;
-  if (grads && n.total > 0 && (!ws || ws_bytes < n.total)) return LA_ERR_WORKSPACE;
+  if (grads && need_bytes > 0 && (!ws || ws_bytes < need_bytes)) return LA_ERR_WORKSPACE;
   if (!aligned16(ws)) return LA_ERR_ALIGN;
   int nl = 0;
   if (!has) {
@@ -964,19 +997,19 @@ int la_layernorm_backward(const la_norm_problem* p, const void* x, const void* d
     return LA_OK;
   }
   const la::ln::Args a = norm_args(*p);
-  const bool slots = grads && n.parts > 1;
+  const bool slots = grads && parts > 1;
   float* s_dw = static_cast<float*>(ws);
-  float* s_db = s_dw + p->groups * int64_t(n.parts) * p->cols;
+  float* s_db = s_dw + p->groups * int64_t(parts) * p->cols;
   const NormGrads g = {x, dy, weight, mean, rstd, dx, slots ? (dweight ? s_dw : nullptr) : dweight,
                        slots ? (dbias ? s_db : nullptr) : dbias};
-  rc = p->dtype == LA_BF16 ? norm_backward_any<__nv_bfloat16>(*p, a, n.parts, g, stream)
-                           : norm_backward_any<float>(*p, a, n.parts, g, stream);
+  rc = p->dtype == LA_BF16 ? norm_backward_any<__nv_bfloat16>(*p, a, parts, g, stream)
+                           : norm_backward_any<float>(*p, a, parts, g, stream);
   if (rc) return rc;
   ++nl;
   if (slots) {
     const int64_t blocks = p->groups * ceil_div(p->cols, la::ln::RED_COLS);
     if (launch_k(la::ln::reduce_kernel, dim3(unsigned(blocks), 2), la::ln::RED_COLS * la::ln::RED_ROWS, 0, stream, true, p->cols,
-                 n.parts, s_dw, s_db, dweight, dbias))
+                 parts, s_dw, s_db, dweight, dbias))
       return LA_ERR_CUDA;
     ++nl;
   }

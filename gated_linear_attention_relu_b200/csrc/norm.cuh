@@ -4,11 +4,16 @@
 //   dx = rstd (a - mean(a) - xh mean(a xh)),  dw_g = sum dy xh,  db_g = sum dy.
 //
 // Both are bound by HBM: one read of x (and dy), one write of y (dx).  A row stays in registers
-// between its read and its write, so the variance is the exact two-pass one.  A row belongs to one
-// warp where it fits (no barrier), else to a block.  In the backward pass a thread owns the same
-// columns of every row it sees, so its shares of dw and db stay in registers until the block has
-// walked its range of rows; blocks write them to their own slots, which a second kernel adds in
-// order (no atomics: the same bits every time).
+// between its read and its write, so the variance is the exact two-pass one.
+//   Short rows (up to 512 channels; forward: up to a warp's 16 packs a lane) belong to a part of a
+// warp, several rows at a time, without a barrier.
+//   Longer rows belong to a block that walks its range of a group's rows, with the weight in
+// registers; the rows to come are on their way to shared memory by bulk copies (a ring of STAGES
+// rows), since loads into registers left too few bytes in flight.
+//   Rows that are not 16-byte aligned take the same kernels' one-element form (without the ring).
+// In the backward pass a thread owns the same columns of every row it sees, so its shares of dw and
+// db stay in registers until the block has walked its rows; blocks write them to their own slots,
+// which a second kernel adds in order (no atomics: the same bits every time).
 #pragma once
 #include "common.cuh"
 #include "sm100.cuh"
@@ -35,6 +40,27 @@ __device__ __forceinline__ float as_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void put(float& d, float x) { d = x; }
 __device__ __forceinline__ void put(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
 
+// A pack of a tensor that is read once: past the L1 cache, which the weights have.
+template <typename P>
+__device__ __forceinline__ P load_pack(const void* p) {
+  if constexpr (sizeof(P) == 16) {
+    uint4 u;
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p) : "memory");
+    return *reinterpret_cast<P*>(&u);
+  } else {
+    return *static_cast<const P*>(p);
+  }
+}
+template <typename P>
+__device__ __forceinline__ void store_pack(void* p, const P& v) {
+  if constexpr (sizeof(P) == 16) {
+    const uint4& u = *reinterpret_cast<const uint4*>(&v);
+    *reinterpret_cast<uint4*>(p) = u;
+  } else {
+    *static_cast<P*>(p) = v;
+  }
+}
+
 template <int VEC>
 __device__ __forceinline__ void load_w(const float* __restrict__ w, float (&o)[VEC]) {
   if constexpr (VEC % 4 == 0) {
@@ -55,17 +81,11 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the WPR warps of a row, in warp order (a row of one warp needs no shared memory).
-// `red` is used by one sum at a time: callers alternate between two buffers.
-template <int WPR>
-__device__ __forceinline__ float row_sum(float v, float* red) {
-  v = warp_sum(v);
-  if constexpr (WPR > 1) {
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) red[w] = v;
-    __syncthreads();
-    v = warp_sum(lane < WPR ? red[lane] : 0.f);
-  }
+// Sum over the LPR lanes that share a row.
+template <int LPR>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
@@ -75,91 +95,90 @@ struct Args {
   float eps, inv_cols;
 };
 
-constexpr int WARP_ROWS = 4;  // rows (warps) per block where a row belongs to one warp
+// ------------------------------------------------------------------------------- short rows
+constexpr int WARPS = 4;  // of a block
 
-// Element offset of pack i of this thread (may be >= cols: then the pack is absent; cols is a
-// multiple of VEC).
-template <int VEC, int WPR>
-__device__ __forceinline__ int col_of(int i) {
-  const int t = WPR == 1 ? int(threadIdx.x & 31) : int(threadIdx.x);
-  return (i * 32 * WPR + t) * VEC;
-}
-
-template <typename T, int VEC, int NV, int WPR>
-__global__ void __launch_bounds__(WPR == 1 ? 32 * WARP_ROWS : 32 * WPR)
-forward_kernel(const Args a, const T* x, const float* __restrict__ weight,
-               const float* __restrict__ bias, T* y, float* __restrict__ mean, float* __restrict__ rstd) {
-  __shared__ float red[2][32];
-  const int64_t row = WPR == 1 ? int64_t(blockIdx.x) * WARP_ROWS + (threadIdx.x >> 5) : int64_t(blockIdx.x);
-  if (row >= a.rows) return;  // (whole warps; a block of one row never leaves here)
-  const T* xr = x + row * a.sx;
-  Pack<T, VEC> p[NV];
+// LPR lanes hold a row of NV packs each; a warp takes U * 32 / LPR rows at a time.
+template <typename T, int VEC, int NV, int LPR, int U>
+__global__ void __launch_bounds__(32 * WARPS)
+forward_short(const Args a, const T* x, const float* __restrict__ weight, const float* __restrict__ bias, T* y,
+              float* __restrict__ mean, float* __restrict__ rstd) {
+  constexpr int RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, li = lane % LPR;
+  const int64_t row0 = (int64_t(blockIdx.x) * WARPS + (threadIdx.x >> 5)) * (U * RPW) + lane / LPR;
+  Pack<T, VEC> p[U][NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = col_of<VEC, WPR>(i);
-    if (c < a.cols) p[i] = *reinterpret_cast<const Pack<T, VEC>*>(xr + c);
-  }
-  float s = 0.f;
+  for (int u = 0; u < U; ++u)
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (col_of<VEC, WPR>(i) < a.cols) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) s += as_f(p[i].v[e]);
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * LPR + li) * VEC;
+      const int64_t row = row0 + u * RPW;
+      if (c < a.cols && row < a.rows) p[u][i] = load_pack<Pack<T, VEC>>(x + row * a.sx + c);
     }
-  const float mu = row_sum<WPR>(s, red[0]) * a.inv_cols;
-  s = 0.f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (col_of<VEC, WPR>(i) < a.cols) {
+  for (int u = 0; u < U; ++u) {
+    const int64_t row = row0 + u * RPW;
+    const bool in = row < a.rows;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (in && (i * LPR + li) * VEC < a.cols) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s += as_f(p[u][i].v[e]);
+      }
+    const float mu = lanes_sum<LPR>(s) * a.inv_cols;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (in && (i * LPR + li) * VEC < a.cols) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float d = as_f(p[u][i].v[e]) - mu;
+          s += d * d;
+        }
+      }
+    const float r = 1.f / sqrtf(lanes_sum<LPR>(s) * a.inv_cols + a.eps);
+    if (!in) continue;
+    if (mean && li == 0) {
+      mean[row] = mu;
+      rstd[row] = r;
+    }
+    const int64_t g = row / a.per_group * a.cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * LPR + li) * VEC;
+      if (c >= a.cols) continue;
+      float w[VEC], b[VEC];
+      if (weight) load_w<VEC>(weight + g + c, w);
+      if (bias) load_w<VEC>(bias + g + c, b);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float d = as_f(p[i].v[e]) - mu;
-        s += d * d;
+        float v = (as_f(p[u][i].v[e]) - mu) * r;
+        if (weight) v *= w[e];
+        if (bias) v += b[e];
+        put(p[u][i].v[e], v);
       }
+      store_pack(y + row * a.sy + c, p[u][i]);
     }
-  const float r = 1.f / sqrtf(row_sum<WPR>(s, red[1]) * a.inv_cols + a.eps);
-  if (mean && (WPR == 1 ? (threadIdx.x & 31) == 0 : threadIdx.x == 0)) {
-    mean[row] = mu;
-    rstd[row] = r;
-  }
-  const int64_t g = row / a.per_group * a.cols;
-  T* yr = y + row * a.sy;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = col_of<VEC, WPR>(i);
-    if (c >= a.cols) continue;
-    float w[VEC], b[VEC];
-    if (weight) load_w<VEC>(weight + g + c, w);
-    if (bias) load_w<VEC>(bias + g + c, b);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      float v = (as_f(p[i].v[e]) - mu) * r;
-      if (weight) v *= w[e];
-      if (bias) v += b[e];
-      put(p[i].v[e], v);
-    }
-    *reinterpret_cast<Pack<T, VEC>*>(yr + c) = p[i];
   }
 }
 
-// Block `part` of group g walks the group's rows part, part + parts, ... and leaves its sums in
-// slot g * parts + part of `slots` ([2][groups * parts][cols]: dw, db), or in dweight and dbias
-// themselves when parts is 1.
-template <typename T, int VEC, int NV, int WPR>
-__global__ void __launch_bounds__(32 * (WPR == 1 ? WARP_ROWS : WPR))
-backward_kernel(const Args a, int parts, const T* x, const T* dy, const float* __restrict__ weight,
-                const float* __restrict__ mean, const float* __restrict__ rstd, T* dx, float* dw_out, float* db_out) {
-  constexpr int STEP = WPR == 1 ? WARP_ROWS : 1;  // rows a block takes at a time
-  __shared__ float2 red[2][32];
-  extern __shared__ float cross[];  // rows of one warp each: the warps' sums, joined at the end
+// Block `part` of group g takes every parts-th step of the group's rows and leaves its sums in slot
+// g * parts + part of dw_out and db_out ([groups * parts][cols]).
+template <typename T, int VEC, int NV, int LPR, int U>
+__global__ void __launch_bounds__(32 * WARPS)
+backward_short(const Args a, int parts, const T* x, const T* dy, const float* __restrict__ weight,
+               const float* __restrict__ mean, const float* __restrict__ rstd, T* dx, float* dw_out, float* db_out) {
+  constexpr int RPW = 32 / LPR, STEP = WARPS * U * RPW;
+  extern __shared__ float cross[];  // [WARPS * RPW][cols]: the sums of the block's row slots, joined at the end
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane % LPR;
   const int64_t g = blockIdx.x / static_cast<uint32_t>(parts);
   const int part = static_cast<int>(blockIdx.x - g * parts);
   float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = col_of<VEC, WPR>(i);
+    const int c = (i * LPR + li) * VEC;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       w[i][e] = 1.f;
@@ -167,23 +186,258 @@ backward_kernel(const Args a, int parts, const T* x, const T* dy, const float* _
     }
     if (weight && c < a.cols) load_w<VEC>(weight + g * a.cols + c, w[i]);
   }
-  int buf = 0;
-  for (int64_t j = int64_t(part) * STEP + (WPR == 1 ? warp : 0); j < a.per_group; j += int64_t(parts) * STEP) {
-    const int64_t row = g * a.per_group + j;
-    Pack<T, VEC> px[NV], pd[NV];
+  for (int64_t j0 = int64_t(part) * STEP; j0 < a.per_group; j0 += int64_t(parts) * STEP) {
+    Pack<T, VEC> px[U][NV], pd[U][NV];
+    float mu[U], r[U];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = col_of<VEC, WPR>(i);
-      if (c < a.cols) {
-        px[i] = *reinterpret_cast<const Pack<T, VEC>*>(x + row * a.sx + c);
-        pd[i] = *reinterpret_cast<const Pack<T, VEC>*>(dy + row * a.sdy + c);
+    for (int u = 0; u < U; ++u) {
+      const int64_t j = j0 + (warp * U + u) * RPW + lane / LPR, row = g * a.per_group + j;
+      const bool in = j < a.per_group;
+      mu[u] = in ? mean[row] : 0.f;
+      r[u] = in ? rstd[row] : 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * LPR + li) * VEC;
+        if (in && c < a.cols) {
+          px[u][i] = load_pack<Pack<T, VEC>>(x + row * a.sx + c);
+          pd[u][i] = load_pack<Pack<T, VEC>>(dy + row * a.sdy + c);
+        }
       }
     }
-    const float mu = mean[row], r = rstd[row];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t j = j0 + (warp * U + u) * RPW + lane / LPR, row = g * a.per_group + j;
+      const bool in = j < a.per_group;
+      float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (in && (i * LPR + li) * VEC < a.cols) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float xh = (as_f(px[u][i].v[e]) - mu[u]) * r[u], d = as_f(pd[u][i].v[e]);
+            dw[i][e] += d * xh;
+            db[i][e] += d;
+            s1 += d * w[i][e];
+            s2 += d * w[i][e] * xh;
+          }
+        }
+      const float c1 = lanes_sum<LPR>(s1) * a.inv_cols, c2 = lanes_sum<LPR>(s2) * a.inv_cols;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * LPR + li) * VEC;
+        if (!in || c >= a.cols) continue;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float xh = (as_f(px[u][i].v[e]) - mu[u]) * r[u];
+          put(px[u][i].v[e], r[u] * (as_f(pd[u][i].v[e]) * w[i][e] - c1 - xh * c2));
+        }
+        store_pack(dx + row * a.sdx + c, px[u][i]);
+      }
+    }
+  }
+  const int64_t slot = int64_t(blockIdx.x) * a.cols;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float* out = k == 0 ? dw_out : db_out;
+    if (!out) continue;
+    // the block's row slots saw different rows of the same columns: join them in order
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * LPR + li) * VEC;
+      if (c < a.cols)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          cross[(warp * RPW + lane / LPR) * a.cols + c + e] = k == 0 ? dw[i][e] : db[i][e];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.cols; c += 32 * WARPS) {
+      float v = cross[c];
+#pragma unroll
+      for (int q = 1; q < WARPS * RPW; ++q) v += cross[q * a.cols + c];
+      out[slot + c] = v;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------- long rows
+// A block of WPR warps per row.  RING: rows come through a ring of `stages` in shared memory (16-byte
+// packs), else straight from global memory.
+struct Ring {
+  uint64_t full[4];
+  int abort_flag;
+};
+
+// The sum of two values over the block's warps, in warp order; one barrier, and the next call's may
+// follow at once (callers alternate the buffers).
+template <int WPR>
+__device__ __forceinline__ float2 block_sum2(float a, float b, float2* red) {
+  a = lanes_sum<32>(a);
+  b = lanes_sum<32>(b);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) red[warp] = make_float2(a, b);
+  __syncthreads();
+  const float2 t = lane < WPR ? red[lane] : make_float2(0.f, 0.f);
+  return make_float2(lanes_sum<32>(t.x), lanes_sum<32>(t.y));
+}
+
+template <typename T, int VEC, int NV, int WPR, bool RING>
+__global__ void __launch_bounds__(32 * WPR)
+forward_long(const Args a, int parts, int stages, const T* x, const float* __restrict__ weight,
+             const float* __restrict__ bias, T* y, float* __restrict__ mean, float* __restrict__ rstd) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float2 red[2][32];
+  __shared__ Ring rg;
+  const int64_t g = blockIdx.x / static_cast<uint32_t>(parts);
+  const int part = static_cast<int>(blockIdx.x - g * parts);
+  const uint32_t bytes = static_cast<uint32_t>(a.cols) * sizeof(T);
+  const int64_t row0 = g * a.per_group;
+  auto fetch = [&](int64_t j, int s) {
+    if (j < a.per_group) {
+      mbar_arrive_expect_tx(&rg.full[s], bytes);
+      bulk_load(ring + s * bytes, x + (row0 + j) * a.sx, bytes, &rg.full[s]);
+    }
+  };
+  if (RING && threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&rg.full[s], 1);
+    rg.abort_flag = 0;
+    fence_mbar_init();
+    for (int s = 0; s < stages; ++s) fetch(part + int64_t(s) * parts, s);
+  }
+  __syncthreads();
+  float w[NV][VEC], b[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * 32 * WPR + threadIdx.x) * VEC;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      w[i][e] = 1.f;
+      b[i][e] = 0.f;
+    }
+    if (weight && c < a.cols) load_w<VEC>(weight + g * a.cols + c, w[i]);
+    if (bias && c < a.cols) load_w<VEC>(bias + g * a.cols + c, b[i]);
+  }
+  int s = 0;
+  uint32_t ph = 0;
+  for (int64_t j = part; j < a.per_group; j += parts) {
+    const int64_t row = row0 + j;
+    Pack<T, VEC> p[NV];
+    if constexpr (RING) mbar_wait_near(&rg.full[s], ph, &rg.abort_flag);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * 32 * WPR + threadIdx.x) * VEC;
+      if (c < a.cols)
+        p[i] = RING ? *reinterpret_cast<const Pack<T, VEC>*>(ring + s * bytes + c * sizeof(T))
+                    : load_pack<Pack<T, VEC>>(x + row * a.sx + c);
+    }
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((i * 32 * WPR + int(threadIdx.x)) * VEC < a.cols) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v += as_f(p[i].v[e]);
+      }
+    const float mu = block_sum2<WPR>(v, 0.f, red[0]).x * a.inv_cols;
+    if constexpr (RING) {  // every thread has its part of the row: the stage can take another one
+      if (threadIdx.x == 0) fetch(j + int64_t(stages) * parts, s);
+      if (++s == stages) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((i * 32 * WPR + int(threadIdx.x)) * VEC < a.cols) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float d = as_f(p[i].v[e]) - mu;
+          v += d * d;
+        }
+      }
+    const float r = 1.f / sqrtf(block_sum2<WPR>(v, 0.f, red[1]).x * a.inv_cols + a.eps);
+    if (mean && threadIdx.x == 0) {
+      mean[row] = mu;
+      rstd[row] = r;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * 32 * WPR + threadIdx.x) * VEC;
+      if (c >= a.cols) continue;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float t = (as_f(p[i].v[e]) - mu) * r;
+        if (weight) t *= w[i][e];
+        if (bias) t += b[i][e];
+        put(p[i].v[e], t);
+      }
+      store_pack(y + row * a.sy + c, p[i]);
+    }
+  }
+}
+
+template <typename T, int VEC, int NV, int WPR, bool RING>
+__global__ void __launch_bounds__(32 * WPR)
+backward_long(const Args a, int parts, int stages, const T* x, const T* dy, const float* __restrict__ weight,
+              const float* __restrict__ mean, const float* __restrict__ rstd, T* dx, float* dw_out, float* db_out) {
+  extern __shared__ __align__(128) uint8_t ring[];  // stages of a row of x, then of dy
+  __shared__ float2 red[2][32];
+  __shared__ Ring rg;
+  pdl_trigger();
+  const int64_t g = blockIdx.x / static_cast<uint32_t>(parts);
+  const int part = static_cast<int>(blockIdx.x - g * parts);
+  const uint32_t bytes = static_cast<uint32_t>(a.cols) * sizeof(T);
+  const int64_t row0 = g * a.per_group;
+  auto fetch = [&](int64_t j, int s) {
+    if (j < a.per_group) {
+      mbar_arrive_expect_tx(&rg.full[s], 2 * bytes);
+      bulk_load(ring + (2 * s) * bytes, x + (row0 + j) * a.sx, bytes, &rg.full[s]);
+      bulk_load(ring + (2 * s + 1) * bytes, dy + (row0 + j) * a.sdy, bytes, &rg.full[s]);
+    }
+  };
+  if (RING && threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&rg.full[s], 1);
+    rg.abort_flag = 0;
+    fence_mbar_init();
+    for (int s = 0; s < stages; ++s) fetch(part + int64_t(s) * parts, s);
+  }
+  __syncthreads();
+  float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * 32 * WPR + threadIdx.x) * VEC;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      w[i][e] = 1.f;
+      dw[i][e] = db[i][e] = 0.f;
+    }
+    if (weight && c < a.cols) load_w<VEC>(weight + g * a.cols + c, w[i]);
+  }
+  int s = 0, buf = 0;
+  uint32_t ph = 0;
+  float mu = 0.f, r = 0.f;
+  if (part < a.per_group) {
+    mu = mean[row0 + part];
+    r = rstd[row0 + part];
+  }
+  for (int64_t j = part; j < a.per_group; j += parts) {
+    const int64_t row = row0 + j;
+    Pack<T, VEC> px[NV], pd[NV];
+    if constexpr (RING) mbar_wait_near(&rg.full[s], ph, &rg.abort_flag);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * 32 * WPR + threadIdx.x) * VEC;
+      if (c < a.cols) {
+        px[i] = RING ? *reinterpret_cast<const Pack<T, VEC>*>(ring + (2 * s) * bytes + c * sizeof(T))
+                     : load_pack<Pack<T, VEC>>(x + row * a.sx + c);
+        pd[i] = RING ? *reinterpret_cast<const Pack<T, VEC>*>(ring + (2 * s + 1) * bytes + c * sizeof(T))
+                     : load_pack<Pack<T, VEC>>(dy + row * a.sdy + c);
+      }
+    }
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (col_of<VEC, WPR>(i) < a.cols) {
+      if ((i * 32 * WPR + int(threadIdx.x)) * VEC < a.cols) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const float xh = (as_f(px[i].v[e]) - mu) * r, d = as_f(pd[i].v[e]);
@@ -193,60 +447,42 @@ backward_kernel(const Args a, int parts, const T* x, const T* dy, const float* _
           s2 += d * w[i][e] * xh;
         }
       }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if constexpr (WPR > 1) {
-      if (lane == 0) red[buf][warp] = make_float2(s1, s2);
-      __syncthreads();
-      const float2 t = lane < WPR ? red[buf][lane] : make_float2(0.f, 0.f);
-      s1 = warp_sum(t.x);
-      s2 = warp_sum(t.y);
-      buf ^= 1;  // the next row's sums go to the other buffer: one barrier per row is enough
+    const float2 c12 = block_sum2<WPR>(s1, s2, red[buf]);
+    buf ^= 1;
+    const float mu0 = mu, r0 = r;
+    if (j + parts < a.per_group) {  // the next row's
+      mu = mean[row + parts];
+      r = rstd[row + parts];
     }
-    const float c1 = s1 * a.inv_cols, c2 = s2 * a.inv_cols;
+    if constexpr (RING) {
+      if (threadIdx.x == 0) fetch(j + int64_t(stages) * parts, s);
+      if (++s == stages) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+    const float c1 = c12.x * a.inv_cols, c2 = c12.y * a.inv_cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = col_of<VEC, WPR>(i);
+      const int c = (i * 32 * WPR + threadIdx.x) * VEC;
       if (c >= a.cols) continue;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float xh = (as_f(px[i].v[e]) - mu) * r;
-        put(px[i].v[e], r * (as_f(pd[i].v[e]) * w[i][e] - c1 - xh * c2));
+        const float xh = (as_f(px[i].v[e]) - mu0) * r0;
+        put(px[i].v[e], r0 * (as_f(pd[i].v[e]) * w[i][e] - c1 - xh * c2));
       }
-      *reinterpret_cast<Pack<T, VEC>*>(dx + row * a.sdx + c) = px[i];
+      store_pack(dx + row * a.sdx + c, px[i]);
     }
   }
-  if (!dw_out && !db_out) return;
   const int64_t slot = int64_t(blockIdx.x) * a.cols;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    float* out = k == 0 ? dw_out : db_out;
-    if (!out) continue;
-    if constexpr (WPR == 1) {
-      // the block's warps saw different rows of the same columns: join them in warp order
-      __syncthreads();
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * 32 * WPR + threadIdx.x) * VEC;
+    if (c >= a.cols) continue;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = col_of<VEC, WPR>(i);
-        if (c < a.cols)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) cross[warp * a.cols + c + e] = k == 0 ? dw[i][e] : db[i][e];
-      }
-      __syncthreads();
-      for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
-        float v = cross[c];
-#pragma unroll
-        for (int q = 1; q < WARP_ROWS; ++q) v += cross[q * a.cols + c];
-        out[slot + c] = v;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = col_of<VEC, WPR>(i);
-        if (c < a.cols)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) out[slot + c + e] = k == 0 ? dw[i][e] : db[i][e];
-      }
+    for (int e = 0; e < VEC; ++e) {
+      if (dw_out) dw_out[slot + c + e] = dw[i][e];
+      if (db_out) db_out[slot + c + e] = db[i][e];
     }
   }
 }
