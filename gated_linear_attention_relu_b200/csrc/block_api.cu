@@ -692,7 +692,7 @@ la::ln::Args norm_args(const la_norm_problem& p) {
 
 // ------------------------------------------------------------------------------- gradient clipping
 constexpr int kClipCap = 1024;           // tensors per launch (the list rides in 32 KB of parameters)
-constexpr int kClipBlocksPerSm = 4;
+constexpr int kClipBlocksPerSm = 8;
 
 int64_t clip_tables(int64_t count) { return std::max<int64_t>(1, ceil_div(count, kClipCap)); }
 
