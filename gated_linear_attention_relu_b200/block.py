@@ -69,6 +69,19 @@ def _lib():
     return lib
 
 
+@functools.cache
+def _lists():
+    """The CPython helper that reads a list of tensors (csrc/lists.cpp), built if it is missing."""
+    import torch  # noqa: F401  (the helper links against it)
+
+    from . import build
+
+    build.build_lists()
+    from . import _lists as helper
+
+    return helper
+
+
 def _torch_dtype(name: str):
     import torch
 
@@ -120,11 +133,12 @@ class _On:
             if stream.device != device:
                 raise ValueError(f"stream: on {stream.device}, the tensors are on {device}")
             self.guard = torch.cuda.stream(stream)
+            self.handle = stream.cuda_stream
         else:
             if torch.cuda.current_device() != device.index:
                 self.guard = torch.cuda.device(device)
-            stream = torch.cuda.current_stream(device)
-        self.handle = stream.cuda_stream
+            # (torch.cuda.current_stream makes a stream object first, which takes longer than the call)
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
 
     def __enter__(self):
         if self.guard is not None:
@@ -398,59 +412,16 @@ def layernorm_backward(p: NormProblem, x, dy, mean, rstd, weight=None, dx=None, 
 
 
 # ------------------------------------------------------------------------------- gradient clipping
-def _grad_fields(tensors, what):
-    """(pointers, element counts, la_dtypes, device index) of a list of contiguous CUDA tensors.
-    One pass in C per property: lists have hundreds of tensors, and a call may be short."""
-    import torch
-
-    T = torch.Tensor
-    kinds = {torch.bfloat16: LA_BF16, torch.float32: LA_F32}
-    types = [kinds.get(t.dtype) for t in tensors]
-    if None in types:
-        i = types.index(None)
-        raise ValueError(f"{what} {i}: {tensors[i].dtype}, expected torch.bfloat16 or torch.float32")
-    devices = list(map(T.get_device, tensors))
-    if min(devices) != max(devices) or devices[0] < 0:
-        i = next(i for i, d in enumerate(devices) if d != devices[0] or d < 0)
-        raise ValueError(f"{what} {i}: on {tensors[i].device}, expected one CUDA device for all")
-    if not all(map(T.is_contiguous, tensors)):
-        i = [t.is_contiguous() for t in tensors].index(False)
-        raise ValueError(f"{what} {i}: must be contiguous")
-    return list(map(T.data_ptr, tensors)), list(map(T.numel, tensors)), types, devices[0]
-
-
-def _grad_list(tensors, out):
-    """The C array of a list (as a numpy array of the struct's layout), its length and its device."""
-    import numpy as np
-    import torch
-
-    n = len(tensors)
-    if out is not None and len(out) != n:
-        raise ValueError(f"out: {len(out)} tensors for {n} gradients")
-    arr = np.zeros(max(n, 1), dtype=[("in", "u8"), ("out", "u8"), ("numel", "i8"), ("dtype", "i4"), ("reserved", "i4")])
-    if n == 0:
-        return arr, 0, None
-    ptr, numel, types, dev = _grad_fields(tensors, "gradient")
-    arr["in"], arr["numel"], arr["dtype"] = ptr, numel, types
-    if out is None:
-        arr["out"] = arr["in"]
-    else:
-        optr, onumel, otypes, odev = _grad_fields(out, "out")
-        if onumel != numel or otypes != types or odev != dev:
-            i = next((i for i in range(n) if onumel[i] != numel[i] or otypes[i] != types[i]), 0)
-            raise ValueError(f"out {i}: must have its gradient's size, type and device")
-        arr["out"] = optr
-    return arr, n, torch.device("cuda", dev)
-
-
 def _norm_call(tensors, max_norm, out, norm, ws, stream):
     import torch
 
-    tensors = list(tensors)
-    arr, n, dev = _grad_list(tensors, None if out is None else list(out))
-    if dev is None:
-        dev = norm.device if norm is not None else torch.device("cuda", torch.cuda.current_device())
     lib = _lib()
+    arr, index = _lists().grad_list(list(tensors), None if out is None else list(out))
+    n = len(arr) // ctypes.sizeof(LaGrad)
+    if n:
+        dev = torch.device("cuda", index)
+    else:
+        dev = norm.device if norm is not None else torch.device("cuda", torch.cuda.current_device())
     with _On(dev, stream) as st:
         if norm is None:
             norm = torch.empty((), dtype=torch.float32, device=dev)
@@ -458,9 +429,9 @@ def _norm_call(tensors, max_norm, out, norm, ws, stream):
             raise ValueError(f"norm: one fp32 element on {dev} is expected")
         ws, nbytes = _workspace(ws, dev, lib.la_clip_workspace_bytes, n)
         if max_norm is None:
-            rc = lib.la_grad_norm(arr.ctypes.data, n, norm.data_ptr(), ws.data_ptr(), nbytes, st)
+            rc = lib.la_grad_norm(arr, n, norm.data_ptr(), ws.data_ptr(), nbytes, st)
         else:
-            rc = lib.la_clip_grad_norm(arr.ctypes.data, n, float(max_norm), norm.data_ptr(), ws.data_ptr(), nbytes, st)
+            rc = lib.la_clip_grad_norm(arr, n, float(max_norm), norm.data_ptr(), ws.data_ptr(), nbytes, st)
     if rc:
         raise LaError(rc, "la_grad_norm" if max_norm is None else "la_clip_grad_norm")
     return norm

@@ -10,6 +10,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblinattn.so")
 SOURCES = [os.path.join(CSRC, "la_api.cu"), os.path.join(CSRC, "block_api.cu")]
+LISTS = os.path.join(HERE, "_lists.so")
+LISTS_SOURCE = os.path.join(CSRC, "lists.cpp")
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
     os.path.join(ROOT, "include", "la.h")]
 
@@ -49,7 +51,31 @@ def up_to_date(out: str = LIB) -> bool:
     return all(os.path.getmtime(f) <= t for f in DEPS)
 
 
+def build_lists(force: bool = False, verbose: bool = False) -> str:
+    """Builds the CPython helper that reads lists of torch tensors, ``_lists.so``."""
+    if not force and os.path.exists(LISTS) and os.path.getmtime(LISTS_SOURCE) <= os.path.getmtime(LISTS):
+        return LISTS
+    import sysconfig
+
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include") if os.path.isabs(nvcc()) else "/usr/local/cuda/include"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", inc, "-I",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"], "-I",
+           os.path.join(ROOT, "include"), "-I", cuda, "-o", LISTS, LISTS_SOURCE, "-L",
+           os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed building _lists.so")
+    return LISTS
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_lists(force, verbose)
     if not force and up_to_date():
         return LIB
     cmd = command()
