@@ -183,8 +183,8 @@ CrossPlan cross_plan(const la_cross_problem& p, int sm) {
                : split_axis(c.q_tiles * group, p.B * p.Hkv * c.k_tiles, want, 2);
   const size_t D = size_t(p.d);
   size_t off = 0;
-  if (c.tc) {
-    const size_t rows = size_t(p.B) * size_t(p.Hkv) * size_t(c.pad) * D * 2;
+  if (c.keys > 0) {
+    const size_t rows = size_t(p.B) * size_t(p.Hkv) * size_t(c.pad) * D * elem_size(p.dtype);
     c.off_kc = 0;
     c.off_vc = align256(rows);
     c.off_count = align256(c.off_vc + rows);
@@ -200,7 +200,7 @@ CrossPlan cross_plan(const la_cross_problem& p, int sm) {
   c.off_delta = off;
   c.off_part = align256(c.off_delta + size_t(c.rows) * 4);
   const size_t part_dq = c.dq.parts > 1 ? size_t(c.dq.parts) * size_t(c.rows) * D * 4 : 0;
-  const size_t part_kv = c.dkv.parts > 1 || c.tc ? 2 * size_t(c.dkv.parts) * size_t(c.keys) * D * 4 : 0;
+  const size_t part_kv = c.keys > 0 ? 2 * size_t(c.dkv.parts) * size_t(c.keys) * D * 4 : 0;
   c.total = std::max(fwd, align256(c.off_part + std::max(part_dq, part_kv)));
   return c;
 }
@@ -228,16 +228,48 @@ void use(la::xs::Args& a, const Split& s) {
   a.tiles_per_split = s.per;
 }
 
+// Gathers the attended keys into the workspace (see gather_kernel).
+template <int D, typename T>
+int gather_keys(const la_cross_problem& p, const CrossPlan& c, const la::xs::Args& a, const void* K, const void* V, uint8_t* ws,
+                cudaStream_t st, int* nl) {
+  const int64_t grid = ceil_div(p.Nk, la::xs::G_KEYS) * p.Hkv * p.B;
+  if (launch_k(la::xs::gather_kernel<T, D / (16 / int(sizeof(T)))>, dim3(unsigned(grid)), la::xs::G_THREADS, 0, st, false, p.Hkv,
+               p.Nk, c.pad, static_cast<const T*>(K), static_cast<const T*>(V), a.k, a.v, a.kv_len, a.mask,
+               reinterpret_cast<T*>(ws + c.off_kc), reinterpret_cast<T*>(ws + c.off_vc),
+               reinterpret_cast<int32_t*>(ws + c.off_count), reinterpret_cast<int32_t*>(ws + c.off_place)))
+    return LA_ERR_CUDA;
+  ++*nl;
+  return LA_OK;
+}
+la::xs::Str gathered(const la_cross_problem& p, const CrossPlan& c) { return {p.Hkv * c.pad * p.d, c.pad * p.d, p.d}; }
+
+// With a mask, the CUDA-core kernels walk the gathered keys: what is left out costs nothing then, and
+// a mask's holes are spread over all tiles.  (Lengths alone end the walk.)
+template <int D, typename T>
+int gather_masked(const la_cross_problem& p, const CrossPlan& c, la::xs::Args* a, const void** K, const void** V, uint8_t* ws,
+                  cudaStream_t st, int* nl) {
+  if (!a->mask || c.keys == 0) return LA_OK;
+  if (const int rc = gather_keys<D, T>(p, c, *a, *K, *V, ws, st, nl)) return rc;
+  *K = ws + c.off_kc;
+  *V = ws + c.off_vc;
+  a->k = a->v = gathered(p, c);
+  a->kv_len = reinterpret_cast<const int32_t*>(ws + c.off_count);
+  a->mask = nullptr;
+  return LA_OK;
+}
+
 template <int D, typename T>
 int cross_forward_simt(const la_cross_problem& p, const CrossPlan& c, la::xs::Args a, const void* Q, const void* K,
                        const void* V, void* O, float* lse, uint8_t* ws, cudaStream_t st, int* nl) {
+  const int before = *nl;
+  if (const int rc = gather_masked<D, T>(p, c, &a, &K, &V, ws, st, nl)) return rc;
   use(a, c.fwd);
   float* part_o = reinterpret_cast<float*>(ws + c.off_o);
   float2* part_ml = reinterpret_cast<float2*>(ws + c.off_ml);
   const size_t smem = la::xs::fwd_smem<D>();
   if (set_smem(la::xs::forward_kernel<D, T>, smem)) return LA_ERR_CUDA;
   if (launch_k(la::xs::forward_kernel<D, T>, dim3(unsigned(c.q_tiles * c.fwd.parts * p.B * p.H)), la::xs::THREADS, smem, st,
-               false, a, static_cast<const T*>(Q), static_cast<const T*>(K), static_cast<const T*>(V),
+               *nl > before, a, static_cast<const T*>(Q), static_cast<const T*>(K), static_cast<const T*>(V),
                static_cast<T*>(O), lse, part_o, part_ml))
     return LA_ERR_CUDA;
   ++*nl;
@@ -256,12 +288,14 @@ int cross_backward_simt(const la_cross_problem& p, const CrossPlan& c, la::xs::A
   float* delta = reinterpret_cast<float*>(ws + c.off_delta);
   float* part = reinterpret_cast<float*>(ws + c.off_part);
   const size_t smem = la::xs::bwd_smem<D>();
+  const bool masked = a.mask != nullptr && c.keys > 0;
+  if (const int rc = gather_masked<D, T>(p, c, &a, &K, &V, ws, st, nl)) return rc;
   const T *q = static_cast<const T*>(Q), *k = static_cast<const T*>(K), *v = static_cast<const T*>(V),
           *g = static_cast<const T*>(dO);
-  bool pdl = false;
+  bool pdl = masked;
   if (c.rows > 0) {
     if (launch_k(la::xs::delta_kernel<D, T>, dim3(unsigned(ceil_div(c.rows, la::xs::THREADS / 32))), la::xs::THREADS, 0, st,
-                 false, a, static_cast<const T*>(O), g, delta))
+                 pdl, a, static_cast<const T*>(O), g, delta))
       return LA_ERR_CUDA;
     use(a, c.dq);
     if (set_smem(la::xs::dq_kernel<D, T>, smem)) return LA_ERR_CUDA;
@@ -270,9 +304,8 @@ int cross_backward_simt(const la_cross_problem& p, const CrossPlan& c, la::xs::A
       return LA_ERR_CUDA;
     *nl += 2;
     if (c.dq.parts > 1) {
-      if (launch_k(la::xs::sum_kernel<D, T>, dim3(unsigned(ceil_div(c.rows * (D / 2), la::xs::THREADS))), la::xs::THREADS, 0,
-                   st, true, c.rows, p.H, p.Nq, c.dq.parts, part, static_cast<float*>(nullptr), static_cast<T*>(dQ),
-                   static_cast<T*>(nullptr), a.dq, a.dq))
+      if (launch_k(la::xs::sum_rows_kernel<D, T>, dim3(unsigned(ceil_div(c.rows * (D / 2), la::xs::THREADS))), la::xs::THREADS, 0,
+                   st, true, a, part, static_cast<T*>(dQ)))
         return LA_ERR_CUDA;
       ++*nl;
     }
@@ -280,16 +313,19 @@ int cross_backward_simt(const la_cross_problem& p, const CrossPlan& c, la::xs::A
   }
   if (c.keys > 0) {
     use(a, c.dkv);
+    const bool parts = c.dkv.parts > 1 || masked;
+    float* part_k = parts ? part : nullptr;
     float* part_v = part + int64_t(c.dkv.parts) * c.keys * D;
     if (set_smem(la::xs::dkv_kernel<D, T>, smem)) return LA_ERR_CUDA;
     if (launch_k(la::xs::dkv_kernel<D, T>, dim3(unsigned(c.k_tiles * c.dkv.parts * p.B * p.Hkv)), la::xs::THREADS, smem, st, pdl,
-                 a, q, k, v, g, lse, delta, static_cast<T*>(dK), static_cast<T*>(dV), part, part_v))
+                 a, q, k, v, g, lse, delta, static_cast<T*>(dK), static_cast<T*>(dV), part_k, part_v))
       return LA_ERR_CUDA;
     ++*nl;
-    if (c.dkv.parts > 1) {
-      if (launch_k(la::xs::sum_kernel<D, T>, dim3(unsigned(ceil_div(c.keys * (D / 2), la::xs::THREADS)), 2), la::xs::THREADS, 0,
-                   st, true, c.keys, p.Hkv, p.Nk, c.dkv.parts, part, part_v, static_cast<T*>(dK), static_cast<T*>(dV),
-                   a.dk, a.dv))
+    if (parts) {
+      if (launch_k(la::xs::sum_keys_kernel<D, T>, dim3(unsigned(ceil_div(c.keys * (D / 2), la::xs::THREADS)), 2), la::xs::THREADS,
+                   0, st, true, c.keys, p.Hkv, p.Nk, c.dkv.parts, part, part_v,
+                   masked ? reinterpret_cast<const int32_t*>(ws + c.off_place) : static_cast<const int32_t*>(nullptr),
+                   static_cast<T*>(dK), static_cast<T*>(dV), a.dk, a.dv))
         return LA_ERR_CUDA;
       ++*nl;
     }
@@ -337,20 +373,11 @@ int prepare_keys(const la_cross_problem& p, const CrossPlan& c, const la::xs::Ar
   if (!a.kv_len && !a.mask)
     return make_tmap4(&out->k, K, D, p.Nk, p.Hkv, p.B, a.k) && make_tmap4(&out->v, V, D, p.Nk, p.Hkv, p.B, a.v) ? LA_OK
                                                                                                           : LA_ERR_CUDA;
-  __nv_bfloat16* kc = reinterpret_cast<__nv_bfloat16*>(ws + c.off_kc);
-  __nv_bfloat16* vc = reinterpret_cast<__nv_bfloat16*>(ws + c.off_vc);
-  int32_t* count = reinterpret_cast<int32_t*>(ws + c.off_count);
-  const la::xs::Str s = {p.Hkv * c.pad * D, c.pad * D, D};
-  if (!make_tmap4(&out->k, kc, D, c.pad, p.Hkv, p.B, s) || !make_tmap4(&out->v, vc, D, c.pad, p.Hkv, p.B, s))
+  const la::xs::Str s = gathered(p, c);
+  if (!make_tmap4(&out->k, ws + c.off_kc, D, c.pad, p.Hkv, p.B, s) || !make_tmap4(&out->v, ws + c.off_vc, D, c.pad, p.Hkv, p.B, s))
     return LA_ERR_CUDA;
-  const int64_t grid = ceil_div(p.Nk, la::xt::G_KEYS) * p.Hkv * p.B;
-  if (launch_k(la::xt::gather_kernel<D>, dim3(unsigned(grid)), la::xt::G_THREADS, 0, st, false, p.Hkv, p.Nk, c.pad,
-               static_cast<const __nv_bfloat16*>(K), static_cast<const __nv_bfloat16*>(V), a.k, a.v, a.kv_len, a.mask, kc, vc,
-               count, reinterpret_cast<int32_t*>(ws + c.off_place)))
-    return LA_ERR_CUDA;
-  out->count = count;
-  ++*nl;
-  return LA_OK;
+  out->count = reinterpret_cast<const int32_t*>(ws + c.off_count);
+  return gather_keys<D, __nv_bfloat16>(p, c, a, K, V, ws, st, nl);
 }
 
 template <int D>
@@ -444,9 +471,9 @@ int cross_backward_tc(const la_cross_problem& p, const CrossPlan& c, la::xs::Arg
     return LA_ERR_CUDA;
   ++*nl;
   if (c.dq.parts > 1) {
-    if (launch_k(la::xs::sum_kernel<D, T>, dim3(unsigned(ceil_div(c.rows * (D / 2), la::xs::THREADS))), la::xs::THREADS, 0, st,
-                 true, c.rows, p.H, p.Nq, c.dq.parts, part, static_cast<float*>(nullptr), static_cast<T*>(dQ),
-                 static_cast<T*>(nullptr), a.dq, a.dq))
+    use(a, c.dq);
+    if (launch_k(la::xs::sum_rows_kernel<D, T>, dim3(unsigned(ceil_div(c.rows * (D / 2), la::xs::THREADS))), la::xs::THREADS, 0, st,
+                 true, a, part, static_cast<T*>(dQ)))
       return LA_ERR_CUDA;
     ++*nl;
   }
@@ -459,8 +486,8 @@ int cross_backward_tc(const la_cross_problem& p, const CrossPlan& c, la::xs::Arg
   if (launch_k(kk, dim3(unsigned(std::min<int64_t>(t.total, sm))), la::xb::THREADS, mk, st, true, tq, tg, keys.k, keys.v, t,
                lse, delta, part, part_v))
     return LA_ERR_CUDA;
-  if (launch_k(la::xb::sum_kernel<D>, dim3(unsigned(ceil_div(c.keys * (D / 2), 256)), 2), 256, 0, st, true, c.keys, p.Hkv,
-               p.Nk, c.dkv.parts, part, part_v,
+  if (launch_k(la::xs::sum_keys_kernel<D, T>, dim3(unsigned(ceil_div(c.keys * (D / 2), la::xs::THREADS)), 2), la::xs::THREADS, 0,
+               st, true, c.keys, p.Hkv, p.Nk, c.dkv.parts, part, part_v,
                keys.count ? reinterpret_cast<const int32_t*>(ws + c.off_place) : static_cast<const int32_t*>(nullptr),
                static_cast<T*>(dK), static_cast<T*>(dV), a.dk, a.dv))
     return LA_ERR_CUDA;

@@ -838,35 +838,5 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
   if (warp == 13) tmem_dealloc(tmem, 512);
 }
 
-// dK and dV from the parts' sums, in order: key j of (b, h) is row place[b][j] of the parts (j itself
-// when nothing was gathered; 0 where it is not attended).  A thread has 2 channels; blockIdx.y
-// selects dK or dV.
-template <int D>
-__global__ void __launch_bounds__(256)
-sum_kernel(int64_t keys, int64_t Hkv, int64_t Nk, int splits, const float* __restrict__ part_k,
-           const float* __restrict__ part_v, const int32_t* __restrict__ place, __nv_bfloat16* __restrict__ dK,
-           __nv_bfloat16* __restrict__ dV, xs::Str sk, xs::Str sv) {
-  pdl_wait();
-  const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t key = e / (D / 2);
-  const int c = static_cast<int>(e % (D / 2)) * 2;
-  if (key >= keys) return;
-  const int64_t n = key % Nk, bh = key / Nk, b = bh / Hkv;
-  const float* part = blockIdx.y == 0 ? part_k : part_v;
-  const xs::Str st = blockIdx.y == 0 ? sk : sv;
-  __nv_bfloat16* out = (blockIdx.y == 0 ? dK : dV) + b * st.b + (bh % Hkv) * st.h + n * st.n + c;
-  const int64_t at = place ? int64_t(place[b * Nk + n]) : n;
-  float2 v = make_float2(0.f, 0.f);
-  if (at >= 0) {
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-      const float2 u = *reinterpret_cast<const float2*>(part + (int64_t(s) * keys + bh * Nk + at) * D + c);
-      v.x += u.x;
-      v.y += u.y;
-    }
-  }
-  *reinterpret_cast<uint32_t*>(out) = pack_bf16(v.x, v.y);
-}
-
 }  // namespace xb
 }  // namespace la

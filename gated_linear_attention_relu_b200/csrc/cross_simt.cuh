@@ -379,6 +379,15 @@ delta_kernel(const __grid_constant__ Args a, const T* __restrict__ O, const T* _
 template <int D>
 __host__ __device__ constexpr size_t bwd_smem() { return (4 * BT * row_stride<D>() + BT * PS + 2 * BT) * 4 + BT; }
 
+// The gradients' threads: a warp covers 4 x 8 of the 16 x 16, so that each of a step's shared-memory
+// loads is one wavefront (2 x 16, which the forward's row sums want, takes 12 instead of 8 for the
+// scores' 16 cycles of FMAs).
+__device__ __forceinline__ void thread_tile(int& tx, int& ty) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  tx = (warp & 1) * 8 + (lane & 7);
+  ty = (warp >> 1) * 4 + (lane >> 3);
+}
+
 // dQ of one query tile over the split's keys; part [splits][rows][D] when splits > 1.
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS)
@@ -397,7 +406,8 @@ dq_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __re
   const Where w = where(a, a.q_tiles, a.H);
   const int64_t kh = w.h / a.group, q0 = w.tile * BT;
   const int qn = static_cast<int>(a.Nq - q0 < BT ? a.Nq - q0 : BT);
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  int tx, ty;
+  thread_tile(tx, ty);
   const int64_t limit = key_limit(a, w.b);
   const int64_t k_begin = int64_t(w.split) * a.tiles_per_split * BT;
   int64_t k_end = k_begin + int64_t(a.tiles_per_split) * BT;
@@ -460,7 +470,7 @@ dq_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __re
 }
 
 // dK and dV of one key tile over the split's query tiles (all heads of the group, head after head);
-// part_k, part_v [splits][B * Hkv * Nk][D] when splits > 1.
+// part_k, part_v [splits][B * Hkv * Nk][D] where given (else dK and dV themselves; splits = 1).
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS)
 dkv_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __restrict__ K, const T* __restrict__ V,
@@ -480,7 +490,8 @@ dkv_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __r
   const Where w = where(a, a.k_tiles, a.Hkv);
   const int64_t k0 = w.tile * BT;
   const int kn = static_cast<int>(a.Nk - k0 < BT ? a.Nk - k0 : BT);
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  int tx, ty;
+  thread_tile(tx, ty);
   const int64_t limit = key_limit(a, w.b);
   load_ok(a, w.b, k0, limit, ok);
   __syncthreads();
@@ -552,7 +563,7 @@ dkv_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __r
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) {
       const int c = chan<D>(tx, k);
-      if (a.splits > 1) {
+      if (part_k) {
         const int64_t at = (int64_t(w.split) * keys + key) * D + c;
         *reinterpret_cast<float2*>(part_k + at) = upk(ak[i][k]);
         *reinterpret_cast<float2*>(part_v + at) = upk(av[i][k]);
@@ -564,29 +575,126 @@ dkv_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __r
   }
 }
 
-// out[b, h, n] = sum over the splits, in order, of part[s][(b * heads + h) * N + n]; one thread per
-// pair of channels.  blockIdx.y selects the second output (dV beside dK).
+// dQ: out[b, h, n] = sum over the splits, in order, of part[s][(b * H + h) * Nq + n]; one thread per
+// pair of channels.
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS)
-sum_kernel(int64_t rows, int64_t heads, int64_t N, int splits, const float* __restrict__ part0, const float* __restrict__ part1,
-           T* __restrict__ out0, T* __restrict__ out1, Str s0, Str s1) {
+sum_rows_kernel(const __grid_constant__ Args a, const float* __restrict__ part, T* __restrict__ dQ) {
   pdl_wait();
   const int64_t e = int64_t(blockIdx.x) * THREADS + threadIdx.x;
   const int64_t row = e / (D / 2);
   const int c = static_cast<int>(e % (D / 2)) * 2;
-  if (row >= rows) return;
-  const float* part = blockIdx.y == 0 ? part0 : part1;
-  T* out = blockIdx.y == 0 ? out0 : out1;
-  const Str st = blockIdx.y == 0 ? s0 : s1;
+  if (row >= a.rows) return;
   float2 v = make_float2(0.f, 0.f);
 #pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    const float2 u = *reinterpret_cast<const float2*>(part + (int64_t(s) * rows + row) * D + c);
+  for (int s = 0; s < a.splits; ++s) {
+    const float2 u = *reinterpret_cast<const float2*>(part + (int64_t(s) * a.rows + row) * D + c);
     v.x += u.x;
     v.y += u.y;
   }
-  const int64_t n = row % N, bh = row / N;
-  store_pair<D>(out + (bh / heads) * st.b + (bh % heads) * st.h + n * st.n + c, v);
+  const int64_t n = row % a.Nq, bh = row / a.Nq;
+  store_pair<D>(dQ + (bh / a.H) * a.dq.b + (bh % a.H) * a.dq.h + n * a.dq.n + c, v);
+}
+
+// dK and dV from the parts' sums, in order: key j of (b, h) is row place[b][j] of the parts (j itself
+// when nothing was gathered; 0 where it is not attended).  A thread has 2 channels; blockIdx.y
+// selects dK or dV.
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS)
+sum_keys_kernel(int64_t keys, int64_t Hkv, int64_t Nk, int splits, const float* __restrict__ part_k,
+                const float* __restrict__ part_v, const int32_t* __restrict__ place, T* __restrict__ dK,
+                T* __restrict__ dV, Str sk, Str sv) {
+  pdl_wait();
+  const int64_t e = int64_t(blockIdx.x) * THREADS + threadIdx.x;
+  const int64_t key = e / (D / 2);
+  const int c = static_cast<int>(e % (D / 2)) * 2;
+  if (key >= keys) return;
+  const int64_t n = key % Nk, bh = key / Nk, b = bh / Hkv;
+  const float* part = blockIdx.y == 0 ? part_k : part_v;
+  const Str st = blockIdx.y == 0 ? sk : sv;
+  T* out = (blockIdx.y == 0 ? dK : dV) + b * st.b + (bh % Hkv) * st.h + n * st.n + c;
+  const int64_t at = place ? int64_t(place[b * Nk + n]) : n;
+  float2 v = make_float2(0.f, 0.f);
+  if (at >= 0) {
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      const float2 u = *reinterpret_cast<const float2*>(part + (int64_t(s) * keys + bh * Nk + at) * D + c);
+      v.x += u.x;
+      v.y += u.y;
+    }
+  }
+  store_pair<D>(out, v);
+}
+
+// Gathers the attended keys: kc, vc [B, Hkv, pad, D] hold the rows of K and V that are attended, in
+// order, then zeros up to a multiple of 16 rows (what lies behind is never read); count[b] is their
+// number and place[b][j] where key j went (-1: unattended).  Unattended rows are not read.
+// One block per 64 keys, head and batch row; each counts the attended keys before its own.
+constexpr int G_THREADS = 256, G_KEYS = 64;
+
+// PR: 16-byte packs of a row of d channels.  Strides count elements of T.
+template <typename T, int PR>
+__global__ void __launch_bounds__(G_THREADS)
+gather_kernel(int64_t Hkv, int64_t Nk, int64_t pad, const T* __restrict__ K, const T* __restrict__ V, Str sk, Str sv,
+              const int32_t* __restrict__ kv_len, const uint8_t* __restrict__ mask, T* __restrict__ kc, T* __restrict__ vc,
+              int32_t* __restrict__ count, int32_t* __restrict__ place) {
+  constexpr int VEC = 16 / int(sizeof(T)), D = PR * VEC;
+  __shared__ int before[G_THREADS / 32];
+  __shared__ int pos[G_KEYS];
+  __shared__ int own[2];
+  pdl_trigger();
+  const int64_t chunks = (Nk + G_KEYS - 1) / G_KEYS;
+  const int64_t chunk = blockIdx.x % chunks, hb = blockIdx.x / chunks;
+  const int64_t h = hb % Hkv, b = hb / Hkv;
+  int64_t limit = Nk;
+  if (kv_len) limit = kv_len[b] < 0 ? 0 : (kv_len[b] < Nk ? kv_len[b] : Nk);
+  const int64_t k0 = chunk * G_KEYS;
+  const uint8_t* mb = mask ? mask + b * Nk : nullptr;
+  const int64_t head = k0 < limit ? k0 : limit;
+  int n = 0;
+  if (mb) {
+    for (int64_t j = threadIdx.x; j < head; j += G_THREADS) n += mb[j] != 0;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if ((threadIdx.x & 31) == 0) before[threadIdx.x >> 5] = n;
+  } else if ((threadIdx.x & 31) == 0) {
+    before[threadIdx.x >> 5] = threadIdx.x == 0 ? static_cast<int>(head) : 0;
+  }
+  bool at = false;
+  uint32_t ball = 0;
+  if (threadIdx.x < G_KEYS) {
+    const int64_t j = k0 + threadIdx.x;
+    at = j < limit && (!mb || mb[j] != 0);
+    ball = __ballot_sync(0xffffffffu, at);
+    if ((threadIdx.x & 31) == 0) own[threadIdx.x >> 5] = __popc(ball);
+  }
+  __syncthreads();
+  int base = 0;
+#pragma unroll
+  for (int i = 0; i < G_THREADS / 32; ++i) base += before[i];
+  if (threadIdx.x < G_KEYS) {
+    const int p = base + (threadIdx.x >= 32 ? own[0] : 0) + __popc(ball & ((1u << (threadIdx.x & 31)) - 1u));
+    pos[threadIdx.x] = at ? p : -1;
+    if (h == 0 && k0 + threadIdx.x < Nk) place[b * Nk + k0 + threadIdx.x] = at ? p : -1;
+  }
+  __syncthreads();
+  const int64_t row0 = (b * Hkv + h) * pad;
+  for (int e = threadIdx.x; e < G_KEYS * PR; e += G_THREADS) {
+    const int r = e / PR, c = (e % PR) * VEC;
+    if (pos[r] < 0) continue;
+    const int64_t j = k0 + r, to = (row0 + pos[r]) * D + c;
+    *reinterpret_cast<uint4*>(kc + to) = *reinterpret_cast<const uint4*>(K + b * sk.b + h * sk.h + j * sk.n + c);
+    *reinterpret_cast<uint4*>(vc + to) = *reinterpret_cast<const uint4*>(V + b * sv.b + h * sv.h + j * sv.n + c);
+  }
+  if (chunk == chunks - 1) {
+    const int total = base + own[0] + own[1];
+    if (h == 0 && threadIdx.x == 0) count[b] = total;
+    const int rows = ((total + 15) & ~15) - total;
+    for (int e = threadIdx.x; e < rows * PR; e += G_THREADS) {
+      const int64_t to = (row0 + total + e / PR) * D + (e % PR) * VEC;
+      *reinterpret_cast<uint4*>(kc + to) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(vc + to) = make_uint4(0, 0, 0, 0);
+    }
+  }
 }
 
 }  // namespace xs

@@ -578,76 +578,5 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   if (warp == 13) tmem_dealloc(tmem, 512);
 }
 
-// Gathers the attended keys: kc, vc [B, Hkv, pad, D] hold the rows of K and V that are attended, in
-// order, then zeros up to a multiple of 16 rows (what lies behind is never read); count[b] is their
-// number and place[b][j] where key j went (-1: unattended).  Unattended rows are not read.
-// One block per 64 keys, head and batch row; each counts the attended keys before its own.
-constexpr int G_THREADS = 256, G_KEYS = 64;
-
-template <int D>
-__global__ void __launch_bounds__(G_THREADS)
-gather_kernel(int64_t Hkv, int64_t Nk, int64_t pad, const __nv_bfloat16* __restrict__ K, const __nv_bfloat16* __restrict__ V,
-              xs::Str sk, xs::Str sv, const int32_t* __restrict__ kv_len, const uint8_t* __restrict__ mask,
-              __nv_bfloat16* __restrict__ kc, __nv_bfloat16* __restrict__ vc, int32_t* __restrict__ count,
-              int32_t* __restrict__ place) {
-  __shared__ int before[G_THREADS / 32];
-  __shared__ int pos[G_KEYS];
-  __shared__ int own[2];
-  pdl_trigger();
-  const int64_t chunks = (Nk + G_KEYS - 1) / G_KEYS;
-  const int64_t chunk = blockIdx.x % chunks, hb = blockIdx.x / chunks;
-  const int64_t h = hb % Hkv, b = hb / Hkv;
-  int64_t limit = Nk;
-  if (kv_len) limit = kv_len[b] < 0 ? 0 : (kv_len[b] < Nk ? kv_len[b] : Nk);
-  const int64_t k0 = chunk * G_KEYS;
-  const uint8_t* mb = mask ? mask + b * Nk : nullptr;
-  const int64_t head = k0 < limit ? k0 : limit;
-  int n = 0;
-  if (mb) {
-    for (int64_t j = threadIdx.x; j < head; j += G_THREADS) n += mb[j] != 0;
-    n = __reduce_add_sync(0xffffffffu, n);
-    if ((threadIdx.x & 31) == 0) before[threadIdx.x >> 5] = n;
-  } else if ((threadIdx.x & 31) == 0) {
-    before[threadIdx.x >> 5] = threadIdx.x == 0 ? static_cast<int>(head) : 0;
-  }
-  bool at = false;
-  uint32_t ball = 0;
-  if (threadIdx.x < G_KEYS) {
-    const int64_t j = k0 + threadIdx.x;
-    at = j < limit && (!mb || mb[j] != 0);
-    ball = __ballot_sync(0xffffffffu, at);
-    if ((threadIdx.x & 31) == 0) own[threadIdx.x >> 5] = __popc(ball);
-  }
-  __syncthreads();
-  int base = 0;
-#pragma unroll
-  for (int i = 0; i < G_THREADS / 32; ++i) base += before[i];
-  if (threadIdx.x < G_KEYS) {
-    const int p = base + (threadIdx.x >= 32 ? own[0] : 0) + __popc(ball & ((1u << (threadIdx.x & 31)) - 1u));
-    pos[threadIdx.x] = at ? p : -1;
-    if (h == 0 && k0 + threadIdx.x < Nk) place[b * Nk + k0 + threadIdx.x] = at ? p : -1;
-  }
-  __syncthreads();
-  constexpr int PR = D / 8;  // 16-byte packs per row
-  const int64_t row0 = (b * Hkv + h) * pad;
-  for (int e = threadIdx.x; e < G_KEYS * PR; e += G_THREADS) {
-    const int r = e / PR, c = (e % PR) * 8;
-    if (pos[r] < 0) continue;
-    const int64_t j = k0 + r, to = (row0 + pos[r]) * D + c;
-    *reinterpret_cast<uint4*>(kc + to) = *reinterpret_cast<const uint4*>(K + b * sk.b + h * sk.h + j * sk.n + c);
-    *reinterpret_cast<uint4*>(vc + to) = *reinterpret_cast<const uint4*>(V + b * sv.b + h * sv.h + j * sv.n + c);
-  }
-  if (chunk == chunks - 1) {
-    const int total = base + own[0] + own[1];
-    if (h == 0 && threadIdx.x == 0) count[b] = total;
-    const int rows = ((total + 15) & ~15) - total;
-    for (int e = threadIdx.x; e < rows * PR; e += G_THREADS) {
-      const int64_t to = (row0 + total + e / PR) * D + (e % PR) * 8;
-      *reinterpret_cast<uint4*>(kc + to) = make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(vc + to) = make_uint4(0, 0, 0, 0);
-    }
-  }
-}
-
 }  // namespace xt
 }  // namespace la
