@@ -1,4 +1,5 @@
-"""Builds the CUDA library in-tree: ``liblinattn.so`` next to this file, for sm_100a only."""
+"""Builds the CUDA library in-tree: ``liblinattn.so`` next to this file, for sm_100a only; and the
+CPython module ``_marshal.so`` that makes the calls of block.py."""
 from __future__ import annotations
 
 import os
@@ -10,8 +11,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblinattn.so")
 SOURCES = [os.path.join(CSRC, "la_api.cu"), os.path.join(CSRC, "block_api.cu")]
-LISTS = os.path.join(HERE, "_lists.so")
-LISTS_SOURCE = os.path.join(CSRC, "lists.cpp")
+MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
     os.path.join(ROOT, "include", "la.h")]
 
@@ -51,10 +52,11 @@ def up_to_date(out: str = LIB) -> bool:
     return all(os.path.getmtime(f) <= t for f in DEPS)
 
 
-def build_lists(force: bool = False, verbose: bool = False) -> str:
-    """Builds the CPython helper that reads lists of torch tensors, ``_lists.so``."""
-    if not force and os.path.exists(LISTS) and os.path.getmtime(LISTS_SOURCE) <= os.path.getmtime(LISTS):
-        return LISTS
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """Builds the CPython module between block.py and the library, ``_marshal.so``."""
+    if not force and os.path.exists(MARSHAL) and all(
+            os.path.getmtime(f) <= os.path.getmtime(MARSHAL) for f in (MARSHAL_SOURCE, os.path.join(ROOT, "include", "la.h"))):
+        return MARSHAL
     import sysconfig
 
     import torch
@@ -63,19 +65,19 @@ def build_lists(force: bool = False, verbose: bool = False) -> str:
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include") if os.path.isabs(nvcc()) else "/usr/local/cuda/include"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", inc, "-I",
            os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"], "-I",
-           os.path.join(ROOT, "include"), "-I", cuda, "-o", LISTS, LISTS_SOURCE, "-L",
-           os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+           os.path.join(ROOT, "include"), "-I", cuda, "-o", MARSHAL, MARSHAL_SOURCE, "-L",
+           os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("g++ failed building _lists.so")
-    return LISTS
+        raise RuntimeError("g++ failed building _marshal.so")
+    return MARSHAL
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    build_lists(force, verbose)
+    build_marshal(force, verbose)
     if not force and up_to_date():
         return LIB
     cmd = command()
