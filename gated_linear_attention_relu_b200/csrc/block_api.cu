@@ -33,15 +33,20 @@ cudaError_t take_block_error(unsigned int* value) {
 
 namespace {
 
+la::KernelTable g_kernels;
+
+template <typename F>
+int set_smem(F* kern, size_t bytes) { return g_kernels.smem(kern, bytes); }
+template <typename F>
+bool launch_regs(F* kern, uint32_t regs) { return g_kernels.regs(kern, regs); }
+
 using la::align256;
 using la::aligned16;
 using la::current_sm_count;
 using la::g_last_launches;
 using la::launch_k;
-using la::set_smem;
 
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1024;
-constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
 
 size_t elem_size(int32_t dtype) { return dtype == LA_BF16 ? 2 : 4; }
 
@@ -351,14 +356,6 @@ bool make_tmap4(CUtensorMap* m, const void* base, int64_t d, int64_t tokens, int
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether the kernel's launch grants at least `regs` registers a thread (what its setmaxnreg split
-// adds up to).
-template <typename F>
-bool launch_regs(F* kern, uint32_t regs) {
-  cudaFuncAttributes at;
-  return cudaFuncGetAttributes(&at, kern) == cudaSuccess && uint32_t(at.numRegs) >= regs;
-}
-
 // The keys as the tensor-core kernels read them: the tensors themselves, or (with lengths or a
 // mask) the attended rows, gathered.
 struct Keys {
@@ -620,7 +617,7 @@ template <typename T, int VEC, int NV, int WPR, bool RING>
 int norm_forward_long(const la_norm_problem& p, const la::ln::Args& a, int sm, const NormForward& f, cudaStream_t st) {
   auto kern = la::ln::forward_long<T, VEC, NV, WPR, RING>;
   const int per_sm = WPR <= 8 ? 4 : 2;
-  const int parts = norm_parts(p, sm, per_sm);
+  const int parts = p.rows <= 2 * int64_t(sm) ? int(p.rows / p.groups) : norm_parts(p, sm, per_sm);
   const size_t row = size_t(p.cols) * sizeof(T);
   const int stages = RING ? norm_stages(row, per_sm) : 0;
   if (RING && set_smem(kern, stages * row)) return LA_ERR_CUDA;
@@ -633,8 +630,12 @@ int norm_forward_any(const la_norm_problem& p, const la::ln::Args& a, int sm, co
   const void* ptr[2] = {f.x, f.y};
   const int64_t str[2] = {p.sx, p.sy};
   const int64_t c = p.cols;
+  // Few rows do not fill the machine: what counts is how soon one is done, so more threads share it.
+  const bool few = p.rows <= 2 * int64_t(sm);
   if (norm_vec<T>(p, 2, ptr, str)) {
     constexpr int V = 16 / int(sizeof(T));
+    if (few && c > 32 * V && c <= 256 * V) return norm_forward_long<T, V, 1, 8, false>(p, a, sm, f, st);
+    if (few && c > 256 * V && c <= 1024 * V) return norm_forward_long<T, V, 2, 16, false>(p, a, sm, f, st);
     if (c <= 8 * V) return norm_forward_short<T, V, 1, 8, 4>(p, a, sm, f, st);
     if (c <= 16 * V) return norm_forward_short<T, V, 1, 16, 4>(p, a, sm, f, st);
     if (c <= 32 * V) return norm_forward_short<T, V, 1, 32, 4>(p, a, sm, f, st);
@@ -646,6 +647,7 @@ int norm_forward_any(const la_norm_problem& p, const la::ln::Args& a, int sm, co
     if (c <= 2048 * V) return norm_forward_long<T, V, 4, 16, true>(p, a, sm, f, st);
     return norm_forward_long<T, V, 8, 16, true>(p, a, sm, f, st);
   }
+  if (few && c > 32 * 4 && c <= 256 * 4) return norm_forward_long<T, 1, 4, 8, false>(p, a, sm, f, st);
   if (c <= 8 * 4) return norm_forward_short<T, 1, 4, 8, 2>(p, a, sm, f, st);
   if (c <= 32 * 4) return norm_forward_short<T, 1, 4, 32, 2>(p, a, sm, f, st);
   if (c <= 32 * 16) return norm_forward_short<T, 1, 16, 32, 1>(p, a, sm, f, st);

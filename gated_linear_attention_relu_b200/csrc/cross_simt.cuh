@@ -209,6 +209,7 @@ forward_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T*
   const int64_t kh = w.h / a.group, q0 = w.tile * BT;
   const int qn = static_cast<int>(a.Nq - q0 < BT ? a.Nq - q0 : BT);
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  pdl_wait();  // (gathered keys and their counts)
   const int64_t limit = key_limit(a, w.b);
   const int64_t k_begin = int64_t(w.split) * a.tiles_per_split * BT;
   int64_t k_end = k_begin + int64_t(a.tiles_per_split) * BT;
@@ -363,6 +364,7 @@ template <int D, typename T>
 __global__ void __launch_bounds__(THREADS)
 delta_kernel(const __grid_constant__ Args a, const T* __restrict__ O, const T* __restrict__ dO, float* __restrict__ delta) {
   pdl_trigger();
+  pdl_wait();  // (it reads nothing of the gather's, but the kernels after it wait for this one only)
   const int64_t row = int64_t(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= a.rows) return;
@@ -408,6 +410,7 @@ dq_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __re
   const int qn = static_cast<int>(a.Nq - q0 < BT ? a.Nq - q0 : BT);
   int tx, ty;
   thread_tile(tx, ty);
+  pdl_wait();  // D_i, gathered keys and their counts
   const int64_t limit = key_limit(a, w.b);
   const int64_t k_begin = int64_t(w.split) * a.tiles_per_split * BT;
   int64_t k_end = k_begin + int64_t(a.tiles_per_split) * BT;
@@ -416,7 +419,6 @@ dq_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __re
 
   load_tile<D>(qs, Q + w.b * a.q.b + w.h * a.q.h + q0 * a.q.n, a.q.n, qn, static_cast<const uint8_t*>(nullptr));
   load_tile<D>(gs, dO + w.b * a.dout.b + w.h * a.dout.h + q0 * a.dout.n, a.dout.n, qn, static_cast<const uint8_t*>(nullptr));
-  pdl_wait();
   float L[4], dl[4];
   uint64_t acc[4][D / 32];
 #pragma unroll
@@ -492,12 +494,12 @@ dkv_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __r
   const int kn = static_cast<int>(a.Nk - k0 < BT ? a.Nk - k0 : BT);
   int tx, ty;
   thread_tile(tx, ty);
+  pdl_wait();  // D_i, gathered keys and their counts
   const int64_t limit = key_limit(a, w.b);
   load_ok(a, w.b, k0, limit, ok);
   __syncthreads();
   load_tile<D>(ks, K + w.b * a.k.b + w.h * a.k.h + k0 * a.k.n, a.k.n, kn, ok);
   load_tile<D>(vs, V + w.b * a.v.b + w.h * a.v.h + k0 * a.v.n, a.v.n, kn, ok);
-  pdl_wait();
   uint64_t ak[4][D / 32], av[4][D / 32];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
