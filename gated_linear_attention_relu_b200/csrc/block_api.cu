@@ -299,7 +299,7 @@ int cross_backward_simt(const la_cross_problem& p, const CrossPlan& c, la::xs::A
           *g = static_cast<const T*>(dO);
   bool pdl = masked;
   if (c.rows > 0) {
-    if (launch_k(la::xs::delta_kernel<D, T>, dim3(unsigned(ceil_div(c.rows, la::xs::THREADS / 32))), la::xs::THREADS, 0, st,
+    if (launch_k(la::xs::delta_kernel<D, T>, dim3(unsigned(p.B * p.H * ceil_div(p.Nq, la::xs::delta_rows<D, T>()))), la::xs::THREADS, 0, st,
                  pdl, a, static_cast<const T*>(O), g, delta))
       return LA_ERR_CUDA;
     use(a, c.dq);
@@ -451,7 +451,10 @@ int cross_backward_tc(const la_cross_problem& p, const CrossPlan& c, la::xs::Arg
   const size_t mq = la::xb::CfgQ<DP>::SMEM, mk = la::xb::CfgK<DP>::SMEM;
   if (set_smem(kq, mq) || set_smem(kk, mk) || !launch_regs(kq, la::xb::REGS_LAUNCH) || !launch_regs(kk, la::xb::REGS_LAUNCH))
     return LA_ERR_CUDA;
-  // dQ (and D_i, which the dK / dV kernel reads)
+  if (launch_k(la::xs::delta_kernel<D, T>, dim3(unsigned(p.B * p.H * ceil_div(p.Nq, la::xs::delta_rows<D, T>()))), la::xs::THREADS, 0, st,
+               keys.count != nullptr, a, static_cast<const T*>(O), static_cast<const T*>(dO), delta))
+    return LA_ERR_CUDA;
+  ++*nl;
   t.tiles = t.q_tiles;
   t.splits = c.dq.parts;
   t.per = c.dq.per;
@@ -462,9 +465,8 @@ int cross_backward_tc(const la_cross_problem& p, const CrossPlan& c, la::xs::Arg
     t.fd_heads = la::make_fastdiv(uint32_t(heads));
   };
   divisions(p.H);
-  if (launch_k(kq, dim3(unsigned(std::min<int64_t>(t.total, sm))), la::xb::THREADS, mq, st, keys.count != nullptr, tq, tg,
-               keys.k, keys.v, t, static_cast<const T*>(O), static_cast<const T*>(dO), lse, delta, static_cast<T*>(dQ), part,
-               int(wide)))
+  if (launch_k(kq, dim3(unsigned(std::min<int64_t>(t.total, sm))), la::xb::THREADS, mq, st, true, tq, tg, keys.k, keys.v, t,
+               lse, delta, static_cast<T*>(dQ), part, int(wide)))
     return LA_ERR_CUDA;
   ++*nl;
   if (c.dq.parts > 1) {

@@ -3,7 +3,8 @@
 //   p_ij = exp(s_ij - lse_i),  D_i = dO_i . O_i,  ds_ij = p_ij (dO_i . v_j - D_i)
 //   dQ_i = scale sum_j ds_ij k_j,  dK_j = scale sum_i ds_ij q_i,  dV_j = sum_i p_ij dO_i
 //
-// Two kernels, so that every sum has one owner and a fixed order (no atomics): dq_kernel keeps a
+// D_i comes from a kernel of its own (one pass over O and dO; inside dq_kernel its code and its loads
+// held up the other warps).  Two more, so that every sum has one owner and a fixed order (no atomics): dq_kernel keeps a
 // query tile and walks the keys, dkv_kernel keeps a key tile and walks the queries.  Each forms the
 // scores and dP = dO V^T again (7 products of a tile pair instead of 5).  p and ds go back to tensor
 // memory as bf16 (rounded once each) as the operand of the product that follows; the softmax scale
@@ -16,9 +17,11 @@
 // dK [384, 512); p overwrites S^T, ds overwrites dP^T.  dV of this step and S^T of the next run while
 // the math warps form ds, dK and the next dP^T while they form the next p.
 //
-// Warps: 0-7 math (warps 0-3 the first 64 columns of a tile, 4-7 the others; thread = row);
-// 8-11 dq: D_i of the next query tile, dQ to memory; dkv: lse and D of the query tiles to come;
-// 12 TMA producer; 13, 14 MMA issuers.  One CTA per SM, persistent.  Every wait is bounded.
+// Warps: 0-15 math (thread = row; warps 4 c .. 4 c + 3 have columns [32 c, 32 c + 32) of a tile: with
+// half as many, and twice the columns each, their latencies showed: a step took 2400 cycles for 1024
+// of exponentials);
+// 16-19 dq: dQ to memory; dkv: lse and D of the query tiles to come;
+// 20 TMA producer; 21, 22 MMA issuers.  One CTA per SM, persistent.  Every wait is bounded.
 #pragma once
 #include "cross_tc.cuh"
 
@@ -34,9 +37,9 @@ using xt::regs_inc;
 using xt::store32;
 using xt::store_row32;
 
-constexpr int THREADS = 512;
-constexpr uint32_t REGS_LAUNCH = 128, REGS_MATH = 176, REGS_AUX = 104, REGS_CTRL = 56;
-static_assert(256 * REGS_MATH + 128 * REGS_AUX + 128 * REGS_CTRL <= THREADS * REGS_LAUNCH, "register split");
+constexpr int THREADS = 768, MATH_WARPS = 16, AUX = 16, CTRL = 20;  // first auxiliary and control warp
+constexpr uint32_t REGS_LAUNCH = 80, REGS_MATH = 88, REGS_AUX = 72, REGS_CTRL = 56;
+static_assert(512 * REGS_MATH + 128 * REGS_AUX + 128 * REGS_CTRL <= THREADS * REGS_LAUNCH, "register split");
 
 struct Args {
   int64_t B, H, Hkv, Nq, Nk, rows, keys;
@@ -61,8 +64,7 @@ struct CfgQ {
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_K = QST * TILE;
   static constexpr uint32_t OFF_V = OFF_K + KST * TILE;
-  static constexpr uint32_t OFF_D = OFF_V + VST * TILE;
-  static constexpr uint32_t OFF_BAR = OFF_D + 2 * BM * 4;
+  static constexpr uint32_t OFF_BAR = OFF_V + VST * TILE;
   static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;
 };
 static_assert(CfgQ<128>::SMEM <= 232448 && CfgQ<64>::SMEM <= 232448, "shared memory budget");
@@ -72,7 +74,7 @@ struct BarsQ {
   uint64_t qfull[CfgQ<DP>::QST], qempty[CfgQ<DP>::QST];
   uint64_t kfull[CfgQ<DP>::KST], kempty[CfgQ<DP>::KST];
   uint64_t vfull[CfgQ<DP>::VST], vempty[CfgQ<DP>::VST];
-  uint64_t sfull[2], dsready[2], dready[2];
+  uint64_t sfull[2], dsready[2];
   uint64_t dpfull, dpfree, dqfull, dqfree, final_[2];
   uint32_t tmem_base;
   int abort_flag;
@@ -141,15 +143,14 @@ template <int DP, int D>
 __global__ void __launch_bounds__(THREADS, 1)
 dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
           const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-          const __grid_constant__ Args a, const __nv_bfloat16* __restrict__ O, const __nv_bfloat16* __restrict__ dO,
-          const float* __restrict__ lse, float* __restrict__ delta, __nv_bfloat16* __restrict__ dQ,
+          const __grid_constant__ Args a, const float* __restrict__ lse, const float* __restrict__ delta,
+          __nv_bfloat16* __restrict__ dQ,
           float* __restrict__ part, int wide) {
   using C = CfgQ<DP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1k(smem_raw);
   BarsQ<DP>* bars = reinterpret_cast<BarsQ<DP>*>(smem + C::OFF_BAR);
   const uint32_t sbase = smem_u32(smem);
-  float* d_sm = reinterpret_cast<float*>(smem + C::OFF_D);
   const int warp = warp_number(), lane = threadIdx.x & 31;
   volatile int* abort_flag = &bars->abort_flag;
 
@@ -159,11 +160,10 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     for (int s = 0; s < C::VST; ++s) mbar_init(&bars->vfull[s], 1), mbar_init(&bars->vempty[s], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->sfull[s], 1);
-      mbar_init(&bars->dsready[s], 8);
-      mbar_init(&bars->dready[s], 4);
+      mbar_init(&bars->dsready[s], MATH_WARPS);
     }
     mbar_init(&bars->dpfull, 1);
-    mbar_init(&bars->dpfree, 8);
+    mbar_init(&bars->dpfree, MATH_WARPS);
     mbar_init(&bars->dqfull, 1);
     mbar_init(&bars->dqfree, 4);
     mbar_init(&bars->final_[0], 1);
@@ -171,11 +171,11 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     bars->abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 13) {
+  if (warp == CTRL + 1) {
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
   }
-  if (warp == 12 && lane == 0) {
+  if (warp == CTRL && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmG);
     tma_prefetch_desc(&tmK);
@@ -186,11 +186,11 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
   pdl_trigger();
-  pdl_wait();  // the gathered keys and their counts
+  pdl_wait();  // D_i, the gathered keys and their counts
 
-  if (warp >= 12) {
+  if (warp >= CTRL) {
     regs_dec<REGS_CTRL>();
-    if (warp == 12 && lane == 0) {
+    if (warp == CTRL && lane == 0) {
       // ---------------------------------------------------------- TMA producer
       uint32_t qi = 0, ki = 0;
       bool ok = true;
@@ -224,7 +224,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         drain(bars->kfull, C::KST, ki);
         drain(bars->vfull, C::VST, ki);
       }
-    } else if (warp == 13) {
+    } else if (warp == CTRL + 1) {
       // ---------------------------------------------------------- MMA issuer of S and dQ
       // (the issuers' warps stay converged; one's waits hide behind the other's products)
       uint32_t i = 0, items = 0;  // steps (key tiles) and items done
@@ -267,7 +267,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
           if (elect_one()) {
 #pragma unroll 1
             for (int kk = 0; kk < ksteps; ++kk)
-              mma_bf16_ts(tmem + Q_DQ, ds + 8u * (kk & 3) + 64u * (kk >> 2), kd + tile::step_mn(kk),
+              mma_bf16_ts(tmem + Q_DQ, ds + 8u * (kk & 1) + 32u * (kk >> 1), kd + tile::step_mn(kk),
                           idesc_bf16_f32(BM, DP, false, true), j > 0 || kk > 0);
             mma_commit(&bars->kempty[ks]);
             if (last) mma_commit(&bars->dqfull);
@@ -281,7 +281,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
       __syncwarp();
       mbar_wait_drain(&bars->final_[0], 0);
       __syncwarp();
-    } else if (warp == 14) {
+    } else if (warp == CTRL + 2) {
       // ---------------------------------------------------------- MMA issuer of dP
       uint32_t i = 0, item = 0;
       bool ok = true;
@@ -312,73 +312,77 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
       mbar_wait_drain(&bars->final_[1], 0);
       __syncwarp();
     }
-  } else if (warp < 8) {
-    // ------------------------------------------------------------ math: p, ds of half a row
+  } else if (warp < MATH_WARPS) {
+    // ------------------------------------------------------------ math: p, ds of a quarter of a row
     regs_inc<REGS_MATH>();
-    const int hf = warp >> 2, quarter = warp & 3;
+    const int cq = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 64u * hf;
-    uint32_t i = 0, item = 0;
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 32u * cq;
+    uint32_t i = 0;
     bool ok = true;
-    for (WorkQ w = before_first_q(); ok && (w = next_q(a, w)).i < a.total; ++item) {
-      const int64_t n = int64_t(w.qt) * BM + row;
-      const float nl = n < a.Nq ? -lse[(int64_t(w.b) * a.H + w.h) * a.Nq + n] * LOG2E : 0.f;
-      if (!(ok = warp_wait_near(&bars->dready[item & 1], (item >> 1) & 1, abort_flag))) break;
-      const float nd = -d_sm[(item & 1) * BM + row];
+    // An item's lse and D are read while the item before is worked on.
+    WorkQ nx = before_first_q();
+    // (Only loaded there: a product of what is on its way would wait for it.)
+    float lse_next = 0.f, delta_next = 0.f;
+    while (ok && nx.i < a.total) {
+      const WorkQ w = nx;
+      const float nl = -lse_next * LOG2E, nd = -delta_next;
+      nx = next_q(a, w);
+      if (nx.i < a.total) {
+        const int64_t n = int64_t(nx.qt) * BM + row, r = (int64_t(nx.b) * a.H + nx.h) * a.Nq + n;
+        lse_next = delta_next = 0.f;
+        if (n < a.Nq) {
+          lse_next = lse[r];
+          delta_next = delta[r];
+        }
+      }
       const uint64_t c2 = pk(a.c, a.c), nl2 = pk(nl, nl), nd2 = pk(nd, nd);
       for (int j = 0; j < w.nk; ++j, ++i) {
-        const int nv = keys_of(w, j) - 64 * hf;  // keys of this half
+        const int nv = keys_of(w, j) - 32 * cq;  // keys of this quarter
         const uint32_t ts = t_row + Q_S + 128u * (i & 1);
         if (!(ok = warp_wait_near(&bars->sfull[i & 1], (i >> 1) & 1, abort_flag))) break;
         tc_fence_after();
-        // 32 columns at a time, by a loop: unrolled over the row, the kernel's code outgrows the
-        // instruction cache (and the warps wait for instructions, not for data).
         uint32_t s[32];
-        if (nv > 0) tmem_ld_x32(ts, s);
-#pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          const int n = nv - 32 * q;
-          if (n > 0) {
-            tmem_ld_wait();
+        if (nv > 0) {
+          tmem_ld_x32(ts, s);
+          tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 x = upk(fma2(pk(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, nl2));
-              s[e] = __float_as_uint(exp2_approx(x.x));
-              s[e + 1] = __float_as_uint(exp2_approx(x.y));
-            }
-            if (n < 32) {
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = upk(fma2(pk(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, nl2));
+            s[e] = __float_as_uint(exp2_approx(x.x));
+            s[e + 1] = __float_as_uint(exp2_approx(x.y));
+          }
+          if (nv < 32) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (e >= n) s[e] = 0;
-            }
-          }
-          if (q == 0) {
-            if (!(ok = warp_wait_near(&bars->dpfull, i & 1, abort_flag))) break;
-            tc_fence_after();
-          }
-          uint32_t g[32];
-          if (n > 0) {
-            tmem_ld_x32(t_row + Q_DP + 32 * q, g);
-            tmem_ld_wait();
-          }
-          if (q == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->dpfree);
-          }
-          if (n > 0) {
-            uint32_t d[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const uint64_t x = add2(pk(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1])), nd2);
-              const float2 y = upk(mul2(x, pk(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]))));
-              d[e] = pack_bf16(y.x, y.y);
-            }
-            if (n > 32 && q == 0) tmem_ld_x32(ts + 32, s);
-            tmem_st_x16(ts + 16 * q, d);
+            for (int e = 0; e < 32; ++e)
+              if (e >= nv) s[e] = 0;
           }
         }
-        if (!ok) break;
+        if (!(ok = warp_wait_near(&bars->dpfull, i & 1, abort_flag))) break;
+        tc_fence_after();
+        auto free_dp = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->dpfree);
+        };
+        if (nv > 0) {
+          uint32_t d[16], g[16];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            tmem_ld_x16(t_row + Q_DP + 16 * q, g);
+            tmem_ld_wait();
+            if (q == 1) free_dp();
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const uint64_t x = add2(pk(__uint_as_float(g[e]), __uint_as_float(g[e + 1])), nd2);
+              const float2 y = upk(mul2(x, pk(__uint_as_float(s[16 * q + e]), __uint_as_float(s[16 * q + e + 1]))));
+              d[8 * q + e / 2] = pack_bf16(y.x, y.y);
+            }
+          }
+          tmem_st_x16(ts, d);
+        } else {
+          free_dp();
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -386,21 +390,22 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
       }
     }
   } else {
-    // ------------------------------------------------------------ D of the next item, dQ of the last
+    // ------------------------------------------------------------ dQ to memory
     regs_dec<REGS_AUX>();
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t t_dq = tmem + Q_DQ + (static_cast<uint32_t>(quarter * 32) << 16);
-    uint32_t item = 0, done = 0;  // items whose D is computed / whose dQ is stored (those with keys)
-    bool ok = true;
-    auto finish = [&](const WorkQ& w) {
+    uint32_t done = 0;  // items with keys whose dQ is stored
+#pragma unroll 1
+    for (int64_t x = blockIdx.x; x < a.total; x += gridDim.x) {
+      const WorkQ w = get_q(a, x);
       const int64_t n = int64_t(w.qt) * BM + row;
       const int64_t r = (int64_t(w.b) * a.H + w.h) * a.Nq + n;
       __nv_bfloat16* o = dQ + w.b * a.dq.b + w.h * a.dq.h + n * a.dq.n;
       float* po = part + (int64_t(w.split) * a.rows + r) * D;
       const bool in = n < a.Nq;
       if (w.nk > 0) {
-        if (!warp_wait_near(&bars->dqfull, done & 1, abort_flag)) return false;
+        if (!warp_wait_near(&bars->dqfull, done & 1, abort_flag)) break;
         ++done;
         tc_fence_after();
       }
@@ -418,102 +423,40 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->dqfree);
       }
-      return true;
-    };
-    WorkQ prev;
-    bool have = false;
-    for (int64_t x = blockIdx.x; ok && x < a.total; x += gridDim.x) {
-      const WorkQ w = get_q(a, x);
-      if (w.nk > 0) {
-        // A row is read by LPR neighbouring lanes, 16 bytes each, GRP rows of the warp's 32 at a time.
-        constexpr int LPR = D / 8, RPI = 32 / LPR, GRP = 4;
-        const int64_t n0 = int64_t(w.qt) * BM + quarter * 32;
-        const int r_in = lane / LPR, ch = (lane % LPR) * 8;
-        const __nv_bfloat16* po = O + w.b * a.o.b + w.h * a.o.h + ch;
-        const __nv_bfloat16* pg = dO + w.b * a.dout.b + w.h * a.dout.h + ch;
-        float* gd = delta + (int64_t(w.b) * a.H + w.h) * a.Nq;
-#pragma unroll 1
-        for (int r0 = 0; r0 < 32; r0 += GRP * RPI) {
-          uint4 u[GRP], v[GRP];
-#pragma unroll
-          for (int k = 0; k < GRP; ++k) {
-            const int64_t n = n0 + r0 + k * RPI + r_in;
-            u[k] = v[k] = make_uint4(0, 0, 0, 0);
-            if (n < a.Nq) {
-              u[k] = __ldg(reinterpret_cast<const uint4*>(po + n * a.o.n));
-              v[k] = __ldg(reinterpret_cast<const uint4*>(pg + n * a.dout.n));
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < GRP; ++k) {
-            float x = (bf16lo(u[k].x) * bf16lo(v[k].x) + bf16hi(u[k].x) * bf16hi(v[k].x)) +
-                      (bf16lo(u[k].y) * bf16lo(v[k].y) + bf16hi(u[k].y) * bf16hi(v[k].y));
-            x += (bf16lo(u[k].z) * bf16lo(v[k].z) + bf16hi(u[k].z) * bf16hi(v[k].z)) +
-                 (bf16lo(u[k].w) * bf16lo(v[k].w) + bf16hi(u[k].w) * bf16hi(v[k].w));
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-            const int r = r0 + k * RPI + r_in;
-            // Buffer item & 1 was last read by the item two before, whose dQ this warp has stored.
-            if (ch == 0) {
-              d_sm[(item & 1) * BM + quarter * 32 + r] = x;
-              if (w.split == 0 && n0 + r < a.Nq) gd[n0 + r] = x;
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->dready[item & 1]);
-        ++item;
-      }
-      if (x + gridDim.x < a.total) {  // the next item's rows on their way to L2 (a line per lane and step)
-        const WorkQ y = get_q(a, x + gridDim.x);
-        constexpr int LINES = (D * 2 + 127) / 128;
-#pragma unroll
-        for (int k = 0; k < LINES; ++k) {
-          const int e = k * 32 + lane;
-          const int64_t n = int64_t(y.qt) * BM + quarter * 32 + e / LINES;
-          if (y.nk > 0 && n < a.Nq) {
-            prefetch_l2(O + y.b * a.o.b + y.h * a.o.h + n * a.o.n + (e % LINES) * 64);
-            prefetch_l2(dO + y.b * a.dout.b + y.h * a.dout.h + n * a.dout.n + (e % LINES) * 64);
-          }
-        }
-      }
-      if (have) ok = finish(prev);
-      prev = w;
-      have = true;
     }
-    if (ok && have) finish(prev);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 13) tmem_dealloc(tmem, 512);
+  if (warp == CTRL + 1) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------------------------ dK, dV
 template <int DP>
 struct CfgK {
   static constexpr uint32_t TILE = (DP / 64) * HALF;
-  static constexpr int QST = DP == 128 ? 2 : 4;   // Q tiles, and as many dO tiles
+  static constexpr int QST = DP == 128 ? 3 : 4;   // Q tiles: one is held until dK has used it
+  static constexpr int GST = DP == 128 ? 2 : 4;   // dO tiles, and the queries' lse and D
   static constexpr uint32_t OFF_K = 0;
   static constexpr uint32_t OFF_V = TILE;
   static constexpr uint32_t OFF_Q = 2 * TILE;
   static constexpr uint32_t OFF_G = OFF_Q + QST * TILE;
-  static constexpr uint32_t OFF_L = OFF_G + QST * TILE;   // [QST][2][128]: -lse log2(e), -D
-  static constexpr uint32_t OFF_BAR = OFF_L + QST * 2 * BM * 4;
-  static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;
+  static constexpr uint32_t OFF_L = OFF_G + GST * TILE;   // [GST][2][128]: -lse log2(e), -D
+  static constexpr uint32_t OFF_BAR = OFF_L + GST * 2 * BM * 4;
+  static constexpr uint32_t SMEM = OFF_BAR + 384;  // (the block's shared memory starts on a 1 KB boundary)
 };
 static_assert(CfgK<128>::SMEM <= 232448 && CfgK<64>::SMEM <= 232448, "shared memory budget");
 
 template <int DP>
 struct BarsK {
   uint64_t qfull[CfgK<DP>::QST], qempty[CfgK<DP>::QST];
-  uint64_t gfull[CfgK<DP>::QST], gempty[CfgK<DP>::QST];
-  uint64_t lfull[CfgK<DP>::QST], lempty[CfgK<DP>::QST];
+  uint64_t gfull[CfgK<DP>::GST], gempty[CfgK<DP>::GST];
+  uint64_t lfull[CfgK<DP>::GST], lempty[CfgK<DP>::GST];
   uint64_t kfull, kempty, vfull, vempty;
   uint64_t sfull, pready, dpfull, dsready, accfull, accfree, final_[2];
   uint32_t tmem_base;
   int abort_flag;
 };
-static_assert(sizeof(BarsK<64>) <= 512, "barrier block too large");
+static_assert(sizeof(BarsK<64>) <= 384, "barrier block too large");
 
 constexpr uint32_t K_S = 0, K_DP = 128, K_DV = 256, K_DK = 384;
 
@@ -563,8 +506,11 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
            const __grid_constant__ Args a, const float* __restrict__ lse, const float* __restrict__ delta,
            float* __restrict__ part_k, float* __restrict__ part_v) {
   using C = CfgK<DP>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align_smem_1k(smem_raw);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // (never: no static shared memory stands before it)
+    if (threadIdx.x == 0) atomicOr(&g_la_error, ERR_SMEM_ALIGN);
+    return;
+  }
   BarsK<DP>* bars = reinterpret_cast<BarsK<DP>*>(smem + C::OFF_BAR);
   const uint32_t sbase = smem_u32(smem);
   float* l_sm = reinterpret_cast<float*>(smem + C::OFF_L);
@@ -575,31 +521,33 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     for (int s = 0; s < C::QST; ++s) {
       mbar_init(&bars->qfull[s], 1);
       mbar_init(&bars->qempty[s], 2);  // both issuers
+    }
+    for (int s = 0; s < C::GST; ++s) {
       mbar_init(&bars->gfull[s], 1);
       mbar_init(&bars->gempty[s], 2);
       mbar_init(&bars->lfull[s], 4);
-      mbar_init(&bars->lempty[s], 8);
+      mbar_init(&bars->lempty[s], MATH_WARPS);
     }
     mbar_init(&bars->kfull, 1);
     mbar_init(&bars->kempty, 1);
     mbar_init(&bars->vfull, 1);
     mbar_init(&bars->vempty, 1);
     mbar_init(&bars->sfull, 1);
-    mbar_init(&bars->pready, 8);
+    mbar_init(&bars->pready, MATH_WARPS);
     mbar_init(&bars->dpfull, 1);
-    mbar_init(&bars->dsready, 8);
+    mbar_init(&bars->dsready, MATH_WARPS);
     mbar_init(&bars->accfull, 2);
-    mbar_init(&bars->accfree, 8);
+    mbar_init(&bars->accfree, MATH_WARPS);
     mbar_init(&bars->final_[0], 1);
     mbar_init(&bars->final_[1], 1);
     bars->abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 13) {
+  if (warp == CTRL + 1) {
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
   }
-  if (warp == 12 && lane == 0) {
+  if (warp == CTRL && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmG);
     tma_prefetch_desc(&tmK);
@@ -612,9 +560,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
   pdl_trigger();
   pdl_wait();  // the gathered keys, and D from the dQ kernel
 
-  if (warp >= 12) {
+  if (warp >= CTRL) {
     regs_dec<REGS_CTRL>();
-    if (warp == 12 && lane == 0) {
+    if (warp == CTRL && lane == 0) {
       // ---------------------------------------------------------- TMA producer
       uint32_t qi = 0, items = 0;
       uint32_t k_out = 0, v_out = 0;
@@ -626,8 +574,8 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         for (int j = 0; ok && j < w.nq; ++j, ++qi) {
           const int32_t it = w.t0 + j, hq = it / a.q_tiles;
           const int32_t h = w.h * a.group + hq, n = (it - hq * a.q_tiles) * BM;
-          const uint32_t s = qi % C::QST, ph = ((qi / C::QST) & 1) ^ 1;
-          if (!(ok = mbar_wait_near(&bars->qempty[s], ph, abort_flag))) break;
+          const uint32_t s = qi % C::QST, sg = qi % C::GST;
+          if (!(ok = mbar_wait_near(&bars->qempty[s], ((qi / C::QST) & 1) ^ 1, abort_flag))) break;
           load_tile<DP>(smem + C::OFF_Q + s * C::TILE, &tmQ, n, h, w.b, &bars->qfull[s]);
           if (j == 0) {
             ok = mbar_wait_near(&bars->vempty, (items & 1) ^ 1, abort_flag);
@@ -636,27 +584,27 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
               ++v_out;
             }
           }
-          if (ok) ok = mbar_wait_near(&bars->gempty[s], ph, abort_flag);
+          if (ok) ok = mbar_wait_near(&bars->gempty[sg], ((qi / C::GST) & 1) ^ 1, abort_flag);
           if (!ok) {
             mbar_wait_drain(&bars->qfull[s], (qi / C::QST) & 1);
             break;
           }
-          load_tile<DP>(smem + C::OFF_G + s * C::TILE, &tmG, n, h, w.b, &bars->gfull[s]);
+          load_tile<DP>(smem + C::OFF_G + sg * C::TILE, &tmG, n, h, w.b, &bars->gfull[sg]);
         }
         if (!ok) break;
       }
       if (*abort_flag) {
         // Let every copy still in flight land before the CTA's shared memory goes away.
         drain(bars->qfull, C::QST, qi);
-        drain(bars->gfull, C::QST, qi);
+        drain(bars->gfull, C::GST, qi);
         drain(&bars->kfull, 1, k_out);
         drain(&bars->vfull, 1, v_out);
       }
-    } else if (warp == 13 || warp == 14) {
+    } else if (warp == CTRL + 1 || warp == CTRL + 2) {
       // ---------------------------------------------------------- MMA issuers (converged warps)
-      // 13: S^T and dV, 14: dP^T and dK.  Each walks the same steps: the product of this step's p (ds)
+      // The first: S^T and dV, the second: dP^T and dK.  Each walks the same steps: the product of this step's p (ds)
       // first, then the scores (dP) of the next step, which overwrite it.
-      const bool sv = warp == 13;
+      const bool sv = warp == CTRL + 1;
       uint32_t i = 0, items = 0;
       bool ok = true;
       const uint32_t id_s = idesc_bf16_f32(BM, BN, false, false), id_d = idesc_bf16_f32(BM, DP, false, true);
@@ -671,6 +619,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       uint64_t* fixed_empty = sv ? &bars->kempty : &bars->vempty;
       uint64_t* in_done = sv ? &bars->sfull : &bars->dpfull;
       uint64_t* ready = sv ? &bars->pready : &bars->dsready;
+      const uint32_t in_st = sv ? C::QST : C::GST, out_st = sv ? C::GST : C::QST;
       const uint64_t fd = tile::desc_k(fixed, 0);
       auto issue_in = [&](bool last, uint32_t s) {
         tile::mma_kk<DP>(t_in, fd, tile::desc_k(in + s * C::TILE, 0), id_s);
@@ -693,20 +642,22 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         for (int j = 0; ok && j < w.nq; ++j, ++i) {
           const bool last = j + 1 == w.nq, more = !last || nx.i < a.total;
           const bool last2 = last ? nx.nq == 1 : j + 2 == w.nq;
-          const uint32_t s = i % C::QST, s2 = (i + 1) % C::QST;
+          const uint32_t s = i % out_st, s2 = (i + 1) % in_st;
           const uint64_t od = tile::desc_mn(out + s * C::TILE, 0);
           if (more) {
             if (last) ok = warp_wait_near(fixed_full, (items + 1) & 1, abort_flag);
-            ok = ok && warp_wait_near(&in_full[s2], ((i + 1) / C::QST) & 1, abort_flag);
+            ok = ok && warp_wait_near(&in_full[s2], ((i + 1) / in_st) & 1, abort_flag);
           }
           if (j == 0) ok = ok && warp_wait_near(&bars->accfree, (items & 1) ^ 1, abort_flag);
           ok = ok && warp_wait_near(ready, i & 1, abort_flag);
+          // The next p waits for the next S^T: dV and S^T have the tensor cores to themselves first.
+          if (!sv && more) ok = ok && warp_wait_near(&bars->sfull, (i + 1) & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < BM / 16; ++kk)
-              mma_bf16_ts(t_acc, t_in + 8u * (kk & 3) + 64u * (kk >> 2), od + tile::step_mn(kk), id_d, j > 0 || kk > 0);
+              mma_bf16_ts(t_acc, t_in + 8u * (kk & 1) + 32u * (kk >> 1), od + tile::step_mn(kk), id_d, j > 0 || kk > 0);
             mma_commit(&out_empty[s]);
             if (last) mma_commit(&bars->accfull);
             if (more) issue_in(last2, s2);
@@ -715,75 +666,69 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         }
         ++items;
       }
-      if (elect_one()) mma_commit(&bars->final_[warp - 13]);
+      if (elect_one()) mma_commit(&bars->final_[sv ? 0 : 1]);
       __syncwarp();
-      mbar_wait_drain(&bars->final_[warp - 13], 0);
+      mbar_wait_drain(&bars->final_[sv ? 0 : 1], 0);
       __syncwarp();
     }
-  } else if (warp < 8) {
-    // ------------------------------------------------------------ math: p, ds of half a key's row
+  } else if (warp < MATH_WARPS) {
+    // ------------------------------------------------------------ math: p, ds of a quarter of a key's row
     regs_inc<REGS_MATH>();
-    const int hf = warp >> 2, quarter = warp & 3;
+    const int cq = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t ts = t_row + K_S + 64u * hf, tp = t_row + K_DP + 64u * hf;
+    const uint32_t ts = t_row + K_S + 32u * cq, tp = t_row + K_DP + 32u * cq;
     const uint64_t c2 = pk(a.c, a.c);
     uint32_t i = 0, item = 0;
     bool ok = true;
     for (WorkK w = before_first_k(); ok && (w = next_k(a, w)).i < a.total; ++item) {
       for (int j = 0; j < w.nq; ++j, ++i) {
-        const uint32_t s_l = i % C::QST;
-        const uint32_t la_ = sbase + C::OFF_L + (s_l * 2 * BM + 64 * hf) * 4, ld_ = la_ + BM * 4;
-        if (!(ok = warp_wait_near(&bars->lfull[s_l], (i / C::QST) & 1, abort_flag))) break;
+        const uint32_t s_l = i % C::GST;
+        const uint32_t la_ = sbase + C::OFF_L + (s_l * 2 * BM + 32 * cq) * 4, ld_ = la_ + BM * 4;
+        if (!(ok = warp_wait_near(&bars->lfull[s_l], (i / C::GST) & 1, abort_flag))) break;
         if (!(ok = warp_wait_near(&bars->sfull, i & 1, abort_flag))) break;
         tc_fence_after();
-        uint32_t s[2][32];
-        tmem_ld_x32(ts, s[0]);
-        tmem_ld_x32(ts + 32, s[1]);
+        uint32_t s[32], d[16];
+        tmem_ld_x32(ts, s);
         tmem_ld_wait();
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t p[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 nl = lds128f(la_ + (32 * q + e) * 4);
-            const float2 x = upk(fma2(pk(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])), c2, pk(nl.x, nl.y)));
-            const float2 y = upk(fma2(pk(__uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3])), c2, pk(nl.z, nl.w)));
-            const float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y), p2 = exp2_approx(y.x), p3 = exp2_approx(y.y);
-            s[q][e] = __float_as_uint(p0);
-            s[q][e + 1] = __float_as_uint(p1);
-            s[q][e + 2] = __float_as_uint(p2);
-            s[q][e + 3] = __float_as_uint(p3);
-            p[e / 2] = pack_bf16(p0, p1);
-            p[e / 2 + 1] = pack_bf16(p2, p3);
-          }
-          tmem_st_x16(ts + 16 * q, p);
+        for (int e = 0; e < 32; e += 4) {
+          const float4 nl = lds128f(la_ + e * 4);
+          const float2 x = upk(fma2(pk(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, pk(nl.x, nl.y)));
+          const float2 y = upk(fma2(pk(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), c2, pk(nl.z, nl.w)));
+          const float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y), p2 = exp2_approx(y.x), p3 = exp2_approx(y.y);
+          s[e] = __float_as_uint(p0);
+          s[e + 1] = __float_as_uint(p1);
+          s[e + 2] = __float_as_uint(p2);
+          s[e + 3] = __float_as_uint(p3);
+          d[e / 2] = pack_bf16(p0, p1);
+          d[e / 2 + 1] = pack_bf16(p2, p3);
         }
+        tmem_st_x16(ts, d);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->pready);
         if (!(ok = warp_wait_near(&bars->dpfull, i & 1, abort_flag))) break;
         tc_fence_after();
-        uint32_t g[2][32];
-        tmem_ld_x32(tp, g[0]);
-        tmem_ld_x32(tp + 32, g[1]);
-        tmem_ld_wait();
+        uint32_t g[16];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          uint32_t d[16];
+          tmem_ld_x16(tp + 16 * q, g);
+          tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 nd = lds128f(ld_ + (32 * q + e) * 4);
-            const float2 x = upk(mul2(add2(pk(__uint_as_float(g[q][e]), __uint_as_float(g[q][e + 1])), pk(nd.x, nd.y)),
-                                      pk(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]))));
-            const float2 y = upk(mul2(add2(pk(__uint_as_float(g[q][e + 2]), __uint_as_float(g[q][e + 3])), pk(nd.z, nd.w)),
-                                      pk(__uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3]))));
-            d[e / 2] = pack_bf16(x.x, x.y);
-            d[e / 2 + 1] = pack_bf16(y.x, y.y);
+          for (int e = 0; e < 16; e += 4) {
+            const float4 nd = lds128f(ld_ + (16 * q + e) * 4);
+            const int k = 16 * q + e;
+            const float2 x = upk(mul2(add2(pk(__uint_as_float(g[e]), __uint_as_float(g[e + 1])), pk(nd.x, nd.y)),
+                                      pk(__uint_as_float(s[k]), __uint_as_float(s[k + 1]))));
+            const float2 y = upk(mul2(add2(pk(__uint_as_float(g[e + 2]), __uint_as_float(g[e + 3])), pk(nd.z, nd.w)),
+                                      pk(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]))));
+            d[k / 2] = pack_bf16(x.x, x.y);
+            d[k / 2 + 1] = pack_bf16(y.x, y.y);
           }
-          tmem_st_x16(tp + 16 * q, d);
         }
+        tmem_st_x16(tp, d);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -793,15 +738,16 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         }
       }
       if (!ok) break;
-      // the item's sums: warps 0-3 store dV, warps 4-7 dK, a key per thread
+      // the item's sums, a key per thread: warps 0-7 store dV, 8-15 dK, half of the channels each
       if (!(ok = warp_wait_near(&bars->accfull, item & 1, abort_flag))) break;
       tc_fence_after();
       const int64_t n = int64_t(w.kt) * BN + row;
-      const float f = hf == 0 ? 1.f : a.scale;
-      float* out = (hf == 0 ? part_v : part_k) + (int64_t(w.split) * a.keys + (int64_t(w.b) * a.Hkv + w.h) * a.Nk + n) * D;
-      const uint32_t ta = t_row + (hf == 0 ? K_DV : K_DK);
+      const bool is_v = cq < 2;
+      const float f = is_v ? 1.f : a.scale;
+      float* out = (is_v ? part_v : part_k) + (int64_t(w.split) * a.keys + (int64_t(w.b) * a.Hkv + w.h) * a.Nk + n) * D;
+      const uint32_t ta = t_row + (is_v ? K_DV : K_DK);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = cq & 1; c < D / 32; c += 2) {
         uint32_t v[32];
         tmem_ld_x32(ta + 32 * c, v);
         tmem_ld_wait();
@@ -819,13 +765,13 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     bool ok = true;
     for (WorkK w = before_first_k(); ok && (w = next_k(a, w)).i < a.total;) {
       for (int j = 0; j < w.nq; ++j, ++i) {
-        const uint32_t s = i % C::QST;
+        const uint32_t s = i % C::GST;
         const int32_t it = w.t0 + j, hq = it / a.q_tiles;
         const int64_t n = int64_t(it - hq * a.q_tiles) * BM + q;
         const int64_t r = (int64_t(w.b) * a.H + w.h * a.group + hq) * a.Nq + n;
         // queries past the end: p = 2^-inf = 0
         const float nl = n < a.Nq ? -lse[r] * LOG2E : xs::NEG_INF, nd = n < a.Nq ? -delta[r] : 0.f;
-        if (!(ok = warp_wait_near(&bars->lempty[s], ((i / C::QST) & 1) ^ 1, abort_flag))) break;
+        if (!(ok = warp_wait_near(&bars->lempty[s], ((i / C::GST) & 1) ^ 1, abort_flag))) break;
         l_sm[s * 2 * BM + q] = nl;
         l_sm[s * 2 * BM + BM + q] = nd;
         __syncwarp();
@@ -835,7 +781,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 13) tmem_dealloc(tmem, 512);
+  if (warp == CTRL + 1) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace xb

@@ -59,7 +59,7 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t stri
     if (r < valid && (!ok || ok[r])) {
       const ln::Pack<T, VEC> p = *reinterpret_cast<const ln::Pack<T, VEC>*>(src + r * stride + c);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) f[i] = ln::as_f(p.v[i]);
+      for (int i = 0; i < VEC; ++i) f[i] = p.get(i);
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) f[i] = 0.f;
@@ -359,23 +359,41 @@ join_kernel(const __grid_constant__ Args a, const float* __restrict__ part_o, co
   if (lse && threadIdx.x == 0) lse[row] = L > 0.f ? M + logf(L) : NEG_INF;
 }
 
-// D_i = dO_i . O_i for every query row, one warp per row.
+// D_i = dO_i . O_i for every query row.  A block has consecutive rows of a head; a row belongs to
+// D * size / 16 neighbouring lanes, and DELTA_ROWS rows of each lane are in flight.
+constexpr int DELTA_ROWS = 8;
+template <int D, typename T>
+__host__ __device__ constexpr int delta_rows() { return THREADS / (D * int(sizeof(T)) / 16) * DELTA_ROWS; }  // per block
+
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS)
 delta_kernel(const __grid_constant__ Args a, const T* __restrict__ O, const T* __restrict__ dO, float* __restrict__ delta) {
+  constexpr int VEC = 16 / int(sizeof(T)), LPR = D / VEC, STEP = THREADS / LPR;
   pdl_trigger();
   pdl_wait();  // (it reads nothing of the gather's, but the kernels after it wait for this one only)
-  const int64_t row = int64_t(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= a.rows) return;
-  const int64_t n = row % a.Nq, bh = row / a.Nq, b = bh / a.H, h = bh % a.H;
-  const T* o = O + b * a.o.b + h * a.o.h + n * a.o.n;
-  const T* g = dO + b * a.dout.b + h * a.dout.h + n * a.dout.n;
-  float s = 0.f;
+  const uint32_t tiles = static_cast<uint32_t>((a.Nq + delta_rows<D, T>() - 1) / delta_rows<D, T>());
+  const uint32_t bh = blockIdx.x / tiles, b = bh / static_cast<uint32_t>(a.H), h = bh - b * static_cast<uint32_t>(a.H);
+  const int64_t n0 = int64_t(blockIdx.x - bh * tiles) * delta_rows<D, T>() + threadIdx.x / LPR;
+  const int c = (threadIdx.x % LPR) * VEC;
+  const T* po = O + b * a.o.b + h * a.o.h + n0 * a.o.n + c;
+  const T* pg = dO + b * a.dout.b + h * a.dout.h + n0 * a.dout.n + c;
+  ln::Pack<T, VEC> o[DELTA_ROWS], g[DELTA_ROWS];
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) s += ln::as_f(o[lane + 32 * c]) * ln::as_f(g[lane + 32 * c]);
-  s = ln::warp_sum(s);
-  if (lane == 0) delta[row] = s;
+  for (int k = 0; k < DELTA_ROWS; ++k)
+    if (n0 + k * STEP < a.Nq) {
+      o[k] = *reinterpret_cast<const ln::Pack<T, VEC>*>(po + int64_t(k) * STEP * a.o.n);
+      g[k] = *reinterpret_cast<const ln::Pack<T, VEC>*>(pg + int64_t(k) * STEP * a.dout.n);
+    }
+#pragma unroll
+  for (int k = 0; k < DELTA_ROWS; ++k) {
+    const int64_t n = n0 + k * STEP;
+    float s = 0.f;
+    if (n < a.Nq)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s += o[k].get(e) * g[k].get(e);
+    s = ln::lanes_sum<LPR>(s);
+    if (n < a.Nq && c == 0) delta[bh * a.Nq + n] = s;
+  }
 }
 
 template <int D>

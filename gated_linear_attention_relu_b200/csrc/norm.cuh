@@ -21,22 +21,36 @@
 namespace la {
 namespace ln {
 
-// VEC elements of a row, as loaded: 16 bytes where rows are 16-byte aligned, else one element.
+// VEC elements of a row, as loaded: 16 bytes where rows are 16-byte aligned, else one element.  (bf16
+// stays in words of two: as eight elements the compiler gives it eight registers.)
 template <typename T, int VEC>
 struct Pack {
   T v[VEC];
+  __device__ __forceinline__ float get(int e) const { return static_cast<float>(v[e]); }
+  __device__ __forceinline__ void set(const float (&f)[VEC]) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = T(f[e]);
+  }
 };
 template <>
 struct __align__(16) Pack<__nv_bfloat16, 8> {
-  __nv_bfloat16 v[8];
+  uint32_t v[4];
+  __device__ __forceinline__ float get(int e) const { return (e & 1) ? bf16hi(v[e >> 1]) : bf16lo(v[e >> 1]); }
+  __device__ __forceinline__ void set(const float (&f)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) v[e >> 1] = pack_bf16(f[e], f[e + 1]);
+  }
 };
 template <>
 struct __align__(16) Pack<float, 4> {
   float v[4];
+  __device__ __forceinline__ float get(int e) const { return v[e]; }
+  __device__ __forceinline__ void set(const float (&f)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = f[e];
+  }
 };
 
-__device__ __forceinline__ float as_f(float x) { return x; }
-__device__ __forceinline__ float as_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float& d, float x) { d = x; }
 __device__ __forceinline__ void put(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
 
@@ -124,7 +138,7 @@ forward_short(const Args a, const T* x, const float* __restrict__ weight, const 
     for (int i = 0; i < NV; ++i)
       if (in && (i * LPR + li) * VEC < a.cols) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s += as_f(p[u][i].v[e]);
+        for (int e = 0; e < VEC; ++e) s += p[u][i].get(e);
       }
     const float mu = lanes_sum<LPR>(s) * a.inv_cols;
     s = 0.f;
@@ -133,7 +147,7 @@ forward_short(const Args a, const T* x, const float* __restrict__ weight, const 
       if (in && (i * LPR + li) * VEC < a.cols) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float d = as_f(p[u][i].v[e]) - mu;
+          const float d = p[u][i].get(e) - mu;
           s += d * d;
         }
       }
@@ -151,13 +165,14 @@ forward_short(const Args a, const T* x, const float* __restrict__ weight, const 
       float w[VEC], b[VEC];
       if (weight) load_w<VEC>(weight + g + c, w);
       if (bias) load_w<VEC>(bias + g + c, b);
+      float t[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        float v = (as_f(p[u][i].v[e]) - mu) * r;
-        if (weight) v *= w[e];
-        if (bias) v += b[e];
-        put(p[u][i].v[e], v);
+        t[e] = (p[u][i].get(e) - mu) * r;
+        if (weight) t[e] *= w[e];
+        if (bias) t[e] += b[e];
       }
+      p[u][i].set(t);
       store_pack(y + row * a.sy + c, p[u][i]);
     }
   }
@@ -214,7 +229,7 @@ backward_short(const Args a, int parts, const T* x, const T* dy, const float* __
         if (in && (i * LPR + li) * VEC < a.cols) {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            const float xh = (as_f(px[u][i].v[e]) - mu[u]) * r[u], d = as_f(pd[u][i].v[e]);
+            const float xh = (px[u][i].get(e) - mu[u]) * r[u], d = pd[u][i].get(e);
             dw[i][e] += d * xh;
             db[i][e] += d;
             s1 += d * w[i][e];
@@ -226,11 +241,13 @@ backward_short(const Args a, int parts, const T* x, const T* dy, const float* __
       for (int i = 0; i < NV; ++i) {
         const int c = (i * LPR + li) * VEC;
         if (!in || c >= a.cols) continue;
+        float t[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float xh = (as_f(px[u][i].v[e]) - mu[u]) * r[u];
-          put(px[u][i].v[e], r[u] * (as_f(pd[u][i].v[e]) * w[i][e] - c1 - xh * c2));
+          const float xh = (px[u][i].get(e) - mu[u]) * r[u];
+          t[e] = r[u] * (pd[u][i].get(e) * w[i][e] - c1 - xh * c2);
         }
+        px[u][i].set(t);
         store_pack(dx + row * a.sdx + c, px[u][i]);
       }
     }
@@ -335,7 +352,7 @@ forward_long(const Args a, int parts, int stages, const T* x, const float* __res
     for (int i = 0; i < NV; ++i)
       if ((i * 32 * WPR + int(threadIdx.x)) * VEC < a.cols) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v += as_f(p[i].v[e]);
+        for (int e = 0; e < VEC; ++e) v += p[i].get(e);
       }
     const float mu = block_sum2<WPR>(v, 0.f, red[0]).x * a.inv_cols;
     if constexpr (RING) {  // every thread has its part of the row: the stage can take another one
@@ -351,7 +368,7 @@ forward_long(const Args a, int parts, int stages, const T* x, const float* __res
       if ((i * 32 * WPR + int(threadIdx.x)) * VEC < a.cols) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float d = as_f(p[i].v[e]) - mu;
+          const float d = p[i].get(e) - mu;
           v += d * d;
         }
       }
@@ -364,13 +381,14 @@ forward_long(const Args a, int parts, int stages, const T* x, const float* __res
     for (int i = 0; i < NV; ++i) {
       const int c = (i * 32 * WPR + threadIdx.x) * VEC;
       if (c >= a.cols) continue;
+      float t[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        float t = (as_f(p[i].v[e]) - mu) * r;
-        if (weight) t *= w[i][e];
-        if (bias) t += b[i][e];
-        put(p[i].v[e], t);
+        t[e] = (p[i].get(e) - mu) * r;
+        if (weight) t[e] *= w[i][e];
+        if (bias) t[e] += b[i][e];
       }
+      p[i].set(t);
       store_pack(y + row * a.sy + c, p[i]);
     }
   }
@@ -440,7 +458,7 @@ backward_long(const Args a, int parts, int stages, const T* x, const T* dy, cons
       if ((i * 32 * WPR + int(threadIdx.x)) * VEC < a.cols) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float xh = (as_f(px[i].v[e]) - mu) * r, d = as_f(pd[i].v[e]);
+          const float xh = (px[i].get(e) - mu) * r, d = pd[i].get(e);
           dw[i][e] += d * xh;
           db[i][e] += d;
           s1 += d * w[i][e];
@@ -466,11 +484,13 @@ backward_long(const Args a, int parts, int stages, const T* x, const T* dy, cons
     for (int i = 0; i < NV; ++i) {
       const int c = (i * 32 * WPR + threadIdx.x) * VEC;
       if (c >= a.cols) continue;
+      float t[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float xh = (as_f(px[i].v[e]) - mu0) * r0;
-        put(px[i].v[e], r0 * (as_f(pd[i].v[e]) * w[i][e] - c1 - xh * c2));
+        const float xh = (px[i].get(e) - mu0) * r0;
+        t[e] = r0 * (pd[i].get(e) * w[i][e] - c1 - xh * c2);
       }
+      px[i].set(t);
       store_pack(dx + row * a.sdx + c, px[i]);
     }
   }

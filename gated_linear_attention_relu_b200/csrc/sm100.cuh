@@ -238,8 +238,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// Requests a line of global memory into L2.
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // 16 bytes global -> shared, asynchronously (the first `bytes` of them; the rest become 0).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -440,25 +438,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-// 2^x of two values on the FMA pipe, for x <= 127 (below -126: 2^-126).  x = j + f with j the nearest
-// integer (adding and taking away 1.5 2^23 rounds to it, and leaves it in the low bits), 2^f by the
-// degree-5 polynomial with the least relative error on [-1/2, 1/2] (Remez exchange; 2.1e-7 with its
-// fp32 rounding, as close as ex2.approx), and j added to the exponent.
-__device__ __forceinline__ float2 exp2_poly2(uint64_t x2) {
-  float2 x = upk(x2);
-  x2 = pk(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
-  constexpr float M = 12582912.f;
-  const uint64_t t = add2(x2, pk(M, M));
-  const uint64_t f = add2(x2, fma2(t, pk(-1.f, -1.f), pk(M, M)));
-  uint64_t p = fma2(f, pk(0x1.5c08e6p-10f, 0x1.5c08e6p-10f), pk(0x1.3d0c52p-7f, 0x1.3d0c52p-7f));
-  p = fma2(f, p, pk(0x1.c6b6e4p-5f, 0x1.c6b6e4p-5f));
-  p = fma2(f, p, pk(0x1.ebf918p-3f, 0x1.ebf918p-3f));
-  p = fma2(f, p, pk(0x1.62e428p-1f, 0x1.62e428p-1f));
-  p = fma2(f, p, pk(0x1.000002p+0f, 0x1.000002p+0f));
-  const float2 tt = upk(t), pp = upk(p);
-  return make_float2(__uint_as_float(__float_as_uint(pp.x) + (__float_as_uint(tt.x) << 23)),
-                     __uint_as_float(__float_as_uint(pp.y) + (__float_as_uint(tt.y) << 23)));
 }
 // The larger of three.
 __device__ __forceinline__ float max3(float a, float b, float c) {
