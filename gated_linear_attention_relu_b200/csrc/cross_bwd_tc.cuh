@@ -58,9 +58,11 @@ struct Args {
 template <int DP>
 struct CfgQ {
   static constexpr uint32_t TILE = (DP / 64) * HALF;
-  static constexpr int QST = DP == 128 ? 3 : 4;   // Q and dO tiles, in turn
+  // Q and dO tiles of this item and the next (from HBM); K and V come from L2, and dP of the next step
+  // leaves a V tile the time of a step's math to arrive in.
+  static constexpr int QST = 4;
   static constexpr int KST = DP == 128 ? 2 : 4;
-  static constexpr int VST = DP == 128 ? 2 : 4;
+  static constexpr int VST = DP == 128 ? 1 : 4;
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_K = QST * TILE;
   static constexpr uint32_t OFF_V = OFF_K + KST * TILE;

@@ -47,35 +47,39 @@ __device__ __forceinline__ int64_t key_limit(const Args& a, int64_t b) {
 template <int D>
 __host__ __device__ constexpr int row_stride() { return D + 4; }  // floats: 16-byte rows whose float4 columns spread over the banks
 
-// 64 rows of D channels to shared memory as fp32; rows outside [0, valid) and unattended ones
-// (ok given: ok[r] = 0) become 0, whatever memory holds there.
+// 64 rows of D channels on their way to shared memory: fetch() starts the loads (rows outside [0,
+// valid) become 0 and are not read), stash() puts them there as fp32.  What is fetched before a tile's
+// products and stashed after them costs no waiting.
 template <int D, typename T>
-__device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t stride, int valid, const uint8_t* ok) {
-  constexpr int VEC = sizeof(T) == 2 ? 8 : 4;
-  constexpr int PR = D / VEC;
-  for (int e = threadIdx.x; e < BT * PR; e += THREADS) {
-    const int r = e / PR, c = (e % PR) * VEC;
-    float f[VEC];
-    if (r < valid && (!ok || ok[r])) {
-      const ln::Pack<T, VEC> p = *reinterpret_cast<const ln::Pack<T, VEC>*>(src + r * stride + c);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) f[i] = p.get(i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) f[i] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < VEC; i += 4)
-      *reinterpret_cast<float4*>(dst + r * row_stride<D>() + c + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
-  }
-}
+struct Tile {
+  static constexpr int VEC = 16 / int(sizeof(T)), PR = D / VEC, N = BT * PR / THREADS;
+  ln::Pack<T, VEC> p[N];
 
-// ok[j] = key k0 + j is attended.
-__device__ __forceinline__ void load_ok(const Args& a, int64_t b, int64_t k0, int64_t limit, uint8_t* ok) {
-  if (threadIdx.x < BT) {
-    const int64_t j = k0 + threadIdx.x;
-    ok[threadIdx.x] = j < limit && (!a.mask || a.mask[b * a.Nk + j] != 0);
+  __device__ __forceinline__ void fetch(const T* src, int64_t stride, int valid) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int e = threadIdx.x + k * THREADS, r = e / PR;
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (r < valid) u = __ldg(reinterpret_cast<const uint4*>(src + r * stride + (e % PR) * VEC));
+      p[k] = *reinterpret_cast<const ln::Pack<T, VEC>*>(&u);
+    }
   }
+  __device__ __forceinline__ void stash(float* dst) const {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int e = threadIdx.x + k * THREADS;
+      float* to = dst + e / PR * row_stride<D>() + (e % PR) * VEC;
+#pragma unroll
+      for (int i = 0; i < VEC; i += 4)
+        *reinterpret_cast<float4*>(to + i) = make_float4(p[k].get(i), p[k].get(i + 1), p[k].get(i + 2), p[k].get(i + 3));
+    }
+  }
+};
+template <int D, typename T>
+__device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t stride, int valid) {
+  Tile<D, T> t;
+  t.fetch(src, stride, valid);
+  t.stash(dst);
 }
 
 // s[ii][jj] = A[ty + 16 ii] . B[tx + 16 jj]
@@ -190,7 +194,7 @@ __device__ __forceinline__ Where where(const Args& a, int64_t tiles, int64_t hea
 }
 
 template <int D>
-__host__ __device__ constexpr size_t fwd_smem() { return (2 * BT * row_stride<D>() + BT * PS) * 4 + BT; }
+__host__ __device__ constexpr size_t fwd_smem() { return (2 * BT * row_stride<D>() + BT * PS) * 4; }
 
 // Forward.  part_o [splits][rows][D] (sums over the split's keys) and part_ml [splits][rows] (the
 // split's maximum and sum) when splits > 1, else O and lse themselves.
@@ -203,7 +207,6 @@ forward_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T*
   float* qs = sm;
   float* kv = qs + BT * row_stride<D>();
   float* ps = kv + BT * row_stride<D>();
-  uint8_t* ok = reinterpret_cast<uint8_t*>(ps + BT * PS);
   pdl_trigger();
   const Where w = where(a, a.q_tiles, a.H);
   const int64_t kh = w.h / a.group, q0 = w.tile * BT;
@@ -215,7 +218,7 @@ forward_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T*
   int64_t k_end = k_begin + int64_t(a.tiles_per_split) * BT;
   if (k_end > limit) k_end = limit;
 
-  load_tile<D>(qs, Q + w.b * a.q.b + w.h * a.q.h + q0 * a.q.n, a.q.n, qn, static_cast<const uint8_t*>(nullptr));
+  load_tile<D>(qs, Q + w.b * a.q.b + w.h * a.q.h + q0 * a.q.n, a.q.n, qn);
   float m[4], l[4];
   uint64_t acc[4][D / 32];
 #pragma unroll
@@ -225,12 +228,16 @@ forward_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T*
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) acc[i][k] = 0;
   }
+  // (at D = 128 a second tile of registers would leave one block an SM)
+  Tile<D, T> next;
+  const T* kb = K + w.b * a.k.b + kh * a.k.h;
+  const T* vb = V + w.b * a.v.b + kh * a.v.h;
+  if (k_begin < k_end) next.fetch(kb + k_begin * a.k.n, a.k.n, static_cast<int>(k_end - k_begin < BT ? k_end - k_begin : BT));
   for (int64_t k0 = k_begin; k0 < k_end; k0 += BT) {
     const int kn = static_cast<int>(k_end - k0 < BT ? k_end - k0 : BT);
-    load_ok(a, w.b, k0, limit, ok);
-    __syncthreads();  // (also: the last tile's products have been read)
-    load_tile<D>(kv, K + w.b * a.k.b + kh * a.k.h + k0 * a.k.n, a.k.n, kn, ok);
+    next.stash(kv);
     __syncthreads();
+    next.fetch(vb + k0 * a.v.n, a.v.n, kn);
     float s[4][4];
     mm_nt<D>(qs, kv, ty, tx, s);
     float corr[4];
@@ -239,7 +246,7 @@ forward_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T*
       float mx = NEG_INF;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[i][j] = ok[tx + 16 * j] ? s[i][j] * a.scale : NEG_INF;
+        s[i][j] = tx + 16 * j < kn ? s[i][j] * a.scale : NEG_INF;
         mx = fmaxf(mx, s[i][j]);
       }
       const float m_new = fmaxf(m[i], lane16_max(mx));
@@ -256,8 +263,10 @@ forward_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T*
       l[i] = l[i] * corr[i] + lane16_sum(sum);
     }
     __syncthreads();  // the keys have been read
-    load_tile<D>(kv, V + w.b * a.v.b + kh * a.v.h + k0 * a.v.n, a.v.n, kn, ok);
+    next.stash(kv);
     __syncthreads();
+    const int64_t k1 = k0 + BT;
+    if (k1 < k_end) next.fetch(kb + k1 * a.k.n, a.k.n, static_cast<int>(k_end - k1 < BT ? k_end - k1 : BT));
     uint64_t t[4][D / 32];
     mm_nn<D>(ps, kv, ty, tx, t);
 #pragma unroll
@@ -397,7 +406,7 @@ delta_kernel(const __grid_constant__ Args a, const T* __restrict__ O, const T* _
 }
 
 template <int D>
-__host__ __device__ constexpr size_t bwd_smem() { return (4 * BT * row_stride<D>() + BT * PS + 2 * BT) * 4 + BT; }
+__host__ __device__ constexpr size_t bwd_smem() { return (4 * BT * row_stride<D>() + BT * PS + 2 * BT) * 4; }
 
 // The gradients' threads: a warp covers 4 x 8 of the 16 x 16, so that each of a step's shared-memory
 // loads is one wavefront (2 x 16, which the forward's row sums want, takes 12 instead of 8 for the
@@ -421,7 +430,6 @@ dq_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __re
   float* ks = gs + BT * RS;
   float* vs = ks + BT * RS;
   float* ps = vs + BT * RS;
-  uint8_t* ok = reinterpret_cast<uint8_t*>(ps + BT * PS + 2 * BT);
   pdl_trigger();
   const Where w = where(a, a.q_tiles, a.H);
   const int64_t kh = w.h / a.group, q0 = w.tile * BT;
@@ -435,8 +443,8 @@ dq_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __re
   if (k_end > limit) k_end = limit;
   const int64_t row0 = (w.b * a.H + w.h) * a.Nq + q0;
 
-  load_tile<D>(qs, Q + w.b * a.q.b + w.h * a.q.h + q0 * a.q.n, a.q.n, qn, static_cast<const uint8_t*>(nullptr));
-  load_tile<D>(gs, dO + w.b * a.dout.b + w.h * a.dout.h + q0 * a.dout.n, a.dout.n, qn, static_cast<const uint8_t*>(nullptr));
+  load_tile<D>(qs, Q + w.b * a.q.b + w.h * a.q.h + q0 * a.q.n, a.q.n, qn);
+  load_tile<D>(gs, dO + w.b * a.dout.b + w.h * a.dout.h + q0 * a.dout.n, a.dout.n, qn);
   float L[4], dl[4];
   uint64_t acc[4][D / 32];
 #pragma unroll
@@ -447,14 +455,23 @@ dq_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __re
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) acc[i][k] = 0;
   }
+  Tile<D, T> tk, tv;
+  const T* kb = K + w.b * a.k.b + kh * a.k.h;
+  const T* vb = V + w.b * a.v.b + kh * a.v.h;
+  auto fetch = [&](int64_t k0) {
+    if (k0 >= k_end) return;
+    const int kn = static_cast<int>(k_end - k0 < BT ? k_end - k0 : BT);
+    tk.fetch(kb + k0 * a.k.n, a.k.n, kn);
+    tv.fetch(vb + k0 * a.v.n, a.v.n, kn);
+  };
+  fetch(k_begin);
   for (int64_t k0 = k_begin; k0 < k_end; k0 += BT) {
     const int kn = static_cast<int>(k_end - k0 < BT ? k_end - k0 : BT);
     __syncthreads();
-    load_ok(a, w.b, k0, limit, ok);
+    tk.stash(ks);
+    tv.stash(vs);
     __syncthreads();
-    load_tile<D>(ks, K + w.b * a.k.b + kh * a.k.h + k0 * a.k.n, a.k.n, kn, ok);
-    load_tile<D>(vs, V + w.b * a.v.b + kh * a.v.h + k0 * a.v.n, a.v.n, kn, ok);
-    __syncthreads();
+    fetch(k0 + BT);
     float s[4][4], dp[4][4];
     mm_nt<D>(qs, ks, ty, tx, s);
     mm_nt<D>(gs, vs, ty, tx, dp);
@@ -462,7 +479,7 @@ dq_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __re
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float p = ok[tx + 16 * j] ? expf(s[i][j] * a.scale - L[i]) : 0.f;
+        const float p = tx + 16 * j < kn ? expf(s[i][j] * a.scale - L[i]) : 0.f;
         ps[(ty + 16 * i) * PS + tx + 16 * j] = p * (dp[i][j] - dl[i]) * a.scale;
       }
     __syncthreads();
@@ -505,7 +522,6 @@ dkv_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __r
   float* ps = vs + BT * RS;
   float* ls = ps + BT * PS;
   float* ds = ls + BT;
-  uint8_t* ok = reinterpret_cast<uint8_t*>(ds + BT);
   pdl_trigger();
   const Where w = where(a, a.k_tiles, a.Hkv);
   const int64_t k0 = w.tile * BT;
@@ -514,10 +530,9 @@ dkv_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __r
   thread_tile(tx, ty);
   pdl_wait();  // D_i, gathered keys and their counts
   const int64_t limit = key_limit(a, w.b);
-  load_ok(a, w.b, k0, limit, ok);
-  __syncthreads();
-  load_tile<D>(ks, K + w.b * a.k.b + w.h * a.k.h + k0 * a.k.n, a.k.n, kn, ok);
-  load_tile<D>(vs, V + w.b * a.v.b + w.h * a.v.h + k0 * a.v.n, a.v.n, kn, ok);
+  const int attended = limit - k0 < kn ? (limit > k0 ? static_cast<int>(limit - k0) : 0) : kn;
+  load_tile<D>(ks, K + w.b * a.k.b + w.h * a.k.h + k0 * a.k.n, a.k.n, attended);
+  load_tile<D>(vs, V + w.b * a.v.b + w.h * a.v.h + k0 * a.v.n, a.v.n, attended);
   uint64_t ak[4][D / 32], av[4][D / 32];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -528,19 +543,33 @@ dkv_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __r
   int64_t t1 = t0 + a.tiles_per_split;
   if (t1 > tiles) t1 = tiles;
   if (k0 >= limit) t1 = t0;  // no key of this tile is attended
-  for (int64_t it = t0; it < t1; ++it) {
+  Tile<D, T> tq, tg;
+  float l_next = 0.f, d_next = 0.f;
+  auto fetch = [&](int64_t it) {
+    if (it >= t1) return;
     const int64_t h = w.h * a.group + it / a.q_tiles, q0 = (it % a.q_tiles) * BT;
     const int qn = static_cast<int>(a.Nq - q0 < BT ? a.Nq - q0 : BT);
-    __syncthreads();
-    load_tile<D>(qs, Q + w.b * a.q.b + h * a.q.h + q0 * a.q.n, a.q.n, qn, static_cast<const uint8_t*>(nullptr));
-    load_tile<D>(gs, dO + w.b * a.dout.b + h * a.dout.h + q0 * a.dout.n, a.dout.n, qn, static_cast<const uint8_t*>(nullptr));
-    if (threadIdx.x < BT) {
+    tq.fetch(Q + w.b * a.q.b + h * a.q.h + q0 * a.q.n, a.q.n, qn);
+    tg.fetch(dO + w.b * a.dout.b + h * a.dout.h + q0 * a.dout.n, a.dout.n, qn);
+    if (int(threadIdx.x) < qn) {
       const int64_t row = (w.b * a.H + h) * a.Nq + q0 + threadIdx.x;
-      const bool in = int(threadIdx.x) < qn;
-      ls[threadIdx.x] = in ? lse[row] : 0.f;
-      ds[threadIdx.x] = in ? delta[row] : 0.f;
+      l_next = lse[row];
+      d_next = delta[row];
+    }
+  };
+  fetch(t0);
+  for (int64_t it = t0; it < t1; ++it) {
+    const int64_t q0 = (it % a.q_tiles) * BT;
+    const int qn = static_cast<int>(a.Nq - q0 < BT ? a.Nq - q0 : BT);
+    __syncthreads();
+    tq.stash(qs);
+    tg.stash(gs);
+    if (threadIdx.x < BT) {
+      ls[threadIdx.x] = l_next;
+      ds[threadIdx.x] = d_next;
     }
     __syncthreads();
+    fetch(it + 1);
     float s[4][4], dp[4][4];
     mm_nt<D>(ks, qs, ty, tx, s);   // s[key][query]
     mm_nt<D>(vs, gs, ty, tx, dp);
@@ -549,7 +578,7 @@ dkv_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T* __r
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = tx + 16 * j;
-        const float p = (ok[ty + 16 * i] && c < qn) ? expf(s[i][j] * a.scale - ls[c]) : 0.f;
+        const float p = (ty + 16 * i < attended && c < qn) ? expf(s[i][j] * a.scale - ls[c]) : 0.f;
         s[i][j] = p * (dp[i][j] - ds[c]) * a.scale;
         ps[(ty + 16 * i) * PS + c] = p;
       }
