@@ -150,6 +150,8 @@ Split split_waves(int64_t tiles, int64_t blocks, int64_t sm) {
   return best;
 }
 
+constexpr int64_t kLongMask = 32768;
+
 struct CrossPlan {
   bool tc;                       // tensor-core kernels (bf16)
   bool few;                      // forward: few rows per key head
@@ -158,7 +160,7 @@ struct CrossPlan {
   int64_t pairs;                 // pairs of 128-query tiles per head (tensor cores)
   int64_t pad;                   // rows per head of the gathered keys
   Split fwd, dq, dkv;
-  size_t off_kc, off_vc, off_count, off_place;  // gathered keys
+  size_t off_kc, off_vc, off_count, off_place, off_spans;  // gathered keys
   size_t off_o, off_ml;          // forward: partial outputs, maxima and sums
   size_t off_delta, off_part;    // gradients: D_i, partial sums (dQ, then dK and dV)
   size_t total;
@@ -194,7 +196,8 @@ CrossPlan cross_plan(const la_cross_problem& p, int sm) {
     c.off_vc = align256(rows);
     c.off_count = align256(c.off_vc + rows);
     c.off_place = align256(c.off_count + size_t(p.B) * 4);
-    off = align256(c.off_place + size_t(p.B) * size_t(p.Nk) * 4);
+    c.off_spans = align256(c.off_place + size_t(p.B) * size_t(p.Nk) * 4);
+    off = align256(c.off_spans + size_t(p.B) * size_t(ceil_div(p.Nk, la::xs::G_SPAN)) * 4);
   }
   size_t fwd = off;
   if (c.fwd.parts > 1) {
@@ -238,8 +241,17 @@ template <int D, typename T>
 int gather_keys(const la_cross_problem& p, const CrossPlan& c, const la::xs::Args& a, const void* K, const void* V, uint8_t* ws,
                 cudaStream_t st, int* nl) {
   const int64_t grid = ceil_div(p.Nk, la::xs::G_KEYS) * p.Hkv * p.B;
-  if (launch_k(la::xs::gather_kernel<T, D / (16 / int(sizeof(T)))>, dim3(unsigned(grid)), la::xs::G_THREADS, 0, st, false, p.Hkv,
-               p.Nk, c.pad, static_cast<const T*>(K), static_cast<const T*>(V), a.k, a.v, a.kv_len, a.mask,
+  // A block counts the mask before its keys: beyond some tens of thousands of keys, from sums of spans.
+  int32_t* spans = nullptr;
+  if (a.mask && p.Nk > kLongMask) {
+    spans = reinterpret_cast<int32_t*>(ws + c.off_spans);
+    if (launch_k(la::xs::count_kernel, dim3(unsigned(ceil_div(p.Nk, la::xs::G_SPAN) * p.B)), la::xs::G_THREADS, 0, st, false,
+                 p.Nk, a.kv_len, a.mask, spans))
+      return LA_ERR_CUDA;
+    ++*nl;
+  }
+  if (launch_k(la::xs::gather_kernel<T, D / (16 / int(sizeof(T)))>, dim3(unsigned(grid)), la::xs::G_THREADS, 0, st, spans != nullptr, p.Hkv,
+               p.Nk, c.pad, static_cast<const T*>(K), static_cast<const T*>(V), a.k, a.v, a.kv_len, a.mask, spans,
                reinterpret_cast<T*>(ws + c.off_kc), reinterpret_cast<T*>(ws + c.off_vc),
                reinterpret_cast<int32_t*>(ws + c.off_count), reinterpret_cast<int32_t*>(ws + c.off_place)))
     return LA_ERR_CUDA;

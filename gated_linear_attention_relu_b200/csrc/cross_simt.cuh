@@ -679,14 +679,38 @@ sum_keys_kernel(int64_t keys, int64_t Hkv, int64_t Nk, int splits, const float* 
 // order, then zeros up to a multiple of 16 rows (what lies behind is never read); count[b] is their
 // number and place[b][j] where key j went (-1: unattended).  Unattended rows are not read.
 // One block per 64 keys, head and batch row; each counts the attended keys before its own.
-constexpr int G_THREADS = 256, G_KEYS = 64;
+// (of the mask; where Nk is long, of the sums that count_kernel took over G_SPAN keys each, and of the
+// rest of the mask).
+constexpr int G_THREADS = 256, G_KEYS = 64, G_SPAN = 4096;
+
+// spans[b][i] = attended keys among keys [G_SPAN i, G_SPAN (i + 1)) of batch row b.
+__global__ void __launch_bounds__(G_THREADS)
+count_kernel(int64_t Nk, const int32_t* __restrict__ kv_len, const uint8_t* __restrict__ mask, int32_t* __restrict__ spans) {
+  __shared__ int part[G_THREADS / 32];
+  pdl_trigger();
+  const int64_t per_row = (Nk + G_SPAN - 1) / G_SPAN;
+  const int64_t i = blockIdx.x % per_row, b = blockIdx.x / per_row;
+  int64_t limit = Nk;
+  if (kv_len) limit = kv_len[b] < 0 ? 0 : (kv_len[b] < Nk ? kv_len[b] : Nk);
+  const int64_t end = (i + 1) * G_SPAN < limit ? (i + 1) * G_SPAN : limit;
+  int n = 0;
+  for (int64_t j = i * G_SPAN + threadIdx.x; j < end; j += G_THREADS) n += mask[b * Nk + j] != 0;
+  n = __reduce_add_sync(0xffffffffu, n);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = n;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int k = 1; k < G_THREADS / 32; ++k) n += part[k];
+    spans[blockIdx.x] = n;
+  }
+}
 
 // PR: 16-byte packs of a row of d channels.  Strides count elements of T.
 template <typename T, int PR>
 __global__ void __launch_bounds__(G_THREADS)
 gather_kernel(int64_t Hkv, int64_t Nk, int64_t pad, const T* __restrict__ K, const T* __restrict__ V, Str sk, Str sv,
-              const int32_t* __restrict__ kv_len, const uint8_t* __restrict__ mask, T* __restrict__ kc, T* __restrict__ vc,
-              int32_t* __restrict__ count, int32_t* __restrict__ place) {
+              const int32_t* __restrict__ kv_len, const uint8_t* __restrict__ mask, const int32_t* __restrict__ spans,
+              T* __restrict__ kc, T* __restrict__ vc, int32_t* __restrict__ count, int32_t* __restrict__ place) {
   constexpr int VEC = 16 / int(sizeof(T)), D = PR * VEC;
   __shared__ int before[G_THREADS / 32];
   __shared__ int pos[G_KEYS];
@@ -702,7 +726,14 @@ gather_kernel(int64_t Hkv, int64_t Nk, int64_t pad, const T* __restrict__ K, con
   const int64_t head = k0 < limit ? k0 : limit;
   int n = 0;
   if (mb) {
-    for (int64_t j = threadIdx.x; j < head; j += G_THREADS) n += mb[j] != 0;
+    int64_t from = 0;
+    if (spans) {
+      pdl_wait();
+      from = k0 / G_SPAN * G_SPAN;
+      const int32_t* sb = spans + b * ((Nk + G_SPAN - 1) / G_SPAN);
+      for (int64_t i = threadIdx.x; i < k0 / G_SPAN; i += G_THREADS) n += sb[i];
+    }
+    for (int64_t j = from + threadIdx.x; j < head; j += G_THREADS) n += mb[j] != 0;
     n = __reduce_add_sync(0xffffffffu, n);
     if ((threadIdx.x & 31) == 0) before[threadIdx.x >> 5] = n;
   } else if ((threadIdx.x & 31) == 0) {
