@@ -51,7 +51,7 @@ static_assert(Cfg<128>::SMEM <= 232448 && Cfg<64>::SMEM <= 232448, "shared memor
 
 constexpr uint32_t S_COL = 0, O_COL = 256;  // + 128 t
 // Registers: 128 a thread at launch (the host checks that), handed on to the softmax warps.
-constexpr uint32_t REGS_LAUNCH = 128, REGS_SOFTMAX = 176, REGS_EPI = 104, REGS_CTRL = 56;
+constexpr uint32_t REGS_LAUNCH = 128, REGS_SOFTMAX = 152, REGS_EPI = 128, REGS_CTRL = 80;
 static_assert(256 * REGS_SOFTMAX + 128 * REGS_EPI + 128 * REGS_CTRL <= THREADS * REGS_LAUNCH, "register split");
 
 template <int DP>
