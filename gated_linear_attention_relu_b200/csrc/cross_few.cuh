@@ -90,7 +90,7 @@ few_kernel(const __grid_constant__ xs::Args a, const T* __restrict__ Q, const T*
   float m[CNT], l[CNT];
 #pragma unroll
   for (int i = 0; i < CNT; ++i) {
-    m[i] = xs::NEG_INF;
+    m[i] = xs::LOWEST;
     l[i] = 0.f;
   }
   const float cexp = a.scale * LOG2E;
@@ -175,7 +175,7 @@ few_kernel(const __grid_constant__ xs::Args a, const T* __restrict__ Q, const T*
 #pragma unroll
       for (int i = 0; i < CNT; ++i) {
         top[i] = fmaxf(top[i], m[i]);
-        f[i] = m[i] == xs::NEG_INF ? 0.f : exp2_approx((m[i] - top[i]) * cexp);
+        f[i] = exp2_approx((m[i] - top[i]) * cexp);
         m[i] = top[i];
         l[i] *= f[i];
       }
@@ -243,26 +243,24 @@ few_kernel(const __grid_constant__ xs::Args a, const T* __restrict__ Q, const T*
   __syncthreads();
   for (int e = threadIdx.x; e < rows * D; e += THREADS) {
     const int r = e / D, c = e % D;
-    float M = xs::NEG_INF;
+    float M = xs::LOWEST;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm_ml[(w * R + r) * 2]);
     float L = 0.f, o = 0.f;
-    if (M > xs::NEG_INF)
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float mw = sm_ml[(w * R + r) * 2];
-        const float f = mw == xs::NEG_INF ? 0.f : exp2_approx((mw - M) * cexp);
-        L += f * sm_ml[(w * R + r) * 2 + 1];
-        o += f * sm_o[(w * R + r) * D + c];
-      }
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = exp2_approx((sm_ml[(w * R + r) * 2] - M) * cexp);
+      L += f * sm_ml[(w * R + r) * 2 + 1];
+      o += f * sm_o[(w * R + r) * D + c];
+    }
     const int64_t h = kh * a.group + r / a.Nq, n = r % a.Nq;
     const int64_t row = (b * a.H + h) * a.Nq + n;
     if (a.splits > 1) {
       part_o[(split * a.rows + row) * D + c] = o;
       if (c == 0) part_ml[split * a.rows + row] = make_float2(M * a.scale, L);
     } else {
-      ln::put(O[b * a.o.b + h * a.o.h + n * a.o.n + c], L > 0.f ? o / L : 0.f);
-      if (lse && c == 0) lse[row] = L > 0.f ? M * a.scale + logf(L) : xs::NEG_INF;
+      ln::put(O[b * a.o.b + h * a.o.h + n * a.o.n + c], L == 0.f ? 0.f : o / L);
+      if (lse && c == 0) lse[row] = L == 0.f ? xs::NEG_INF : M * a.scale + logf(L);
     }
   }
 }

@@ -21,6 +21,8 @@ constexpr int THREADS = 256;
 constexpr int BT = 64;           // queries and keys per tile
 constexpr int PS = BT + 4;       // row stride (floats) of a score tile
 constexpr float NEG_INF = -__builtin_huge_valf();
+// A running maximum to start from: -inf minus it is -inf and not NaN, so that scores of -inf weigh 0.
+constexpr float LOWEST = -3.402823466e38f;
 
 struct Str {
   int64_t b, h, n;
@@ -289,14 +291,14 @@ forward_kernel(const __grid_constant__ Args a, const T* __restrict__ Q, const T*
         *reinterpret_cast<float2*>(part_o + slot * D + chan<D>(tx, k)) = upk(acc[i][k]);
       if (tx == 0) part_ml[slot] = make_float2(m[i], l[i]);
     } else {
-      const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+      const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // (a sum of NaN stays one)
       T* o = O + w.b * a.o.b + w.h * a.o.h + (q0 + r) * a.o.n;
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
         const float2 v = upk(acc[i][k]);
         store_pair<D>(o + chan<D>(tx, k), make_float2(v.x * inv, v.y * inv));
       }
-      if (lse && tx == 0) lse[row] = l[i] > 0.f ? m[i] + logf(l[i]) : NEG_INF;
+      if (lse && tx == 0) lse[row] = l[i] == 0.f ? NEG_INF : m[i] + logf(l[i]);
     }
   }
 }
@@ -329,9 +331,9 @@ join_kernel(const __grid_constant__ Args a, const float* __restrict__ part_o, co
   __syncthreads();
   float L = 0.f;
   for (int s = threadIdx.x; s < a.splits; s += 32 * JOIN_WARPS) {
-    const float m = f[s];
-    f[s] = m == NEG_INF ? 0.f : expf(m - M);
-    L += f[s] * part_ml[int64_t(s) * a.rows + row].y;
+    const float l = part_ml[int64_t(s) * a.rows + row].y;
+    f[s] = l == 0.f ? 0.f : expf(f[s] - M);
+    L += f[s] * l;
   }
   L = ln::warp_sum(L);
   if (lane == 0) red[warp] = L;
@@ -362,10 +364,10 @@ join_kernel(const __grid_constant__ Args a, const float* __restrict__ part_o, co
   __syncthreads();
   const int64_t n = row % a.Nq, bh = row / a.Nq;
   T* o = O + (bh / a.H) * a.o.b + (bh % a.H) * a.o.h + n * a.o.n;
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
   for (int c = threadIdx.x; c < D; c += 32 * JOIN_WARPS)
     ln::put(o[c], ((sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c])) * inv);
-  if (lse && threadIdx.x == 0) lse[row] = L > 0.f ? M + logf(L) : NEG_INF;
+  if (lse && threadIdx.x == 0) lse[row] = L == 0.f ? NEG_INF : M + logf(L);
 }
 
 // D_i = dO_i . O_i for every query row.  A block has consecutive rows of a head; a row belongs to

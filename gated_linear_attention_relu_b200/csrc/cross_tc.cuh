@@ -463,7 +463,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
         tmem_ld_x32(ts, s0);
         if (j == 0) {
-          m = top;
+          m = fmaxf(top, xs::LOWEST);  // (scores of -inf only, so far)
         } else if (__any_sync(0xffffffffu, top > m + RESCALE)) {
           // rare: raise the reference maximum of the rows that need it
           const float m2 = top > m + RESCALE ? top : m;
@@ -512,7 +512,7 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       if (!ok) break;
       // the epilogue has read the last item's sums
       if (!(ok = warp_wait_near(&bars->ofree[t], (item & 1) ^ 1, abort_flag))) break;
-      inv_l[t * BM + row] = 1.f / l;
+      inv_l[t * BM + row] = l == 0.f ? 0.f : 1.f / l;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->lready[t]);
       ++item;

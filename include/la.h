@@ -287,7 +287,10 @@ typedef struct {
  * Query head h reads key head h / (H / Hkv).  Key j of batch row b is attended when
  * j < kv_len[b] (kv_len given; values are clamped to [0, Nk]) and key_mask[b][j] != 0 (key_mask
  * given).  What stands in unattended rows of K and V has no influence, not even infinities and
- * NaN.  Where nothing is attended, o = 0, lse = -inf and every gradient is 0. */
+ * NaN.  Where nothing is attended, o = 0, lse = -inf and every gradient is 0; in the forward call a
+ * score of -inf weighs 0 as well.  NaN in attended rows, and scores of +inf, give NaN as the formulas
+ * do.  Outputs must not overlap inputs, or one another (equal addresses: LA_ERR_SHAPE); views whose
+ * rows interleave in one buffer, as those of a fused projection, do not overlap. */
 typedef struct {
   int64_t B, H, Hkv;     /* batch, query heads, key/value heads (H a multiple of Hkv) */
   int64_t Nq, Nk;        /* latent tokens; encoder states per batch row, padding included */

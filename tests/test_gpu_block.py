@@ -254,3 +254,56 @@ def test_clip_refuses_overlaps():
             la.clip_grad_norm(grads, 1.0, out=out)
     assert float(la.grad_norm([t, t])) == pytest.approx(math.sqrt(128), rel=1e-6)  # reading twice is no overlap
     la.clip_grad_norm([t[:32], t[:32]], 1.0, out=[torch.empty(32, device="cuda"), torch.empty(32, device="cuda")])
+
+
+# (B, H, Hkv, Nq, Nk, d): several key tiles; the keys split; a few rows, split and not
+SPECIAL = [(2, 2, 2, 140, 300, 64), (1, 1, 1, 130, 2100, 128), (1, 4, 2, 1, 700, 128), (2, 2, 1, 3, 40, 32)]
+PATHS = [("f32", False), ("bf16", True), ("bf16", False)]
+
+
+@pytest.mark.parametrize("shape", SPECIAL, ids=str)
+@pytest.mark.parametrize("dtype,simt", PATHS)
+def test_cross_forward_scores_of_minus_infinity(shape, dtype, simt):
+    """A score of -inf weighs 0, also where a whole tile has nothing else; a row of them has o = 0."""
+    B, H, Hkv, Nq, Nk, d = shape
+    p = la.CrossProblem(B=B, H=H, Hkv=Hkv, Nq=Nq, Nk=Nk, d=d, dtype=dtype, force_simt=simt)
+    Q, K, V, *_, ok = inputs(*shape, dtype, "none", seed=2)
+    Q[..., 0] = Q[..., 0].abs() + 0.5
+    gone = Nk * 2 // 3
+    o, l, to, tl = bo.cross_forward(Q, K, V, d ** -0.5, ok & (torch.arange(Nk, device="cuda") >= gone), unit(dtype, simt))
+    K[:, :, :gone, 0] = -math.inf
+    O, lse = la.cross_forward(p, Q, K, V, return_lse=True)
+    close(O, o, to, "O")
+    close(lse, l, tl, "lse")
+    K[..., 0] = -math.inf
+    O, lse = la.cross_forward(p, Q, K, V, return_lse=True)
+    assert not O.any() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("shape", SPECIAL, ids=str)
+@pytest.mark.parametrize("dtype,simt", PATHS)
+def test_cross_forward_hands_nan_on(shape, dtype, simt):
+    """NaN that is attended comes out as NaN where it belongs, and nowhere else."""
+    B, H, Hkv, Nq, Nk, d = shape
+    p = la.CrossProblem(B=B, H=H, Hkv=Hkv, Nq=Nq, Nk=Nk, d=d, dtype=dtype, force_simt=simt)
+    Q, K, V, *_ = inputs(*shape, dtype, "none", seed=3)
+    whole, l0 = la.cross_forward(p, Q, K, V, return_lse=True)
+    heads = slice((Hkv - 1) * (H // Hkv), H)  # those that read the last key head
+
+    def check(q, k, v, at, channels=slice(None), lse_too=True):
+        O, lse = la.cross_forward(p, q, k, v, return_lse=True)
+        hit = torch.zeros(O.shape, dtype=torch.bool, device="cuda")
+        hit[at][..., channels] = True
+        assert O[hit].isnan().all() and torch.equal(O[~hit], whole[~hit])
+        rows = hit.any(3) if lse_too else torch.zeros_like(l0, dtype=torch.bool)
+        assert lse[rows].isnan().all() and torch.equal(lse[~rows], l0[~rows])
+
+    q, k, v, bad = Q.clone(), K.clone(), V.clone(), K.clone()
+    q[-1, -1, Nq - 1, 3] = math.nan
+    check(q, K, V, (slice(B - 1, B), slice(H - 1, H), slice(Nq - 1, Nq)))
+    k[-1, -1, Nk - 1, 5] = math.nan
+    check(Q, k, V, (slice(B - 1, B), heads))
+    bad[-1, -1] = math.nan
+    check(Q, bad, V, (slice(B - 1, B), heads))
+    v[-1, -1, Nk // 2, 7] = math.nan
+    check(Q, K, v, (slice(B - 1, B), heads), slice(7, 8), lse_too=False)
