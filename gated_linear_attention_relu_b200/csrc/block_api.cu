@@ -133,16 +133,20 @@ Split split_axis(int64_t tiles, int64_t blocks, int64_t want, int64_t least) {
   return {static_cast<int>(ceil_div(tiles, per)), static_cast<int>(per)};
 }
 
-// The split of a long axis whose parts are summed afterwards: the fewest parts that (nearly) bring
-// the last wave of blocks to an end with the others.  A part costs about 3 tiles of its own.
-Split split_waves(int64_t tiles, int64_t blocks, int64_t sm) {
+// The split of a long axis whose parts are joined afterwards: the fewest parts that (nearly) bring
+// the last wave of blocks (`slots` at a time) to an end with the others.  A part costs `extra` tiles
+// of its own.
+Split split_waves(int64_t tiles, int64_t blocks, int64_t slots, int64_t extra) {
   Split best = {1, static_cast<int>(std::max<int64_t>(tiles, 1))};
   if (tiles <= 0 || blocks <= 0) return best;
-  double cost = 0;
-  for (int64_t s = 1; s <= std::min<int64_t>(std::max<int64_t>(1, 8 * sm / blocks), ceil_div(tiles, 4)); ++s) {
+  const int64_t most = std::min<int64_t>(ceil_div(tiles, 4), la::xs::MAX_SPLITS);
+  double cost = double(ceil_div(blocks, slots)) * double(tiles + extra);
+  for (int64_t w = 1; w <= 8; ++w) {  // the most parts that take w waves
+    const int64_t s = std::min(w * slots / blocks, most);
+    if (s < 2) continue;
     const int64_t per = ceil_div(tiles, s), parts = ceil_div(tiles, per);
-    const double c = double(ceil_div(blocks * parts, sm)) * double(per + 3);
-    if (s == 1 || c < 0.97 * cost) {
+    const double c = double(ceil_div(blocks * parts, slots)) * double(per + extra);
+    if (c < 0.97 * cost) {
       cost = c;
       best = {static_cast<int>(parts), static_cast<int>(per)};
     }
@@ -179,14 +183,16 @@ CrossPlan cross_plan(const la_cross_problem& p, int sm) {
   c.pairs = ceil_div(p.Nq, 2 * la::xt::BM);
   c.pad = ceil_div(p.Nk, 16) * 16;
   // A key head's rows in one block: one pass over the keys for all of them, where a tile of rows
-  // would be all but empty.
+  // would be all but empty.  (Two such blocks share an SM up to 4 rows, and the keys are split into
+  // whole waves of them: 8 x 8 heads of 16384 keys, one row each of 4 query heads, take 100 us in 9
+  // parts, 105 in 4 or 13 and 110 in 18.)
   c.few = !(p.flags & LA_FLAG_FORCE_SIMT) && c.rows > 0 && c.keys > 0 && group * p.Nq <= la::xf::MAX_ROWS;
-  c.fwd = c.few ? split_axis(c.k_tiles, p.B * p.Hkv, 8 * int64_t(sm), 4)
+  c.fwd = c.few ? split_waves(c.k_tiles, p.B * p.Hkv, (group * p.Nq <= 4 ? 2 : 1) * int64_t(sm), 2)
           : c.tc ? split_axis(ceil_div(p.Nk, la::xt::BN), p.B * p.H * c.pairs, sm, 4)
                : split_axis(c.k_tiles, p.B * p.H * c.q_tiles, want, 2);
   const int64_t q128 = ceil_div(p.Nq, la::xt::BM), k128 = ceil_div(p.Nk, la::xt::BN);
   c.dq = c.tc ? split_axis(k128, p.B * p.H * q128, sm, 4) : split_axis(c.k_tiles, p.B * p.H * c.q_tiles, want, 2);
-  c.dkv = c.tc ? split_waves(q128 * group, p.B * p.Hkv * k128, sm)
+  c.dkv = c.tc ? split_waves(q128 * group, p.B * p.Hkv * k128, sm, 3)
                : split_axis(c.q_tiles * group, p.B * p.Hkv * c.k_tiles, want, 2);
   const size_t D = size_t(p.d);
   size_t off = 0;
