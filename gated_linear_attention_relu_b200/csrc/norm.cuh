@@ -284,6 +284,12 @@ struct Ring {
   uint64_t full[4];
   int abort_flag;
 };
+// Thread 0 when a wait gave up: waits (with a limit) for the copies that it has issued, so that none
+// lands in shared memory that is no longer the block's.
+__device__ __forceinline__ void ring_drain(Ring& rg, int stages, uint32_t issued) {
+  const uint32_t n = static_cast<uint32_t>(stages);
+  for (uint32_t i = issued > n ? issued - n : 0; i < issued; ++i) mbar_wait_drain(&rg.full[i % n], (i / n) & 1);
+}
 
 // The sum of two values over the block's warps, in warp order; one barrier, and the next call's may
 // follow at once (callers alternate the buffers).
@@ -309,8 +315,10 @@ forward_long(const Args a, int parts, int stages, const T* x, const float* __res
   const int part = static_cast<int>(blockIdx.x - g * parts);
   const uint32_t bytes = static_cast<uint32_t>(a.cols) * sizeof(T);
   const int64_t row0 = g * a.per_group;
+  uint32_t issued = 0;  // (thread 0's)
   auto fetch = [&](int64_t j, int s) {
     if (j < a.per_group) {
+      ++issued;
       mbar_arrive_expect_tx(&rg.full[s], bytes);
       bulk_load(ring + s * bytes, x + (row0 + j) * a.sx, bytes, &rg.full[s]);
     }
@@ -356,6 +364,7 @@ forward_long(const Args a, int parts, int stages, const T* x, const float* __res
       }
     const float mu = block_sum2<WPR>(v, 0.f, red[0]).x * a.inv_cols;
     if constexpr (RING) {  // every thread has its part of the row: the stage can take another one
+      if (*static_cast<volatile int*>(&rg.abort_flag)) break;
       if (threadIdx.x == 0) fetch(j + int64_t(stages) * parts, s);
       if (++s == stages) {
         s = 0;
@@ -392,6 +401,7 @@ forward_long(const Args a, int parts, int stages, const T* x, const float* __res
       store_pack(y + row * a.sy + c, p[i]);
     }
   }
+  if (RING && threadIdx.x == 0 && rg.abort_flag) ring_drain(rg, stages, issued);
 }
 
 template <typename T, int VEC, int NV, int WPR, bool RING>
@@ -406,8 +416,10 @@ backward_long(const Args a, int parts, int stages, const T* x, const T* dy, cons
   const int part = static_cast<int>(blockIdx.x - g * parts);
   const uint32_t bytes = static_cast<uint32_t>(a.cols) * sizeof(T);
   const int64_t row0 = g * a.per_group;
+  uint32_t issued = 0;  // (thread 0's)
   auto fetch = [&](int64_t j, int s) {
     if (j < a.per_group) {
+      ++issued;
       mbar_arrive_expect_tx(&rg.full[s], 2 * bytes);
       bulk_load(ring + (2 * s) * bytes, x + (row0 + j) * a.sx, bytes, &rg.full[s]);
       bulk_load(ring + (2 * s + 1) * bytes, dy + (row0 + j) * a.sdy, bytes, &rg.full[s]);
@@ -473,6 +485,7 @@ backward_long(const Args a, int parts, int stages, const T* x, const T* dy, cons
       r = rstd[row + parts];
     }
     if constexpr (RING) {
+      if (*static_cast<volatile int*>(&rg.abort_flag)) break;
       if (threadIdx.x == 0) fetch(j + int64_t(stages) * parts, s);
       if (++s == stages) {
         s = 0;
@@ -494,6 +507,7 @@ backward_long(const Args a, int parts, int stages, const T* x, const T* dy, cons
       store_pack(dx + row * a.sdx + c, px[i]);
     }
   }
+  if (RING && threadIdx.x == 0 && rg.abort_flag) ring_drain(rg, stages, issued);
   const int64_t slot = int64_t(blockIdx.x) * a.cols;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
