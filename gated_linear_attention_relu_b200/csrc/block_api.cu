@@ -134,12 +134,12 @@ Split split_axis(int64_t tiles, int64_t blocks, int64_t want, int64_t least) {
 }
 
 // The split of a long axis whose parts are joined afterwards: the fewest parts that (nearly) bring
-// the last wave of blocks (`slots` at a time) to an end with the others.  A part costs `extra` tiles
-// of its own.
-Split split_waves(int64_t tiles, int64_t blocks, int64_t slots, int64_t extra) {
+// the last wave of blocks (`slots` at a time) to an end with the others.  A part has `least` tiles or
+// more and costs `extra` of its own.
+Split split_waves(int64_t tiles, int64_t blocks, int64_t slots, int64_t least, int64_t extra) {
   Split best = {1, static_cast<int>(std::max<int64_t>(tiles, 1))};
   if (tiles <= 0 || blocks <= 0) return best;
-  const int64_t most = std::min<int64_t>(ceil_div(tiles, 4), la::xs::MAX_SPLITS);
+  const int64_t most = std::min<int64_t>(ceil_div(tiles, least), la::xs::MAX_SPLITS);
   double cost = double(ceil_div(blocks, slots)) * double(tiles + extra);
   for (int64_t w = 1; w <= 8; ++w) {  // the most parts that take w waves
     const int64_t s = std::min(w * slots / blocks, most);
@@ -177,7 +177,6 @@ CrossPlan cross_plan(const la_cross_problem& p, int sm) {
   c.keys = p.B * p.Hkv * p.Nk;
   c.q_tiles = ceil_div(p.Nq, la::xs::BT);
   c.k_tiles = ceil_div(p.Nk, la::xs::BT);
-  const int64_t want = 2 * int64_t(sm);
   const int64_t group = p.Hkv > 0 ? p.H / p.Hkv : 1;
   c.tc = p.dtype == LA_BF16 && !(p.flags & LA_FLAG_FORCE_SIMT) && c.rows > 0 && c.keys > 0;
   c.pairs = ceil_div(p.Nq, 2 * la::xt::BM);
@@ -187,13 +186,16 @@ CrossPlan cross_plan(const la_cross_problem& p, int sm) {
   // whole waves of them: 8 x 8 heads of 16384 keys, one row each of 4 query heads, take 100 us in 9
   // parts, 105 in 4 or 13 and 110 in 18.)
   c.few = !(p.flags & LA_FLAG_FORCE_SIMT) && c.rows > 0 && c.keys > 0 && group * p.Nq <= la::xf::MAX_ROWS;
-  c.fwd = c.few ? split_waves(c.k_tiles, p.B * p.Hkv, (group * p.Nq <= 4 ? 2 : 1) * int64_t(sm), 2)
+  c.fwd = c.few ? split_waves(c.k_tiles, p.B * p.Hkv, (group * p.Nq <= 4 ? 2 : 1) * int64_t(sm), 4, 2)
           : c.tc ? split_axis(ceil_div(p.Nk, la::xt::BN), p.B * p.H * c.pairs, sm, 4)
-               : split_axis(c.k_tiles, p.B * p.H * c.q_tiles, want, 2);
+               : split_waves(c.k_tiles, p.B * p.H * c.q_tiles, 2 * int64_t(sm), 2, 1);
   const int64_t q128 = ceil_div(p.Nq, la::xt::BM), k128 = ceil_div(p.Nk, la::xt::BN);
-  c.dq = c.tc ? split_axis(k128, p.B * p.H * q128, sm, 4) : split_axis(c.k_tiles, p.B * p.H * c.q_tiles, want, 2);
-  c.dkv = c.tc ? split_waves(q128 * group, p.B * p.Hkv * k128, sm, 3)
-               : split_axis(c.q_tiles * group, p.B * p.Hkv * c.k_tiles, want, 2);
+  // CUDA cores: whole waves too (as many parts as bring two blocks to every SM took 760 instead of 625 us
+  // for 32 heads of 4000 queries and 300 keys, d = 32).  The gradients' blocks of d = 128 fill an SM.
+  const int64_t slots = p.d == 128 ? sm : 2 * int64_t(sm);
+  c.dq = c.tc ? split_axis(k128, p.B * p.H * q128, sm, 4) : split_waves(c.k_tiles, p.B * p.H * c.q_tiles, slots, 2, 1);
+  c.dkv = c.tc ? split_waves(q128 * group, p.B * p.Hkv * k128, sm, 4, 3)
+               : split_waves(c.q_tiles * group, p.B * p.Hkv * c.k_tiles, slots, 2, 1);
   const size_t D = size_t(p.d);
   size_t off = 0;
   if (c.keys > 0) {
