@@ -120,22 +120,14 @@ int validate(const la_cross_problem* p, bool backward) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// How a long axis of `tiles` is split over blocks where `blocks` alone do not fill the machine:
-// at most as many parts as bring the grid to `want` blocks, each of at least `least` tiles.
+// How a long axis is split over blocks, whose parts are joined afterwards: the fewest parts that
+// (nearly) bring the last wave of blocks (`slots` at a time) to an end with the others.  A part has
+// `least` tiles or more and costs `extra` of its own (as it starts, and its sums' way through memory).
+// Parts for every SM whatever the waves are slower: forward of 32 heads 1024 x 1024, 66 instead of
+// 27 us; 20 heads 1000 x 2000 (d = 64), 62 instead of 39; 100 heads 256 x 8192, 184 instead of 153.
 struct Split {
   int parts, per;  // parts * per >= tiles
 };
-Split split_axis(int64_t tiles, int64_t blocks, int64_t want, int64_t least) {
-  if (tiles <= 0 || blocks <= 0) return {1, static_cast<int>(std::max<int64_t>(tiles, 1))};
-  int64_t parts = std::min(ceil_div(want, blocks), ceil_div(tiles, least));
-  parts = std::max<int64_t>(1, std::min<int64_t>(parts, la::xs::MAX_SPLITS));
-  const int64_t per = ceil_div(tiles, parts);
-  return {static_cast<int>(ceil_div(tiles, per)), static_cast<int>(per)};
-}
-
-// The split of a long axis whose parts are joined afterwards: the fewest parts that (nearly) bring
-// the last wave of blocks (`slots` at a time) to an end with the others.  A part has `least` tiles or
-// more and costs `extra` of its own.
 Split split_waves(int64_t tiles, int64_t blocks, int64_t slots, int64_t least, int64_t extra) {
   Split best = {1, static_cast<int>(std::max<int64_t>(tiles, 1))};
   if (tiles <= 0 || blocks <= 0) return best;
@@ -187,13 +179,13 @@ CrossPlan cross_plan(const la_cross_problem& p, int sm) {
   // parts, 105 in 4 or 13 and 110 in 18.)
   c.few = !(p.flags & LA_FLAG_FORCE_SIMT) && c.rows > 0 && c.keys > 0 && group * p.Nq <= la::xf::MAX_ROWS;
   c.fwd = c.few ? split_waves(c.k_tiles, p.B * p.Hkv, (group * p.Nq <= 4 ? 2 : 1) * int64_t(sm), 4, 2)
-          : c.tc ? split_axis(ceil_div(p.Nk, la::xt::BN), p.B * p.H * c.pairs, sm, 4)
+          : c.tc ? split_waves(ceil_div(p.Nk, la::xt::BN), p.B * p.H * c.pairs, sm, 4, 4)
                : split_waves(c.k_tiles, p.B * p.H * c.q_tiles, 2 * int64_t(sm), 2, 1);
   const int64_t q128 = ceil_div(p.Nq, la::xt::BM), k128 = ceil_div(p.Nk, la::xt::BN);
   // CUDA cores: whole waves too (as many parts as bring two blocks to every SM took 760 instead of 625 us
   // for 32 heads of 4000 queries and 300 keys, d = 32).  The gradients' blocks of d = 128 fill an SM.
   const int64_t slots = p.d == 128 ? sm : 2 * int64_t(sm);
-  c.dq = c.tc ? split_axis(k128, p.B * p.H * q128, sm, 4) : split_waves(c.k_tiles, p.B * p.H * c.q_tiles, slots, 2, 1);
+  c.dq = c.tc ? split_waves(k128, p.B * p.H * q128, sm, 4, 4) : split_waves(c.k_tiles, p.B * p.H * c.q_tiles, slots, 2, 1);
   c.dkv = c.tc ? split_waves(q128 * group, p.B * p.Hkv * k128, sm, 4, 3)
                : split_waves(c.q_tiles * group, p.B * p.Hkv * c.k_tiles, slots, 2, 1);
   const size_t D = size_t(p.d);
