@@ -173,11 +173,14 @@ CrossPlan cross_plan(const la_cross_problem& p, int sm) {
   c.tc = p.dtype == LA_BF16 && !(p.flags & LA_FLAG_FORCE_SIMT) && c.rows > 0 && c.keys > 0;
   c.pairs = ceil_div(p.Nq, 2 * la::xt::BM);
   c.pad = ceil_div(p.Nk, 16) * 16;
-  // A key head's rows in one block: one pass over the keys for all of them, where a tile of rows
-  // would be all but empty.  (Two such blocks share an SM up to 4 rows, and the keys are split into
-  // whole waves of them: 8 x 8 heads of 16384 keys, one row each of 4 query heads, take 100 us in 9
-  // parts, 105 in 4 or 13 and 110 in 18.)
-  c.few = !(p.flags & LA_FLAG_FORCE_SIMT) && c.rows > 0 && c.keys > 0 && group * p.Nq <= la::xf::MAX_ROWS;
+  // A key head's rows in one block: one pass over the keys for all of them, where tiles of 64 or 128
+  // rows would be all but empty and read them once for every query head.  16384 keys, 8 x 8 key heads:
+  // 1 row 88 us (tensor cores: 137), 8 query heads of 1 row 175 (896); a single query head of 8 rows
+  // takes 175 here and 137 there, so that from 5 rows on it goes there.
+  const int64_t most = c.tc && group == 1 ? la::xf::MAX_ROWS / 2 : la::xf::MAX_ROWS;
+  c.few = !(p.flags & LA_FLAG_FORCE_SIMT) && c.rows > 0 && c.keys > 0 && group * p.Nq <= most;
+  // (Two blocks of up to 4 rows share an SM, and the keys are split into whole waves of them: 9 parts
+  // take 100 us, 4 or 13 parts 105 and 18 parts 110, for 4 rows of the above.)
   c.fwd = c.few ? split_waves(c.k_tiles, p.B * p.Hkv, (group * p.Nq <= 4 ? 2 : 1) * int64_t(sm), 4, 2)
           : c.tc ? split_waves(ceil_div(p.Nk, la::xt::BN), p.B * p.H * c.pairs, sm, 4, 4)
                : split_waves(c.k_tiles, p.B * p.H * c.q_tiles, 2 * int64_t(sm), 2, 1);
@@ -241,9 +244,11 @@ template <int D, typename T>
 int gather_keys(const la_cross_problem& p, const CrossPlan& c, const la::xs::Args& a, const void* K, const void* V, uint8_t* ws,
                 cudaStream_t st, int* nl) {
   const int64_t grid = ceil_div(p.Nk, la::xs::G_KEYS) * p.Hkv * p.B;
-  // A block counts the mask before its keys: beyond some tens of thousands of keys, from sums of spans.
+  // A block counts the mask before its keys; of long masks, from sums of spans, which a kernel more
+  // takes (whole forward calls with and without them: 8192 keys 22.7 and 21.7 us, 32768: 43.2 and 45.2,
+  // 262144: 235 and 318).
   int32_t* spans = nullptr;
-  if (a.mask && p.Nk > kLongMask) {
+  if (a.mask && p.Nk >= kLongMask) {
     spans = reinterpret_cast<int32_t*>(ws + c.off_spans);
     if (launch_k(la::xs::count_kernel, dim3(unsigned(ceil_div(p.Nk, la::xs::G_SPAN) * p.B)), la::xs::G_THREADS, 0, st, false,
                  p.Nk, a.kv_len, a.mask, spans))
@@ -455,7 +460,7 @@ int cross_backward_tc(const la_cross_problem& p, const CrossPlan& c, la::xs::Arg
   t.c = p.scale * la::xt::LOG2E;
   t.scale = p.scale;
   t.count = keys.count;
-  t.o = a.o; t.dout = a.dout; t.dq = a.dq;
+  t.dq = a.dq;
   const bool wide = (reinterpret_cast<uintptr_t>(dQ) & 31) == 0 && (p.Nq == 1 || p.dq.n % 16 == 0) &&
                     (p.H == 1 || p.dq.h % 16 == 0) && (p.B == 1 || p.dq.b % 16 == 0);
   auto kq = la::xb::dq_kernel<DP, D>;
@@ -551,6 +556,7 @@ int check_len(const int32_t* kv_len) { return (reinterpret_cast<uintptr_t>(kv_le
 
 // ------------------------------------------------------------------------------- layer norm
 constexpr int64_t kMaxCols = 16384;
+constexpr int64_t kFewRowsPerSm = 4;  // forward: up to here a block has one row
 
 int validate(const la_norm_problem* p, bool backward) {
   if (!p) return LA_ERR_NULL;
@@ -631,7 +637,7 @@ template <typename T, int VEC, int NV, int WPR, bool RING>
 int norm_forward_long(const la_norm_problem& p, const la::ln::Args& a, int sm, const NormForward& f, cudaStream_t st) {
   auto kern = la::ln::forward_long<T, VEC, NV, WPR, RING>;
   const int per_sm = WPR <= 8 ? 4 : 2;
-  const int parts = p.rows <= 2 * int64_t(sm) ? int(p.rows / p.groups) : norm_parts(p, sm, per_sm);
+  const int parts = p.rows <= kFewRowsPerSm * int64_t(sm) ? int(p.rows / p.groups) : norm_parts(p, sm, per_sm);
   const size_t row = size_t(p.cols) * sizeof(T);
   const int stages = RING ? norm_stages(row, per_sm) : 0;
   if (RING && set_smem(kern, stages * row)) return LA_ERR_CUDA;
@@ -644,8 +650,9 @@ int norm_forward_any(const la_norm_problem& p, const la::ln::Args& a, int sm, co
   const void* ptr[2] = {f.x, f.y};
   const int64_t str[2] = {p.sx, p.sy};
   const int64_t c = p.cols;
-  // Few rows do not fill the machine: what counts is how soon one is done, so more threads share it.
-  const bool few = p.rows <= 2 * int64_t(sm);
+  // Few rows do not fill the machine: what counts is how soon one is done, so more threads share it
+  // (4096 channels of bf16, 64 rows: 2.5 us, a warp each 6.9; 600 rows: 7.1 and 7.7; 1200: 11.4 and 8.4).
+  const bool few = p.rows <= kFewRowsPerSm * int64_t(sm);
   if (norm_vec<T>(p, 2, ptr, str)) {
     constexpr int V = 16 / int(sizeof(T));
     if (few && c > 32 * V && c <= 256 * V) return norm_forward_long<T, V, 1, 8, false>(p, a, sm, f, st);

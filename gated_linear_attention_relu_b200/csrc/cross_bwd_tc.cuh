@@ -3,12 +3,17 @@
 //   p_ij = exp(s_ij - lse_i),  D_i = dO_i . O_i,  ds_ij = p_ij (dO_i . v_j - D_i)
 //   dQ_i = scale sum_j ds_ij k_j,  dK_j = scale sum_i ds_ij q_i,  dV_j = sum_i p_ij dO_i
 //
-// D_i comes from a kernel of its own (one pass over O and dO; inside dq_kernel its code and its loads
-// held up the other warps).  Two more, so that every sum has one owner and a fixed order (no atomics): dq_kernel keeps a
-// query tile and walks the keys, dkv_kernel keeps a key tile and walks the queries.  Each forms the
-// scores and dP = dO V^T again (7 products of a tile pair instead of 5).  p and ds go back to tensor
-// memory as bf16 (rounded once each) as the operand of the product that follows; the softmax scale
-// is applied to the fp32 sums at the end.
+// D_i comes from a kernel of its own (one pass over O and dO, 5.2 TB/s; inside dq_kernel its code and
+// its loads held up the other warps).  Two more, so that every sum has one owner and a fixed order (no
+// atomics): dq_kernel keeps a query tile and walks the keys, dkv_kernel keeps a key tile and walks the
+// queries.  Each forms the scores and dP = dO V^T again (7 products of a tile pair instead of 5).  p
+// and ds go back to tensor memory as bf16 (rounded once each, for the product that follows); the
+// softmax scale is applied to the fp32 sums at the end.
+//
+// 32 heads of 75600 queries and 300 keys (929 GFLOP in 5 products): 1590 us with D's pass of 240, which
+// is 584 TFLOP/s, or 818 for the 7 products.  What bounds it is the chain of a step, score product ->
+// exponentials -> dP -> ds -> product, of which tensor memory holds one and a half steps; the third key
+// tile of 44 keys costs dkv_kernel as much as a full one.
 //
 // dq_kernel, tensor memory: S of even and odd steps [0, 256), dP [256, 384), dQ [384, 512); ds
 // overwrites its S.  S of the next step and dP of the next step are computed while the math warps
@@ -51,7 +56,7 @@ struct Args {
   FastDiv fd_tiles, fd_splits, fd_heads;  // tiles, splits, H (dq) or Hkv (dkv)
   float c, scale;         // scale * log2(e), scale
   const int32_t* count;
-  xs::Str o, dout, dq;
+  xs::Str dq;
 };
 
 // ------------------------------------------------------------------------------------ dQ
@@ -560,7 +565,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
   pdl_trigger();
-  pdl_wait();  // the gathered keys, and D from the dQ kernel
+  pdl_wait();  // D_i, the gathered keys and their counts (every kernel of the chain has waited for the one before)
 
   if (warp >= CTRL) {
     regs_dec<REGS_CTRL>();
@@ -604,8 +609,8 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       }
     } else if (warp == CTRL + 1 || warp == CTRL + 2) {
       // ---------------------------------------------------------- MMA issuers (converged warps)
-      // The first: S^T and dV, the second: dP^T and dK.  Each walks the same steps: the product of this step's p (ds)
-      // first, then the scores (dP) of the next step, which overwrite it.
+      // The first: S^T and dV, the second: dP^T and dK.  Each walks the same steps: the product of this
+      // step's p (ds) first, then the scores (dP) of the next step, which overwrite it.
       const bool sv = warp == CTRL + 1;
       uint32_t i = 0, items = 0;
       bool ok = true;

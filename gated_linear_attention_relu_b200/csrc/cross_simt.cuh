@@ -4,8 +4,11 @@
 //   s_ij = scale q_i.k_j,  o_i = sum_j exp(s_ij - lse_i) v_j   (la_cross_forward / _backward)
 //
 // One pass over the keys with the running maximum and sum of the softmax; 64 x 64 score tiles,
-// 4 x 4 scores a thread, so a step along d feeds 16 FMAs from 8 shared-memory values and the FMA
-// pipe is what bounds it.  Products over many keys (or, in the gradients, many queries) are summed
+// 4 x 4 scores a thread, so a step along d feeds 16 FMAs from 8 shared-memory values; tiles of global
+// memory are fetched into registers during the products of the tile before.  8 heads, 2048 x 1000,
+// d = 64: forward 317 us (26 of 74.5 TFLOP/s), gradients 895 (23 in 5 products, 33 in the 7 done):
+// the barriers between a tile's products and its exponentials leave the FMA pipe idle for the rest.
+// Products over many keys (or, in the gradients, many queries) are summed
 // per tile and the tiles' sums then added up, which keeps the rounding of long sums at the level of
 // one tile.  Where there are too few tiles to fill the machine the long axis is split over blocks,
 // whose partial results are joined in order by a second kernel.
@@ -680,7 +683,7 @@ sum_keys_kernel(int64_t keys, int64_t Hkv, int64_t Nk, int splits, const float* 
 // Gathers the attended keys: kc, vc [B, Hkv, pad, D] hold the rows of K and V that are attended, in
 // order, then zeros up to a multiple of 16 rows (what lies behind is never read); count[b] is their
 // number and place[b][j] where key j went (-1: unattended).  Unattended rows are not read.
-// One block per 64 keys, head and batch row; each counts the attended keys before its own.
+// One block per 64 keys, head and batch row; each counts the attended keys before its own
 // (of the mask; where Nk is long, of the sums that count_kernel took over G_SPAN keys each, and of the
 // rest of the mask).
 constexpr int G_THREADS = 256, G_KEYS = 64, G_SPAN = 4096;

@@ -4,12 +4,16 @@
 //   dx = rstd (a - mean(a) - xh mean(a xh)),  dw_g = sum dy xh,  db_g = sum dy.
 //
 // Both are bound by HBM: one read of x (and dy), one write of y (dx).  A row stays in registers
-// between its read and its write, so the variance is the exact two-pass one.
+// between its read and its write, so the variance is the exact two-pass one.  75600 rows of 4096 in
+// bf16: forward 238 us (5.2 TB/s), backward 349 (5.3); 32760 rows of 1000 in fp32: 45 us (5.8) and
+// 76 (5.2).
 //   Short rows (up to 512 channels; forward: up to a warp's 16 packs a lane) belong to a part of a
-// warp, several rows at a time, without a barrier.
+// warp, several rows at a time, without a barrier.  (Forward rows of 4096 in a block each took 300 to
+// 385 us instead of 270.)
 //   Longer rows belong to a block that walks its range of a group's rows, with the weight in
-// registers; the rows to come are on their way to shared memory by bulk copies (a ring of STAGES
-// rows), since loads into registers left too few bytes in flight.
+// registers; the rows to come are on their way to shared memory by bulk copies (a ring of up to 4
+// rows), since loads into registers left too few bytes in flight (backward of two groups of 75600 rows:
+// 1286 us, with the ring 707).
 //   Rows that are not 16-byte aligned take the same kernels' one-element form (without the ring).
 // In the backward pass a thread owns the same columns of every row it sees, so its shares of dw and
 // db stay in registers until the block has walked its rows; blocks write them to their own slots,
