@@ -6,7 +6,7 @@
 // Both are bound by HBM: one read of x (and dy), one write of y (dx).  A row stays in registers
 // between its read and its write, so the variance is the exact two-pass one.  75600 rows of 4096 in
 // bf16: forward 238 us (5.2 TB/s), backward 349 (5.3); 32760 rows of 1000 in fp32: 45 us (5.8) and
-// 76 (5.2).
+// 69 (5.7).
 //   Short rows (up to 512 channels; forward: up to a warp's 16 packs a lane) belong to a part of a
 // warp, several rows at a time, without a barrier.  (Forward rows of 4096 in a block each took 300 to
 // 385 us instead of 270.)
@@ -525,10 +525,11 @@ backward_long(const Args a, int parts, int stages, const T* x, const T* dy, cons
   }
 }
 
-constexpr int RED_COLS = 32, RED_ROWS = 8;
+constexpr int RED_COLS = 32, RED_ROWS = 32;
 
 // out[g][c] = sum over the group's parts of slots[g * parts + part][c]: RED_ROWS threads of a
-// column take every RED_ROWS-th part, and their sums are added in order.  blockIdx.y: dw, db.
+// column take every RED_ROWS-th part, and their sums are added in order.  blockIdx.y: dw, db.  (With 8
+// threads a column it took 20 of the 76 us of 32760 rows of 1000; with 32 the whole takes 69.)
 __global__ void __launch_bounds__(RED_COLS * RED_ROWS)
 reduce_kernel(int64_t cols, int parts, const float* __restrict__ dw_slots, const float* __restrict__ db_slots,
               float* __restrict__ dw, float* __restrict__ db) {
@@ -542,7 +543,7 @@ reduce_kernel(int64_t cols, int parts, const float* __restrict__ dw_slots, const
   pdl_wait();
   float v = 0.f;
   if (out && c < cols)
-#pragma unroll 4
+#pragma unroll 8
     for (int k = y; k < parts; k += RED_ROWS) v += in[(g * parts + k) * cols + c];
   s[y][threadIdx.x % RED_COLS] = v;
   __syncthreads();
