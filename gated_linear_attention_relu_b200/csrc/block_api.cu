@@ -1087,4 +1087,11 @@ int la_clip_grad_norm(const la_grad* grads, int64_t count, float max_norm, float
   return clip_common(grads, count, true, max_norm, norm, ws, ws_bytes, stream);
 }
 
+#ifdef LA_TEST_HOOKS
+// Test-hook build only: the roles that are held back (see hold in sm100.cuh; 0: none).
+int la_test_hold(unsigned int what) {
+  return cudaMemcpyToSymbol(la::g_la_hold, &what, sizeof what) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+#endif
+
 }  // extern "C"

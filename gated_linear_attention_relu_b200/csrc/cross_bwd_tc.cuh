@@ -596,6 +596,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             mbar_wait_drain(&bars->qfull[s], (qi / C::QST) & 1);
             break;
           }
+          hold(HOLD_DO_LOAD);
           load_tile<DP>(smem + C::OFF_G + sg * C::TILE, &tmG, n, h, w.b, &bars->gfull[sg]);
         }
         if (!ok) break;
@@ -620,6 +621,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       const uint32_t in = sbase + (sv ? C::OFF_Q : C::OFF_G);             // ... times Q (dO) tiles
       const uint32_t out = sbase + (sv ? C::OFF_G : C::OFF_Q);            // p dO (ds Q)
       uint64_t* in_full = sv ? bars->qfull : bars->gfull;
+      uint64_t* out_full = sv ? bars->gfull : bars->qfull;
       uint64_t* in_empty = sv ? bars->qempty : bars->gempty;
       uint64_t* out_empty = sv ? bars->gempty : bars->qempty;
       uint64_t* fixed_full = sv ? &bars->kfull : &bars->vfull;
@@ -656,6 +658,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             ok = ok && warp_wait_near(&in_full[s2], ((i + 1) / in_st) & 1, abort_flag);
           }
           if (j == 0) ok = ok && warp_wait_near(&bars->accfree, (items & 1) ^ 1, abort_flag);
+          // This step's dO (Q) tile: p is ready from S^T and the exponentials alone, and loads land in any
+          // order, so neither it nor the next Q tile says that dO is there.
+          ok = ok && warp_wait_near(&out_full[s], (i / out_st) & 1, abort_flag);
           ok = ok && warp_wait_near(ready, i & 1, abort_flag);
           // The next p waits for the next S^T: dV and S^T have the tensor cores to themselves first.
           if (!sv && more) ok = ok && warp_wait_near(&bars->sfull, (i + 1) & 1, abort_flag);

@@ -39,6 +39,19 @@ __device__ __forceinline__ constexpr bool in_bounds(bool) { return true; }
 __device__ long long g_la_skip_tile = -1;
 #endif
 
+// Test hook of the same build: holds a role of the cross-attention kernels back for 20 us at each of
+// its steps, as a slow load or a warp that is not scheduled would; results must not change.
+enum : unsigned { HOLD_DO_LOAD = 1u };
+#ifdef LA_TEST_HOOKS
+__device__ unsigned int g_la_hold;
+__device__ __forceinline__ void hold(unsigned int what) {
+  if (!(g_la_hold & what)) return;
+  for (int i = 0; i < 20; ++i) __nanosleep(1000);
+}
+#else
+__device__ __forceinline__ void hold(unsigned int) {}
+#endif
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
