@@ -27,6 +27,13 @@
 // of exponentials);
 // 16-19 dq: dQ to memory; dkv: lse and D of the query tiles to come;
 // 20 TMA producer; 21, 22 MMA issuers.  One CTA per SM, persistent.  Every wait is bounded.
+//
+// A wait on a barrier's parity tells its phase from the one before only, so no barrier may complete two
+// phases ahead of anyone who waits for it.  Tiles and rings: a slot is filled again after everyone who
+// waits for it has given it back (dkv: both issuers).  S, dP, dQ and the sums: the next phase is issued
+// after all math (or storing) warps have arrived behind their wait.  p, ds, dpfree, dqfree, accfree:
+// the next phase follows a product that the waiting issuer itself issues after its wait.  S^T of
+// dkv_kernel, for which the other issuer waits too: see sfull.
 #pragma once
 #include "cross_tc.cuh"
 
@@ -459,7 +466,11 @@ struct BarsK {
   uint64_t gfull[CfgK<DP>::GST], gempty[CfgK<DP>::GST];
   uint64_t lfull[CfgK<DP>::GST], lempty[CfgK<DP>::GST];
   uint64_t kfull, kempty, vfull, vempty;
-  uint64_t sfull, pready, dpfull, dsready, accfull, accfree, final_[2];
+  // S^T of even and odd steps: a wait tells a phase from the one before it only, and the S^T issuer may
+  // be a step ahead of the other one, which waits for it too (S^T(i + 2) wants p(i + 1), which wants
+  // nothing of dP).  It cannot be three steps ahead: p(i + 2) wants dP(i + 1), which comes after that wait.
+  uint64_t sfull[2];
+  uint64_t pready, dpfull, dsready, accfull, accfree, final_[2];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -539,7 +550,8 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     mbar_init(&bars->kempty, 1);
     mbar_init(&bars->vfull, 1);
     mbar_init(&bars->vempty, 1);
-    mbar_init(&bars->sfull, 1);
+    mbar_init(&bars->sfull[0], 1);
+    mbar_init(&bars->sfull[1], 1);
     mbar_init(&bars->pready, MATH_WARPS);
     mbar_init(&bars->dpfull, 1);
     mbar_init(&bars->dsready, MATH_WARPS);
@@ -626,13 +638,12 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
       uint64_t* out_empty = sv ? bars->gempty : bars->qempty;
       uint64_t* fixed_full = sv ? &bars->kfull : &bars->vfull;
       uint64_t* fixed_empty = sv ? &bars->kempty : &bars->vempty;
-      uint64_t* in_done = sv ? &bars->sfull : &bars->dpfull;
       uint64_t* ready = sv ? &bars->pready : &bars->dsready;
       const uint32_t in_st = sv ? C::QST : C::GST, out_st = sv ? C::GST : C::QST;
       const uint64_t fd = tile::desc_k(fixed, 0);
-      auto issue_in = [&](bool last, uint32_t s) {
+      auto issue_in = [&](bool last, uint32_t s, uint32_t step) {
         tile::mma_kk<DP>(t_in, fd, tile::desc_k(in + s * C::TILE, 0), id_s);
-        mma_commit(in_done);
+        mma_commit(sv ? &bars->sfull[step & 1] : &bars->dpfull);
         mma_commit(&in_empty[s]);
         if (last) mma_commit(fixed_empty);
       };
@@ -644,7 +655,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
           if (nx.i >= a.total) break;
           ok = warp_wait_near(fixed_full, 0, abort_flag) && warp_wait_near(&in_full[0], 0, abort_flag);
           tc_fence_after();
-          if (ok && elect_one()) issue_in(nx.nq == 1, 0);
+          if (ok && elect_one()) issue_in(nx.nq == 1, 0, 0);
           __syncwarp();
           continue;
         }
@@ -663,7 +674,8 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
           ok = ok && warp_wait_near(&out_full[s], (i / out_st) & 1, abort_flag);
           ok = ok && warp_wait_near(ready, i & 1, abort_flag);
           // The next p waits for the next S^T: dV and S^T have the tensor cores to themselves first.
-          if (!sv && more) ok = ok && warp_wait_near(&bars->sfull, (i + 1) & 1, abort_flag);
+          if (!sv) hold(HOLD_DP_ISSUER);
+          if (!sv && more) ok = ok && warp_wait_near(&bars->sfull[(i + 1) & 1], ((i + 1) >> 1) & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
@@ -672,7 +684,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
               mma_bf16_ts(t_acc, t_in + 8u * (kk & 1) + 32u * (kk >> 1), od + tile::step_mn(kk), id_d, j > 0 || kk > 0);
             mma_commit(&out_empty[s]);
             if (last) mma_commit(&bars->accfull);
-            if (more) issue_in(last2, s2);
+            if (more) issue_in(last2, s2, i + 1);
           }
           __syncwarp();
         }
@@ -698,7 +710,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         const uint32_t s_l = i % C::GST;
         const uint32_t la_ = sbase + C::OFF_L + (s_l * 2 * BM + 32 * cq) * 4, ld_ = la_ + BM * 4;
         if (!(ok = warp_wait_near(&bars->lfull[s_l], (i / C::GST) & 1, abort_flag))) break;
-        if (!(ok = warp_wait_near(&bars->sfull, i & 1, abort_flag))) break;
+        if (!(ok = warp_wait_near(&bars->sfull[i & 1], (i >> 1) & 1, abort_flag))) break;
         tc_fence_after();
         uint32_t s[32], d[16];
         tmem_ld_x32(ts, s);

@@ -25,7 +25,10 @@
 //   12         TMA producer
 //   13, 14     MMA issuers of query tile 0 / 1 (15 completes the warpgroup)
 // Tensor memory: S (and P) of the two tiles in columns [0, 256), O in [256, 512).
-// Every wait is bounded (mbar_wait).
+// Every wait is bounded (mbar_wait_near), and no barrier completes two phases ahead of anyone who waits
+// for it: a slot is filled again after its issuers (K and V: both) have given it back, S after all of a
+// tile's softmax warps have arrived, P and O after a product that the waiting issuer issues behind its
+// wait, a turn after the other tile's, inv_l after the epilogue has read the last one.
 #pragma once
 #include "common.cuh"
 #include "cross_simt.cuh"

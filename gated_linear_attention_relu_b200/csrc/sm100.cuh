@@ -41,7 +41,7 @@ __device__ long long g_la_skip_tile = -1;
 
 // Test hook of the same build: holds a role of the cross-attention kernels back for 20 us at each of
 // its steps, as a slow load or a warp that is not scheduled would; results must not change.
-enum : unsigned { HOLD_DO_LOAD = 1u };
+enum : unsigned { HOLD_DO_LOAD = 1u, HOLD_DP_ISSUER = 2u };
 #ifdef LA_TEST_HOOKS
 __device__ unsigned int g_la_hold;
 __device__ __forceinline__ void hold(unsigned int what) {

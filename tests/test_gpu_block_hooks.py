@@ -13,7 +13,7 @@ from test_gpu_block import P_UNIT, close, gen, inputs, rnd
 
 pytestmark = pytest.mark.gpu
 
-HOLD_DO_LOAD = 1
+HOLD_DO_LOAD, HOLD_DP_ISSUER = 1, 2
 
 
 @pytest.fixture(scope="module")
@@ -40,7 +40,7 @@ def _backward(lib, p, Q, K, V, O, lse, dO, kv_len, grads, ws):
 
 # (B, H, Hkv, Nq, Nk, d): one query tile to an item, several, several items to a CTA
 @pytest.mark.parametrize("shape", [(1, 2, 2, 100, 300, 128), (2, 2, 1, 700, 200, 128), (2, 12, 6, 520, 1700, 64)], ids=str)
-@pytest.mark.parametrize("what", [HOLD_DO_LOAD])
+@pytest.mark.parametrize("what", [HOLD_DO_LOAD, HOLD_DP_ISSUER, HOLD_DO_LOAD | HOLD_DP_ISSUER])
 def test_a_late_role_changes_nothing(hooks, shape, what):
     B, H, Hkv, Nq, Nk, d = shape
     Q, K, V, kv_len, _, ok = inputs(B, H, Hkv, Nq, Nk, d, "bf16", "len")
