@@ -545,6 +545,21 @@ int cross_few(const la_cross_problem& p, const CrossPlan& c, la::xs::Args a, con
   return LA_OK;
 }
 
+// Partial sums leave the kernels in 32-byte stores.  Workspaces have the 16-byte alignment of every
+// pointer, so the parts start at the first 32-byte boundary, for which 16 bytes more are asked for.
+constexpr size_t kCrossSlack = 16;
+size_t cross_need(const CrossPlan& c) { return c.total + kCrossSlack; }
+
+// The workspace of a call, from its first 32-byte boundary on.
+int cross_workspace(const CrossPlan& c, void* ws, size_t ws_bytes, uint8_t** out) {
+  const uintptr_t at = (reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31);
+  *out = reinterpret_cast<uint8_t*>(at);
+  if (!aligned16(ws)) return LA_ERR_ALIGN;
+  if (c.total == 0) return LA_OK;
+  const size_t skip = at - reinterpret_cast<uintptr_t>(ws);
+  return ws && ws_bytes >= skip + c.total ? LA_OK : LA_ERR_WORKSPACE;
+}
+
 int need(const void* ptr, bool needed) {
   if (!needed) return LA_OK;
   if (!ptr) return LA_ERR_NULL;
@@ -899,7 +914,7 @@ extern "C" {
 
 size_t la_cross_workspace_bytes_for(const la_cross_problem* p, int sm_count) {
   if (validate(p, false) != LA_OK || sm_count <= 0) return 0;
-  return std::max<size_t>(cross_plan(*p, sm_count).total, 16);
+  return cross_need(cross_plan(*p, sm_count));
 }
 
 size_t la_cross_workspace_bytes(const la_cross_problem* p) {
@@ -920,15 +935,14 @@ int la_cross_forward(const la_cross_problem* p, const void* Q, const void* K, co
   int sm = 0;
   if ((rc = current_sm_count(&sm))) return rc;
   const CrossPlan c = cross_plan(*p, sm);
-  if (c.total > 0 && (!ws || ws_bytes < c.total)) return LA_ERR_WORKSPACE;
-  if (!aligned16(ws)) return LA_ERR_ALIGN;
+  uint8_t* w = nullptr;
+  if ((rc = cross_workspace(c, ws, ws_bytes, &w))) return rc;
   int nl = 0;
   if (has_q) {
     const la::xs::Args a = cross_args(*p, c, kv_len, key_mask);
     rc = with_type(*p, [&](auto d, auto t) {
       constexpr int D = decltype(d)::value;
       using T = decltype(t);
-      uint8_t* w = static_cast<uint8_t*>(ws);
       if (c.few) {
         const int64_t r = p->H / p->Hkv * p->Nq;
         auto f = r <= 1 ? cross_few<D, T, 1> : r <= 2 ? cross_few<D, T, 2> : r <= 4 ? cross_few<D, T, 4> : cross_few<D, T, 8>;
@@ -967,13 +981,12 @@ int la_cross_backward(const la_cross_problem* p, const void* Q, const void* K, c
   int sm = 0;
   if ((rc = current_sm_count(&sm))) return rc;
   const CrossPlan c = cross_plan(*p, sm);
-  if (c.total > 0 && (!ws || ws_bytes < c.total)) return LA_ERR_WORKSPACE;
-  if (!aligned16(ws)) return LA_ERR_ALIGN;
+  uint8_t* w = nullptr;
+  if ((rc = cross_workspace(c, ws, ws_bytes, &w))) return rc;
   int nl = 0;
   const la::xs::Args a = cross_args(*p, c, kv_len, key_mask);
   rc = with_type(*p, [&](auto d, auto t) {
     constexpr int D = decltype(d)::value;
-    uint8_t* w = static_cast<uint8_t*>(ws);
     if constexpr (sizeof(t) == 2) {
       if (c.tc) return cross_backward_tc<D>(*p, c, a, Q, K, V, O, lse, dO, dQ, dK, dV, w, sm, stream, &nl);
     }

@@ -303,7 +303,7 @@ typedef struct {
 } la_cross_problem;
 
 /* Bytes of workspace for both cross-attention calls on the current device / for an SM count;
- * 0 for an invalid problem. */
+ * 0 for an invalid problem.  (16 of them let the workspace start on any 16-byte boundary.) */
 size_t la_cross_workspace_bytes(const la_cross_problem* p);
 size_t la_cross_workspace_bytes_for(const la_cross_problem* p, int sm_count);
 
