@@ -566,6 +566,19 @@ int need(const void* ptr, bool needed) {
   return aligned16(ptr) ? LA_OK : LA_ERR_ALIGN;
 }
 
+// Whether an output stands at the address of an input or of another output (null: not there).
+template <size_t O, size_t I>
+bool same_address(const void* const (&out)[O], const void* const (&in)[I]) {
+  for (size_t i = 0; i < O; ++i) {
+    if (!out[i]) continue;
+    for (const void* x : in)
+      if (x == out[i]) return true;
+    for (size_t j = 0; j < i; ++j)
+      if (out[j] == out[i]) return true;
+  }
+  return false;
+}
+
 // kv_len: 4-byte aligned.  (key_mask has no alignment.)
 int check_len(const int32_t* kv_len) { return (reinterpret_cast<uintptr_t>(kv_len) & 3u) ? LA_ERR_ALIGN : LA_OK; }
 
@@ -931,7 +944,8 @@ int la_cross_forward(const la_cross_problem* p, const void* Q, const void* K, co
   if ((rc = need(Q, has_q)) || (rc = need(K, has_k)) || (rc = need(V, has_k)) || (rc = need(O, has_q)) ||
       (rc = need(lse, has_q && lse)) || (rc = check_len(kv_len)))
     return rc;
-  if (has_q && (O == Q || (has_k && (O == K || O == V)))) return LA_ERR_SHAPE;  // O is written as K and V are read
+  // (O and lse are written as the rest is read; K and V of no keys have no address)
+  if (has_q && same_address({O, lse}, {Q, has_k ? K : nullptr, has_k ? V : nullptr, kv_len, key_mask})) return LA_ERR_SHAPE;
   int sm = 0;
   if ((rc = current_sm_count(&sm))) return rc;
   const CrossPlan c = cross_plan(*p, sm);
@@ -969,15 +983,12 @@ int la_cross_backward(const la_cross_problem* p, const void* Q, const void* K, c
       (rc = need(lse, has_q)) || (rc = need(dO, has_q)) || (rc = need(dQ, has_q)) || (rc = need(dK, has_k)) ||
       (rc = need(dV, has_k)) || (rc = check_len(kv_len)))
     return rc;
-  const void* in[5] = {Q, K, V, O, dO};
-  const void* out[3] = {dQ, dK, dV};
-  for (int i = 0; i < 3; ++i) {
-    if (!out[i]) continue;
-    for (const void* x : in)
-      if (x == out[i]) return LA_ERR_SHAPE;  // an input is read after the first gradient is written
-    for (int j = 0; j < i; ++j)
-      if (out[j] == out[i]) return LA_ERR_SHAPE;
-  }
+  // (an input is read after the first gradient is written)
+  auto here = [](const void* x, bool has) { return has ? x : nullptr; };
+  if (same_address({here(dQ, has_q), here(dK, has_k), here(dV, has_k)},
+                   {here(Q, has_q), here(K, has_k), here(V, has_k), here(O, has_q), static_cast<const void*>(here(lse, has_q)),
+                    here(dO, has_q), kv_len, key_mask}))
+    return LA_ERR_SHAPE;
   int sm = 0;
   if ((rc = current_sm_count(&sm))) return rc;
   const CrossPlan c = cross_plan(*p, sm);
