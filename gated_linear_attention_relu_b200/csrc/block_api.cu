@@ -795,10 +795,11 @@ int validate(const la_grad* g, int64_t count, bool clip) {
   return LA_OK;
 }
 
-// Outputs may overlap nothing but their own input at the same address.  One sweep over all ranges
+// Outputs (the norm too: it is written while gradients are still read) may overlap nothing but their own
+// input at the same address.  One sweep over all ranges
 // by rising start: an overlap shows between a range and the furthest end so far (kept for outputs
 // and for inputs apart).
-int clip_overlaps(const la_grad* g, int64_t count) {
+int clip_overlaps(const la_grad* g, int64_t count, const float* norm) {
   struct Range {
     uintptr_t a, b;
     bool out;
@@ -815,10 +816,12 @@ int clip_overlaps(const la_grad* g, int64_t count) {
   }
   auto before = [](const Range& x, const Range& y) { return x.a < y.a; };
   if (!std::is_sorted(r, r + n, before)) std::sort(r, r + n, before);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(norm);  // (apart, so that lists in order stay in order)
   uintptr_t end_out = 0, end_in = 0;
   int rc = LA_OK;
   for (int64_t i = 0; i < n && rc == LA_OK; ++i) {
     if (r[i].a < end_out || (r[i].out && r[i].a < end_in)) rc = LA_ERR_SHAPE;
+    if (r[i].a < at + sizeof(float) && at < r[i].b) rc = LA_ERR_SHAPE;
     uintptr_t& end = r[i].out ? end_out : end_in;
     end = std::max(end, r[i].b);
   }
@@ -881,7 +884,7 @@ int clip_common(const la_grad* g, int64_t count, bool clip, float max_norm, floa
   if (!norm) return LA_ERR_NULL;
   if (reinterpret_cast<uintptr_t>(norm) & 3u) return LA_ERR_ALIGN;
   if (clip && (!std::isfinite(max_norm) || max_norm < 0.f)) return LA_ERR_SHAPE;
-  if (clip && (rc = clip_overlaps(g, count))) return rc;
+  if (clip && (rc = clip_overlaps(g, count, norm))) return rc;
   int sm = 0;
   if ((rc = current_sm_count(&sm))) return rc;
   if (!ws || ws_bytes < clip_need(count, sm)) return LA_ERR_WORKSPACE;

@@ -377,7 +377,8 @@ int la_grad_norm(const la_grad* grads, int64_t count, float* norm, void* workspa
  * coefficient from the norm in fp64.  An infinite or NaN gradient gives the coefficient 0 or NaN, as
  * the formula says.  max_norm: finite, >= 0.
  * Memory that an output writes may be read as that output's own `in` (same address) and as
- * nothing else: LA_ERR_SHAPE for outputs that overlap one another or another input. */
+ * nothing else: LA_ERR_SHAPE for outputs, norm among them, that overlap one another or another
+ * input. */
 int la_clip_grad_norm(const la_grad* grads, int64_t count, float max_norm, float* norm, void* workspace,
                       size_t workspace_bytes, cudaStream_t stream);
 

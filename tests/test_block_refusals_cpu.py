@@ -30,3 +30,18 @@ def test_cross_tensors_without_elements_have_no_address():
     none = la.CrossProblem(B=2, H=4, Nq=8, Nk=0, d=64)
     assert _cross({**CROSS, "K": 96, "V": 96}, none) in (6, 7)
     assert _cross({**GRADS, "K": 144, "dK": 144, "dV": 144}, none) in (6, 7)
+
+
+def test_clip_refuses_a_norm_inside_the_gradients():
+    lib = blk._lib()
+
+    def clip(rows, norm):
+        arr = (blk.LaGrad * len(rows))(*[blk.LaGrad(*r) for r in rows])
+        return lib.la_clip_grad_norm(arr, len(rows), 1.0, norm, 16, 0, None)
+
+    inside = (4096, 4096, 8, 1, 0)      # 32 bytes, in place
+    moved = (8192, 12288, 8, 1, 0)
+    for norm in (4096, 4124, 8192, 8220, 12288, 12316):
+        assert clip([moved, inside], norm) == 2, norm
+    for norm in (4092, 4128, 8188, 8224, 12284, 12320):
+        assert clip([moved, inside], norm) in (6, 7), norm
