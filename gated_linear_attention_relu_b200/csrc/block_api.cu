@@ -614,6 +614,24 @@ bool norm_alias_ok(const la_norm_problem& p, const void* in, int64_t si, const v
   return d >= p.cols * e && d <= s - p.cols * e;
 }
 
+// Statistics, weights, biases and their gradients: dense fp32.  Whether one that is written shares an
+// element with another one.
+struct Floats {
+  const float* at;
+  int64_t n;
+  bool output;
+};
+template <size_t N>
+bool floats_overlap(const Floats (&f)[N]) {
+  for (size_t i = 0; i < N; ++i)
+    for (size_t j = 0; j < N; ++j) {
+      if (i == j || !f[i].output || !f[i].at || !f[j].at || f[i].n == 0 || f[j].n == 0) continue;
+      const uintptr_t a = reinterpret_cast<uintptr_t>(f[i].at), b = reinterpret_cast<uintptr_t>(f[j].at);
+      if (a < b + uintptr_t(f[j].n) * sizeof(float) && b < a + uintptr_t(f[i].n) * sizeof(float)) return true;
+    }
+  return false;
+}
+
 template <typename T>
 bool norm_vec(const la_norm_problem& p, int n, const void* const* ptr, const int64_t* stride) {
   const int64_t vec = 16 / int64_t(sizeof(T));
@@ -1032,6 +1050,10 @@ int la_layernorm_forward(const la_norm_problem* p, const void* x, const float* w
   if ((reinterpret_cast<uintptr_t>(x) & mask) || (reinterpret_cast<uintptr_t>(y) & mask)) return LA_ERR_ALIGN;
   if (!aligned16(weight) || !aligned16(bias) || !aligned16(mean) || !aligned16(rstd)) return LA_ERR_ALIGN;
   if (has && !norm_alias_ok(*p, x, p->sx, y, p->sy)) return LA_ERR_SHAPE;
+  const int64_t params = p->groups * p->cols;
+  if (floats_overlap({{weight, params, false}, {bias, params, false}, {mean, p->rows, true}, {rstd, p->rows, true}}) ||
+      (has && (same_address({y}, {weight, bias}) || same_address({mean, rstd}, {x, y}))))
+    return LA_ERR_SHAPE;
   if (has) {
     int sm = 0;
     if ((rc = current_sm_count(&sm))) return rc;
@@ -1057,6 +1079,11 @@ int la_layernorm_backward(const la_norm_problem* p, const void* x, const void* d
   for (const float* t : {weight, mean, rstd, static_cast<const float*>(dweight), static_cast<const float*>(dbias)})
     if (!aligned16(t)) return LA_ERR_ALIGN;
   if (has && (!norm_alias_ok(*p, x, p->sx, dx, p->sdx) || !norm_alias_ok(*p, dy, p->sdy, dx, p->sdx))) return LA_ERR_SHAPE;
+  const int64_t params = p->groups * p->cols;
+  if (floats_overlap({{weight, params, false}, {mean, p->rows, false}, {rstd, p->rows, false}, {dweight, params, true},
+                      {dbias, params, true}}) ||
+      (has && (same_address({dx}, {weight, mean, rstd}) || same_address({dweight, dbias}, {x, dy, dx}))))
+    return LA_ERR_SHAPE;
   int sm = 0;
   if ((rc = current_sm_count(&sm))) return rc;
   const size_t need_bytes = norm_slots(*p, sm);

@@ -341,15 +341,17 @@ size_t la_layernorm_workspace_bytes(const la_norm_problem* p);
 size_t la_layernorm_workspace_bytes_for(const la_norm_problem* p, int sm_count);
 
 /* weight, bias: fp32 [groups, cols] or NULL (1 and 0); mean, rstd: fp32 [rows], both or neither.
- * y may be x (same stride).  x and y need the alignment of their type only; rows that are not
- * 16-byte aligned take a slower path. */
+ * y may be x (same stride); no other output may overlap another tensor (LA_ERR_SHAPE).  x and y need
+ * the alignment of their type only; rows that are not 16-byte aligned take a slower path.  weight,
+ * bias, mean and rstd are 16-byte aligned in any case. */
 int la_layernorm_forward(const la_norm_problem* p, const void* x, const float* weight, const float* bias, void* y,
                          float* mean, float* rstd, cudaStream_t stream);
 
 /* dx and, where given, dweight and dbias (fp32 [groups, cols]), from the forward's mean and rstd:
  * with xh = (x - mean) rstd and a = dy weight_g,
  *   dx = rstd (a - mean_c(a) - xh mean_c(a xh)),  dweight_g = sum dy xh,  dbias_g = sum dy
- * (sums over the group's rows).  dx may be dy or x (same stride). */
+ * (sums over the group's rows).  dx may be dy or x (same stride); no other output may overlap another
+ * tensor (LA_ERR_SHAPE).  Alignment as in the forward call. */
 int la_layernorm_backward(const la_norm_problem* p, const void* x, const void* dy, const float* weight,
                           const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
