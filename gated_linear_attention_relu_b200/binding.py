@@ -73,7 +73,7 @@ def load(path: Optional[str] = None):
     if not os.path.exists(path) and path == LIB_PATH:
         from . import build as _build
 
-        _build.build()
+        _build.build_library()
     try:
         lib = ctypes.CDLL(path)
     except OSError as e:  # no silent fallback: the CUDA library is the product

@@ -77,15 +77,12 @@ def _calls():
 
     from . import build
 
-    build.build_marshal()
-    from . import _marshal
-
-    lib = _lib()
-    _marshal.bind(*(ctypes.cast(getattr(lib, name), _VP).value for name in (
+    module, lib = build.load_marshal(), _lib()
+    module.bind(*(ctypes.cast(getattr(lib, name), _VP).value for name in (
         "la_cross_workspace_bytes", "la_cross_forward", "la_cross_backward", "la_layernorm_workspace_bytes",
         "la_layernorm_forward", "la_layernorm_backward", "la_clip_workspace_bytes", "la_grad_norm",
         "la_clip_grad_norm")))
-    return _marshal
+    return module
 
 
 def _on(stream, device, call, *args):
