@@ -30,7 +30,8 @@ EXPORTS = [
     "la_state_update", "la_forward_gated", "la_block_step", "la_forward_tokencausal", "la_backward_bidir",
     "la_backward", "la_backward_saved",
     # block.py declares these
-    "la_cross_workspace_bytes", "la_cross_workspace_bytes_for", "la_cross_forward", "la_cross_backward",
+    "la_cross_workspace_bytes", "la_cross_workspace_bytes_for", "la_cross_workspace_bytes_of", "la_cross_forward",
+    "la_cross_backward",
     "la_layernorm_workspace_bytes", "la_layernorm_workspace_bytes_for", "la_layernorm_forward",
     "la_layernorm_backward", "la_clip_workspace_bytes", "la_clip_workspace_bytes_for", "la_grad_norm",
     "la_clip_grad_norm",

@@ -17,6 +17,8 @@ from typing import Optional
 
 from .binding import LA_BF16, LA_F32, LA_FLAG_FORCE_SIMT, LaError, load
 
+LA_CROSS_FORWARD, LA_CROSS_BACKWARD, LA_CROSS_LENGTHS, LA_CROSS_MASK = 1, 2, 4, 8
+
 _SIZE, _INT, _VP = ctypes.c_size_t, ctypes.c_int, ctypes.c_void_p
 
 
@@ -52,6 +54,7 @@ def _lib():
         for name, res, args in (
             ("la_cross_workspace_bytes", _SIZE, [C]),
             ("la_cross_workspace_bytes_for", _SIZE, [C, _INT]),
+            ("la_cross_workspace_bytes_of", _SIZE, [C, ctypes.c_uint, _INT]),
             ("la_cross_forward", _INT, [C] + [_VP] * 8 + [_SIZE, _VP]),
             ("la_cross_backward", _INT, [C] + [_VP] * 12 + [_SIZE, _VP]),
             ("la_layernorm_workspace_bytes", _SIZE, [N]),
@@ -79,7 +82,7 @@ def _calls():
 
     module, lib = build.load_marshal(), _lib()
     module.bind(*(ctypes.cast(getattr(lib, name), _VP).value for name in (
-        "la_cross_workspace_bytes", "la_cross_forward", "la_cross_backward", "la_layernorm_workspace_bytes",
+        "la_cross_workspace_bytes_of", "la_cross_forward", "la_cross_backward", "la_layernorm_workspace_bytes",
         "la_layernorm_forward", "la_layernorm_backward", "la_clip_workspace_bytes", "la_grad_norm",
         "la_clip_grad_norm")))
     return module
@@ -140,20 +143,24 @@ class CrossProblem:
         return c
 
 
-def cross_workspace_bytes(p: CrossProblem, sm_count: Optional[int] = None) -> int:
-    lib, c = _lib(), p.c()
-    if sm_count is None:
-        return int(lib.la_cross_workspace_bytes(ctypes.byref(c)))
-    return int(lib.la_cross_workspace_bytes_for(ctypes.byref(c), int(sm_count)))
+def cross_workspace_bytes(p: CrossProblem, sm_count: Optional[int] = None, backward: bool = True,
+                          padded: bool = True) -> int:
+    """Bytes for ``cross_forward`` and, with ``backward``, ``cross_backward``; with ``padded`` they may be
+    given a ``kv_len`` or ``key_mask``."""
+    uses = LA_CROSS_FORWARD | (LA_CROSS_BACKWARD if backward else 0) | (LA_CROSS_LENGTHS | LA_CROSS_MASK if padded else 0)
+    if sm_count is not None and sm_count <= 0:
+        return 0
+    return int(_lib().la_cross_workspace_bytes_of(ctypes.byref(p.c()), uses, int(sm_count or 0)))
 
 
-def cross_workspace(p: CrossProblem, device="cuda"):
-    """A workspace for ``cross_forward`` and ``cross_backward``.  Calls that may run at the same
-    time (other streams, captured graphs) need workspaces of their own."""
+def cross_workspace(p: CrossProblem, device="cuda", backward: bool = True, padded: bool = True):
+    """A workspace for ``cross_forward`` and ``cross_backward`` (a program that only serves needs far less
+    with ``backward`` False).  Calls that may run at the same time (other streams, captured graphs) need
+    workspaces of their own."""
     import torch
 
     with torch.cuda.device(torch.device(device)):
-        n = cross_workspace_bytes(p)
+        n = cross_workspace_bytes(p, backward=backward, padded=padded)
         return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 

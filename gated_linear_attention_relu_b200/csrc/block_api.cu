@@ -162,7 +162,8 @@ struct CrossPlan {
   size_t total;
 };
 
-CrossPlan cross_plan(const la_cross_problem& p, int sm) {
+// `uses`: la_cross_use, of which LA_CROSS_FORWARD or LA_CROSS_BACKWARD says whose workspace it is.
+CrossPlan cross_plan(const la_cross_problem& p, int sm, unsigned uses) {
   CrossPlan c;
   std::memset(&c, 0, sizeof c);
   c.rows = p.B * p.H * p.Nq;
@@ -192,8 +193,10 @@ CrossPlan cross_plan(const la_cross_problem& p, int sm) {
   c.dkv = c.tc ? split_waves(q128 * group, p.B * p.Hkv * k128, sm, 4, 3)
                : split_waves(c.q_tiles * group, p.B * p.Hkv * c.k_tiles, slots, 2, 1);
   const size_t D = size_t(p.d);
+  const bool back = (uses & LA_CROSS_BACKWARD) != 0;
   size_t off = 0;
-  if (c.keys > 0) {
+  // (a few rows read K and V where they are; lengths alone end the CUDA-core kernels' walk)
+  if (c.keys > 0 && (back || !c.few) && (uses & (c.tc ? LA_CROSS_LENGTHS | LA_CROSS_MASK : LA_CROSS_MASK))) {
     const size_t rows = size_t(p.B) * size_t(p.Hkv) * size_t(c.pad) * D * elem_size(p.dtype);
     c.off_kc = 0;
     c.off_vc = align256(rows);
@@ -202,18 +205,26 @@ CrossPlan cross_plan(const la_cross_problem& p, int sm) {
     c.off_spans = align256(c.off_place + size_t(p.B) * size_t(p.Nk) * 4);
     off = align256(c.off_spans + size_t(p.B) * size_t(ceil_div(p.Nk, la::xs::G_SPAN)) * 4);
   }
-  size_t fwd = off;
-  if (c.fwd.parts > 1) {
-    c.off_o = off;
-    c.off_ml = align256(c.off_o + size_t(c.fwd.parts) * size_t(c.rows) * D * 4);
-    fwd = align256(c.off_ml + size_t(c.fwd.parts) * size_t(c.rows) * 8);
+  if (back) {
+    c.off_delta = off;
+    c.off_part = align256(c.off_delta + size_t(c.rows) * 4);
+    const size_t part_dq = c.dq.parts > 1 ? size_t(c.dq.parts) * size_t(c.rows) * D * 4 : 0;
+    const size_t part_kv = c.keys > 0 ? 2 * size_t(c.dkv.parts) * size_t(c.keys) * D * 4 : 0;
+    c.total = align256(c.off_part + std::max(part_dq, part_kv));
+  } else {
+    c.total = off;
+    if (c.fwd.parts > 1) {
+      c.off_o = off;
+      c.off_ml = align256(c.off_o + size_t(c.fwd.parts) * size_t(c.rows) * D * 4);
+      c.total = align256(c.off_ml + size_t(c.fwd.parts) * size_t(c.rows) * 8);
+    }
   }
-  c.off_delta = off;
-  c.off_part = align256(c.off_delta + size_t(c.rows) * 4);
-  const size_t part_dq = c.dq.parts > 1 ? size_t(c.dq.parts) * size_t(c.rows) * D * 4 : 0;
-  const size_t part_kv = c.keys > 0 ? 2 * size_t(c.dkv.parts) * size_t(c.keys) * D * 4 : 0;
-  c.total = std::max(fwd, align256(c.off_part + std::max(part_dq, part_kv)));
   return c;
+}
+
+// What a call with these optional tensors uses.
+unsigned uses_of(unsigned call, const int32_t* kv_len, const uint8_t* mask) {
+  return call | (kv_len ? LA_CROSS_LENGTHS : 0) | (mask ? LA_CROSS_MASK : 0);
 }
 
 la::xs::Str str(const la_strides& s) { return {s.b, s.h, s.n}; }
@@ -548,7 +559,6 @@ int cross_few(const la_cross_problem& p, const CrossPlan& c, la::xs::Args a, con
 // Partial sums leave the kernels in 32-byte stores.  Workspaces have the 16-byte alignment of every
 // pointer, so the parts start at the first 32-byte boundary, for which 16 bytes more are asked for.
 constexpr size_t kCrossSlack = 16;
-size_t cross_need(const CrossPlan& c) { return c.total + kCrossSlack; }
 
 // The workspace of a call, from its first 32-byte boundary on.
 int cross_workspace(const CrossPlan& c, void* ws, size_t ws_bytes, uint8_t** out) {
@@ -946,16 +956,21 @@ int clip_common(const la_grad* g, int64_t count, bool clip, float max_norm, floa
 
 extern "C" {
 
-size_t la_cross_workspace_bytes_for(const la_cross_problem* p, int sm_count) {
-  if (validate(p, false) != LA_OK || sm_count <= 0) return 0;
-  return cross_need(cross_plan(*p, sm_count));
+size_t la_cross_workspace_bytes_of(const la_cross_problem* p, unsigned uses, int sm_count) {
+  if (validate(p, false) != LA_OK || sm_count < 0 || (uses & ~unsigned(LA_CROSS_ANY))) return 0;
+  if (sm_count == 0 && current_sm_count(&sm_count) != LA_OK) return 0;
+  const unsigned forward = uses & ~unsigned(LA_CROSS_BACKWARD), backward = uses & ~unsigned(LA_CROSS_FORWARD);
+  size_t total = 0;
+  if (uses & LA_CROSS_FORWARD) total = cross_plan(*p, sm_count, forward).total;
+  if (uses & LA_CROSS_BACKWARD) total = std::max(total, cross_plan(*p, sm_count, backward).total);
+  return total + kCrossSlack;
 }
 
-size_t la_cross_workspace_bytes(const la_cross_problem* p) {
-  int sm = 0;
-  if (validate(p, false) != LA_OK || current_sm_count(&sm) != LA_OK) return 0;
-  return la_cross_workspace_bytes_for(p, sm);
+size_t la_cross_workspace_bytes_for(const la_cross_problem* p, int sm_count) {
+  return sm_count > 0 ? la_cross_workspace_bytes_of(p, LA_CROSS_ANY, sm_count) : 0;
 }
+
+size_t la_cross_workspace_bytes(const la_cross_problem* p) { return la_cross_workspace_bytes_of(p, LA_CROSS_ANY, 0); }
 
 int la_cross_forward(const la_cross_problem* p, const void* Q, const void* K, const void* V, const int32_t* kv_len,
                      const uint8_t* key_mask, void* O, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
@@ -969,7 +984,7 @@ int la_cross_forward(const la_cross_problem* p, const void* Q, const void* K, co
   if (has_q && same_address({O, lse}, {Q, has_k ? K : nullptr, has_k ? V : nullptr, kv_len, key_mask})) return LA_ERR_SHAPE;
   int sm = 0;
   if ((rc = current_sm_count(&sm))) return rc;
-  const CrossPlan c = cross_plan(*p, sm);
+  const CrossPlan c = cross_plan(*p, sm, uses_of(LA_CROSS_FORWARD, kv_len, key_mask));
   uint8_t* w = nullptr;
   if ((rc = cross_workspace(c, ws, ws_bytes, &w))) return rc;
   int nl = 0;
@@ -1012,7 +1027,7 @@ int la_cross_backward(const la_cross_problem* p, const void* Q, const void* K, c
     return LA_ERR_SHAPE;
   int sm = 0;
   if ((rc = current_sm_count(&sm))) return rc;
-  const CrossPlan c = cross_plan(*p, sm);
+  const CrossPlan c = cross_plan(*p, sm, uses_of(LA_CROSS_BACKWARD, kv_len, key_mask));
   uint8_t* w = nullptr;
   if ((rc = cross_workspace(c, ws, ws_bytes, &w))) return rc;
   int nl = 0;

@@ -25,7 +25,7 @@ namespace {
 struct Failed {};  // a Python exception is set
 
 struct Library {
-  decltype(&la_cross_workspace_bytes) cross_workspace_bytes;
+  decltype(&la_cross_workspace_bytes_of) cross_workspace_bytes;
   decltype(&la_cross_forward) cross_forward;
   decltype(&la_cross_backward) cross_backward;
   decltype(&la_layernorm_workspace_bytes) layernorm_workspace_bytes;
@@ -155,6 +155,10 @@ void want_masks(const at::Tensor* len, const at::Tensor* mask, const la_cross_pr
   }
 }
 
+unsigned uses(unsigned call, const at::Tensor* len, const at::Tensor* mask) {
+  return call | (len ? LA_CROSS_LENGTHS : 0) | (mask ? LA_CROSS_MASK : 0);
+}
+
 // cross_forward(head, Q, K, V, kv_len, key_mask, O, lse, return_lse, ws)
 PyObject* cross_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count_is(n, 10)) return nullptr;
@@ -176,7 +180,7 @@ PyObject* cross_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor lse;
     if (stats) lse = given_or_new(a[7], "lse", Shape(qs, 3), at::kFloat, dev);
     p.q = strides(*Q); p.k = strides(*K); p.v = strides(*V); p.o = strides(O);
-    const Workspace ws = workspace(a[9], dev, [&] { return lib.cross_workspace_bytes(&p); });
+    const Workspace ws = workspace(a[9], dev, [&] { return lib.cross_workspace_bytes(&p, uses(LA_CROSS_FORWARD, len, mask), 0); });
     const int rc = lib.cross_forward(&p, ptr(Q), ptr(K), ptr(V), as<int32_t>(len), as<uint8_t>(mask), O.data_ptr(),
                                      stats ? as<float>(&lse) : nullptr, ws.t.data_ptr(), ws.bytes,
                                      c10::cuda::getCurrentCUDAStream(dev.index()));
@@ -213,7 +217,7 @@ PyObject* cross_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                  : given_or_new(a[9 + i], gnames[i], i == 0 ? Shape(qs) : Shape(ks), type, dev, false);
     p.q = strides(*t[0]); p.k = strides(*t[1]); p.v = strides(*t[2]); p.o = strides(*t[3]); p.dout = strides(*t[5]);
     p.dq = strides(g[0]); p.dk = strides(g[1]); p.dv = strides(g[2]);
-    const Workspace ws = workspace(a[12], dev, [&] { return lib.cross_workspace_bytes(&p); });
+    const Workspace ws = workspace(a[12], dev, [&] { return lib.cross_workspace_bytes(&p, uses(LA_CROSS_BACKWARD, len, mask), 0); });
     const int rc = lib.cross_backward(&p, ptr(t[0]), ptr(t[1]), ptr(t[2]), as<int32_t>(len), as<uint8_t>(mask), ptr(t[3]),
                                       as<float>(t[4]), ptr(t[5]), g[0].data_ptr(), g[1].data_ptr(), g[2].data_ptr(),
                                       ws.t.data_ptr(), ws.bytes, c10::cuda::getCurrentCUDAStream(dev.index()));

@@ -302,10 +302,23 @@ typedef struct {
   la_strides dout, dq, dk, dv;       /* of dO, dQ, dK and dV (la_cross_backward only) */
 } la_cross_problem;
 
-/* Bytes of workspace for both cross-attention calls on the current device / for an SM count;
- * 0 for an invalid problem.  (16 of them let the workspace start on any 16-byte boundary.) */
+/* Bytes of workspace for both cross-attention calls, with or without kv_len and key_mask, on the
+ * current device / for an SM count; 0 for an invalid problem.  (16 of them let the workspace start on
+ * any 16-byte boundary.) */
 size_t la_cross_workspace_bytes(const la_cross_problem* p);
 size_t la_cross_workspace_bytes_for(const la_cross_problem* p, int sm_count);
+
+/* The same for some calls only.  `uses`: the calls, and the optional tensors that they may be given (a
+ * forward call alone needs far less than the gradients do, and no copies of K and V without those
+ * tensors).  sm_count 0: the current device's. */
+enum {
+  LA_CROSS_FORWARD = 1,
+  LA_CROSS_BACKWARD = 2,
+  LA_CROSS_LENGTHS = 4,   /* kv_len */
+  LA_CROSS_MASK = 8,      /* key_mask */
+  LA_CROSS_ANY = 15
+};
+size_t la_cross_workspace_bytes_of(const la_cross_problem* p, unsigned uses, int sm_count);
 
 /* O [B,H,Nq,d] and, when lse is non-NULL, lse [B,H,Nq] fp32 (dense; natural logarithm).
  * kv_len: int32 [B] on the device or NULL; key_mask: one byte per key, dense [B,Nk], or NULL. */

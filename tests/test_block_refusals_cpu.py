@@ -64,3 +64,21 @@ def test_layernorm_refuses_outputs_over_other_tensors():
     big = la.NormProblem(rows=4096, cols=64).c()
     bwd = dict(x=1 << 20, dy=1 << 20, weight=4096, mean=1 << 23, rstd=1 << 23, dx=1 << 22, dweight=4096 + 256, dbias=4096 + 512)
     assert lib.la_layernorm_backward(ctypes.byref(big), *bwd.values(), 16, 0, None) in (6, 7)
+
+
+def test_a_forward_call_does_not_need_the_gradients_workspace():
+    size = la.cross_workspace_bytes
+    serve = la.CrossProblem(B=8, H=32, Hkv=8, Nq=1, Nk=16384)
+    kv = 2 * 8 * 8 * 16384 * 128 * 2
+    assert size(serve, 148, backward=False) < 1 << 22          # parts of a few rows; nothing is gathered
+    train = la.CrossProblem(B=1, H=32, Nq=75600, Nk=300)
+    assert size(train, 148, backward=False, padded=False) == 16  # straight to the output
+    assert size(train, 148, backward=False) < 2 * 32 * 304 * 128 * 2 + 4096
+    for p in (serve, train, la.CrossProblem(B=2, H=4, Hkv=2, Nq=9, Nk=5000, dtype="f32")):
+        whole = size(p, 148)
+        assert whole == blk._lib().la_cross_workspace_bytes_for(ctypes.byref(p.c()), 148)
+        assert size(p, 148, padded=False) < whole and size(p, 148, backward=False) <= whole
+        assert size(p, 148, backward=False, padded=False) <= size(p, 148, backward=False)
+    assert size(serve, 148) - size(serve, 148, padded=False) >= kv  # the gathered keys and values
+    of = blk._lib().la_cross_workspace_bytes_of
+    assert of(ctypes.byref(serve.c()), 16, 148) == 0 and of(ctypes.byref(serve.c()), 1, -1) == 0 and of(None, 1, 148) == 0

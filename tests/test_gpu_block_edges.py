@@ -1,9 +1,12 @@
 """The operators of the block around the token mixer where calls are legal but unusual: workspaces on
 odd boundaries."""
+import ctypes
+
 import pytest
 import torch
 
 import gated_linear_attention_relu_b200 as la
+from gated_linear_attention_relu_b200 import block as blk
 from oracle import block_oracle as bo
 from test_gpu_block import DT, gen, inputs, rnd
 from test_gpu_block_use import same_bits
@@ -38,4 +41,34 @@ def test_workspaces_on_any_16_byte_boundary(shape, dtype):
         both(arena[272:272 + n - 1])
     with pytest.raises(la.LaError, match="LA_ERR_ALIGN"):
         both(arena[264:264 + n])
+    assert la.device_error() == 0
+
+
+# (the shapes and paths that gather, that read keys where they are, and that split)
+@pytest.mark.parametrize("shape", [(2, 4, 2, 300, 170, 64), (1, 1, 1, 40, 3000, 128), (2, 4, 2, 1, 5000, 128), (1, 2, 2, 0, 40, 32)],
+                         ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pad", ["none", "len", "mask", "both"])
+def test_calls_fit_the_workspace_of_their_own(shape, dtype, pad):
+    """Each call stays within the bytes that are reported for it and for what it is given."""
+    B, H, Hkv, Nq, Nk, d = shape
+    Q, K, V, kv_len, mask, _ = inputs(*shape, dtype, pad)
+    dO = rnd(Q.shape, DT[dtype], gen(1))
+    p = la.CrossProblem(B=B, H=H, Hkv=Hkv, Nq=Nq, Nk=Nk, d=d, dtype=dtype)
+    kw = dict(kv_len=kv_len, key_mask=mask)
+    O, lse = la.cross_forward(p, Q, K, V, return_lse=True, ws=la.cross_workspace(p), **kw)
+    grads = la.cross_backward(p, Q, K, V, O, lse, dO, ws=la.cross_workspace(p), **kw)
+    lib = blk._lib()
+    for use, call, want in ((1, lambda ws: la.cross_forward(p, Q, K, V, return_lse=True, ws=ws, **kw), (O, lse)),
+                            (2, lambda ws: la.cross_backward(p, Q, K, V, O, lse, dO, ws=ws, **kw), grads)):
+        uses = use | (4 if kv_len is not None else 0) | (8 if mask is not None else 0)
+        n = lib.la_cross_workspace_bytes_of(ctypes.byref(p.c()), uses, 0)
+        assert 16 <= n <= la.cross_workspace_bytes(p)
+        arena = torch.full((n + 1024,), 171, dtype=torch.uint8, device="cuda")
+        assert all(same_bits(a, b) for a, b in zip(call(arena[272:272 + n]), want))
+        assert (arena[:272] == 171).all() and (arena[272 + n:] == 171).all()
+        assert all(same_bits(a, b) for a, b in zip(call(None), want))
+        if n > 16:
+            with pytest.raises(la.LaError, match="LA_ERR_WORKSPACE"):
+                call(arena[256:256 + n - 17])
     assert la.device_error() == 0
