@@ -123,6 +123,15 @@ at::ScalarType type_of(int32_t dtype) { return dtype == LA_BF16 ? at::kBFloat16 
 // The status of a call that failed, as an int (the caller makes an LaError of it).
 PyObject* status(int rc) { return PyLong_FromLong(rc); }
 
+// Sets torch.OutOfMemoryError, as torch's own allocations do.
+void out_of_memory(const char* what) {
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+  if (type) PyErr_SetString(type, what);
+  Py_XDECREF(type);
+  Py_XDECREF(torch);
+}
+
 // Runs f(args) with this thread's exceptions turned into Python's.
 template <typename F>
 PyObject* guarded(F&& f) {
@@ -131,7 +140,7 @@ PyObject* guarded(F&& f) {
   } catch (const Failed&) {
     return nullptr;
   } catch (const c10::OutOfMemoryError& e) {
-    PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
+    out_of_memory(e.what_without_backtrace());
   } catch (const c10::Error& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
   } catch (const std::exception& e) {

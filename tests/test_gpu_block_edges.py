@@ -72,3 +72,14 @@ def test_calls_fit_the_workspace_of_their_own(shape, dtype, pad):
             with pytest.raises(la.LaError, match="LA_ERR_WORKSPACE"):
                 call(arena[256:256 + n - 17])
     assert la.device_error() == 0
+
+
+def test_out_of_memory_is_torchs_error():
+    # an output of 8 TB: refused by the allocator, and the next call is right
+    huge = la.CrossProblem(B=1, H=1 << 24, Hkv=1 << 24, Nq=1024, Nk=0, d=128)
+    one = torch.zeros((1, 1, 1024, 128), dtype=torch.bfloat16, device="cuda")
+    none = torch.zeros((1, 1, 0, 128), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        la.cross_forward(huge, one.expand(1, 1 << 24, -1, -1), none.expand(1, 1 << 24, -1, -1), none.expand(1, 1 << 24, -1, -1))
+    p = la.CrossProblem(B=1, H=1, Nq=1024, Nk=0, d=128)
+    assert not la.cross_forward(p, one, none, none).any()
