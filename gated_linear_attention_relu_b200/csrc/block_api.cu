@@ -1157,9 +1157,10 @@ int la_clip_grad_norm(const la_grad* grads, int64_t count, float max_norm, float
 }
 
 #ifdef LA_TEST_HOOKS
-// Test-hook build only: the roles that are held back (see hold in sm100.cuh; 0: none).
-int la_test_hold(unsigned int what) {
-  return cudaMemcpyToSymbol(la::g_la_hold, &what, sizeof what) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+// Hooks build only (not part of the regular library): what is held back or lost from the next launch on
+// (HOLD_*, LOSE_* in sm100.cuh; 0: nothing).
+int la_test_hooks(unsigned int what) {
+  return cudaMemcpyToSymbol(la::g_la_hooks, &what, sizeof what) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 #endif
 

@@ -229,15 +229,13 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             mbar_wait_drain(&bars->kfull[sk], (ki / C::KST) & 1);
             break;
           }
-          load_tile<DP>(smem + C::OFF_V + sv * C::TILE, &tmV, n, kh, w.b, &bars->vfull[sv]);
+          if (!lose(LOSE_DQ_V)) load_tile<DP>(smem + C::OFF_V + sv * C::TILE, &tmV, n, kh, w.b, &bars->vfull[sv]);
         }
       }
-      if (*abort_flag) {
-        // Let every copy still in flight land before the CTA's shared memory goes away.
-        drain(bars->qfull, C::QST, qi);
-        drain(bars->kfull, C::KST, ki);
-        drain(bars->vfull, C::VST, ki);
-      }
+      // Every copy lands before the CTA's shared memory goes away, whoever gives up, now or later.
+      drain(bars->qfull, C::QST, qi);
+      drain(bars->kfull, C::KST, ki);
+      drain(bars->vfull, C::VST, ki);
     } else if (warp == CTRL + 1) {
       // ---------------------------------------------------------- MMA issuer of S and dQ
       // (the issuers' warps stay converged; one's waits hide behind the other's products)
@@ -609,17 +607,15 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             break;
           }
           hold(HOLD_DO_LOAD);
-          load_tile<DP>(smem + C::OFF_G + sg * C::TILE, &tmG, n, h, w.b, &bars->gfull[sg]);
+          if (!lose(LOSE_DKV_DO)) load_tile<DP>(smem + C::OFF_G + sg * C::TILE, &tmG, n, h, w.b, &bars->gfull[sg]);
         }
         if (!ok) break;
       }
-      if (*abort_flag) {
-        // Let every copy still in flight land before the CTA's shared memory goes away.
-        drain(bars->qfull, C::QST, qi);
-        drain(bars->gfull, C::GST, qi);
-        drain(&bars->kfull, 1, k_out);
-        drain(&bars->vfull, 1, v_out);
-      }
+      // (as in dq_kernel)
+      drain(bars->qfull, C::QST, qi);
+      drain(bars->gfull, C::GST, qi);
+      drain(&bars->kfull, 1, k_out);
+      drain(&bars->vfull, 1, v_out);
     } else if (warp == CTRL + 1 || warp == CTRL + 2) {
       // ---------------------------------------------------------- MMA issuers (converged warps)
       // The first: S^T and dV, the second: dP^T and dK.  Each walks the same steps: the product of this

@@ -289,9 +289,10 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         uint8_t* dst = smem + C::OFF_KV + s * C::TILE;
         mbar_arrive_expect_tx(&bars->kvfull[s], C::TILE);
         const int32_t n = (w.k0 + j) * BN, h = w.h / a.group;
+        ++ki;
+        if (m == &tmV && lose(LOSE_FORWARD_V)) return true;
         tma_load_4d(dst, m, 0, n, h, w.b, &bars->kvfull[s]);
         if (DP == 128) tma_load_4d(dst + HALF, m, 64, n, h, w.b, &bars->kvfull[s]);
-        ++ki;
         return true;
       };
       Work w = before_first();
@@ -316,12 +317,10 @@ forward_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           }
         }
       }
-      if (*abort_flag) {
-        // Let every copy still in flight land before the CTA's shared memory goes away.
-        for (uint32_t j = (qi > QST ? qi - QST : 0); j < qi; ++j) mbar_wait_drain(&bars->qfull[j % QST], (j / QST) & 1);
-        for (uint32_t j = (ki > C::KVST ? ki - C::KVST : 0); j < ki; ++j)
-          mbar_wait_drain(&bars->kvfull[j % C::KVST], (j / C::KVST) & 1);
-      }
+      // Every copy lands before the CTA's shared memory goes away, whoever gives up, now or later.
+      for (uint32_t j = (qi > QST ? qi - QST : 0); j < qi; ++j) mbar_wait_drain(&bars->qfull[j % QST], (j / QST) & 1);
+      for (uint32_t j = (ki > C::KVST ? ki - C::KVST : 0); j < ki; ++j)
+        mbar_wait_drain(&bars->kvfull[j % C::KVST], (j / C::KVST) & 1);
     } else if (warp == 13 || warp == 14) {
       // ---------------------------------------------------------- MMA issuers, one for each query tile
       // (so that one's waits and bookkeeping hide behind the other's products).  The warp stays

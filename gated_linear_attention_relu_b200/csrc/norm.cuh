@@ -324,7 +324,7 @@ forward_long(const Args a, int parts, int stages, const T* x, const float* __res
     if (j < a.per_group) {
       ++issued;
       mbar_arrive_expect_tx(&rg.full[s], bytes);
-      bulk_load(ring + s * bytes, x + (row0 + j) * a.sx, bytes, &rg.full[s]);
+      if (!lose(LOSE_NORM_ROW)) bulk_load(ring + s * bytes, x + (row0 + j) * a.sx, bytes, &rg.full[s]);
     }
   };
   if (RING && threadIdx.x == 0) {
@@ -425,7 +425,7 @@ backward_long(const Args a, int parts, int stages, const T* x, const T* dy, cons
     if (j < a.per_group) {
       ++issued;
       mbar_arrive_expect_tx(&rg.full[s], 2 * bytes);
-      bulk_load(ring + (2 * s) * bytes, x + (row0 + j) * a.sx, bytes, &rg.full[s]);
+      if (!lose(LOSE_NORM_ROW)) bulk_load(ring + (2 * s) * bytes, x + (row0 + j) * a.sx, bytes, &rg.full[s]);
       bulk_load(ring + (2 * s + 1) * bytes, dy + (row0 + j) * a.sdy, bytes, &rg.full[s]);
     }
   };

@@ -1,6 +1,6 @@
 // sm100.cuh -- thin inline-PTX wrappers for the Blackwell (sm_100a) features the kernels use:
 // mbarriers, TMA tensor/bulk copies, tcgen05 tensor-memory allocation, MMA, commit and loads.
-// Every wait on an mbarrier is bounded: after LA_WAIT_LIMIT_NS of fruitless polling it records
+// Every wait on an mbarrier is bounded: after LA_WAIT_LIMIT_NS (or LA_WAIT_TESTS) of fruitless polling it records
 // a device error, raises the CTA's abort flag and returns false so the caller can wind down.
 #pragma once
 #include <cstdint>
@@ -39,17 +39,24 @@ __device__ __forceinline__ constexpr bool in_bounds(bool) { return true; }
 __device__ long long g_la_skip_tile = -1;
 #endif
 
-// Test hook of the same build: holds a role of the cross-attention kernels back for 20 us at each of
-// its steps, as a slow load or a warp that is not scheduled would; results must not change.
-enum : unsigned { HOLD_DO_LOAD = 1u, HOLD_DP_ISSUER = 2u };
+// Test hooks of the same build for the operators of the block around the mixer.  HOLD: a role of the
+// cross-attention kernels is held back for 20 us at each of its steps, as a slow load or a warp that is
+// not scheduled would be; results must not change.  LOSE: a kernel's loads of one kind are never issued,
+// so that its waits run out and it winds down.
+enum : unsigned {
+  HOLD_DO_LOAD = 1u, HOLD_DP_ISSUER = 2u,
+  LOSE_FORWARD_V = 4u, LOSE_DQ_V = 8u, LOSE_DKV_DO = 16u, LOSE_NORM_ROW = 32u,
+};
 #ifdef LA_TEST_HOOKS
-__device__ unsigned int g_la_hold;
+__device__ unsigned int g_la_hooks;
 __device__ __forceinline__ void hold(unsigned int what) {
-  if (!(g_la_hold & what)) return;
+  if (!(g_la_hooks & what)) return;
   for (int i = 0; i < 20; ++i) __nanosleep(1000);
 }
+__device__ __forceinline__ bool lose(unsigned int what) { return (g_la_hooks & what) != 0; }
 #else
 __device__ __forceinline__ void hold(unsigned int) {}
+__device__ __forceinline__ constexpr bool lose(unsigned int) { return false; }
 #endif
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -154,8 +161,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 // mbar_wait and warp_wait for kernels of many roles, whose code has to stay within the instruction
-// cache: a few instructions at every wait, and a limit on the tests (each of which the hardware
-// lets last up to some microseconds) instead of one on the time.
+// cache: a few instructions at every wait, and a limit on the tests instead of one on the time.  A
+// fruitless test lasts 3.97 us (measured), so 2^22 of them are 16.6 s.  The longest wait there is spans
+// a work item (a storing warp waits for all of its key tiles, at about 1 us each).
 #ifndef LA_WAIT_TESTS
 #define LA_WAIT_TESTS (1u << 22)
 #endif
