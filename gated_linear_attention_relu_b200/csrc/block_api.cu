@@ -721,8 +721,9 @@ int norm_forward_any(const la_norm_problem& p, const la::ln::Args& a, int sm, co
     if (c <= 256 * V) return norm_forward_short<T, V, 8, 32, 1>(p, a, sm, f, st);
     if (c <= 512 * V) return norm_forward_short<T, V, 16, 32, 1>(p, a, sm, f, st);
     if (c <= 1024 * V) return norm_forward_long<T, V, 2, 16, true>(p, a, sm, f, st);
-    if (c <= 2048 * V) return norm_forward_long<T, V, 4, 16, true>(p, a, sm, f, st);
-    return norm_forward_long<T, V, 8, 16, true>(p, a, sm, f, st);
+    if constexpr (2048 * V < kMaxCols)
+      if (c > 2048 * V) return norm_forward_long<T, V, 8, 16, true>(p, a, sm, f, st);
+    return norm_forward_long<T, V, 4, 16, true>(p, a, sm, f, st);
   }
   if (few && c > 32 * 4 && c <= 256 * 4) return norm_forward_long<T, 1, 4, 8, false>(p, a, sm, f, st);
   if (c <= 8 * 4) return norm_forward_short<T, 1, 4, 8, 2>(p, a, sm, f, st);
