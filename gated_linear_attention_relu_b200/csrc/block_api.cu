@@ -369,8 +369,6 @@ int cross_backward_simt(const la_cross_problem& p, const CrossPlan& c, la::xs::A
 // A [B, heads, tokens, d] bf16 view as a 4D tensor {d, tokens, heads, B}; boxes of 64 channels x 128
 // tokens, 128-byte swizzle (the canonical UMMA operand layout).  Channels and tokens outside read 0.
 bool make_tmap4(CUtensorMap* m, const void* base, int64_t d, int64_t tokens, int64_t heads, int64_t B, const la::xs::Str& s) {
-  la::EncodeTiledFn enc = la::encode_fn();
-  if (!enc) return false;
   cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(tokens), cuuint64_t(heads), cuuint64_t(B)};
   // (the stride of a dimension of extent 1 is never used: any legal value)
   cuuint64_t strides[3] = {tokens > 1 ? cuuint64_t(s.n) * 2 : 256, heads > 1 ? cuuint64_t(s.h) * 2 : 256,
@@ -379,9 +377,9 @@ bool make_tmap4(CUtensorMap* m, const void* base, int64_t d, int64_t tokens, int
     if (x >= cuuint64_t(1) << 40) return false;
   cuuint32_t box[4] = {64, 128, 1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return la::encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // The keys as the tensor-core kernels read them: the tensors themselves, or (with lengths or a

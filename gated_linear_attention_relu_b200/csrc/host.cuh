@@ -50,6 +50,21 @@ inline EncodeTiledFn encode_fn() {
   return fn;
 }
 
+// Encodes a tensor map (the arguments are cuTensorMapEncodeTiled's).  A driver call needs a context that
+// is current in the calling thread, and a host thread has none before its first runtime call that needs
+// one: that of its current device is made current then.
+template <typename... Args>
+bool encode_tiled(const Args&... args) {
+  const EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  CUresult r = enc(args...);
+  int dev = 0;
+  if ((r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) && cudaGetDevice(&dev) == cudaSuccess &&
+      cudaSetDevice(dev) == cudaSuccess)
+    r = enc(args...);
+  return r == CUDA_SUCCESS;
+}
+
 inline int launched_ok() { return cudaGetLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA; }
 
 // Launches `kern`; with `pdl` it may start while the previous kernel in the stream is still

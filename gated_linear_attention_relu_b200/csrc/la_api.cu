@@ -30,8 +30,6 @@ namespace {
 using la::align256;
 using la::aligned16;
 using la::current_sm_count;
-using la::encode_fn;
-using la::EncodeTiledFn;
 using la::g_last_launches;
 using la::launch_k;
 using la::launched_ok;
@@ -229,16 +227,13 @@ Rope make_rope(const la_problem& q) {
 // [BH, N, 128] bf16 viewed as a 3D tensor {128, N, BH}; boxes of 64 channels x 128 tokens,
 // 128-byte swizzle (the canonical UMMA operand layout).
 bool make_tmap(CUtensorMap* m, const void* base, int64_t BH, int64_t N, uint32_t box_rows = 128) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
   cuuint64_t dims[3] = {128, cuuint64_t(N), cuuint64_t(BH)};
   cuuint64_t strides[2] = {128 * 2, cuuint64_t(N) * 128 * 2};
   cuuint32_t box[3] = {64, box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  return la::encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // Optional terms of the full gated form (la_gates), as the launchers see them.

@@ -1,13 +1,13 @@
-"""The operators of the block around the token mixer where calls are legal but unusual: workspaces on
-odd boundaries."""
+"""The operators of the block around the token mixer where calls are legal but unusual: workspaces of odd
+boundaries and exact sizes, host threads that have not used CUDA."""
 import ctypes
+import threading
 
 import pytest
 import torch
 
 import gated_linear_attention_relu_b200 as la
 from gated_linear_attention_relu_b200 import block as blk
-from oracle import block_oracle as bo
 from test_gpu_block import DT, gen, inputs, rnd
 from test_gpu_block_use import same_bits
 
@@ -83,3 +83,29 @@ def test_out_of_memory_is_torchs_error():
         la.cross_forward(huge, one.expand(1, 1 << 24, -1, -1), none.expand(1, 1 << 24, -1, -1), none.expand(1, 1 << 24, -1, -1))
     p = la.CrossProblem(B=1, H=1, Nq=1024, Nk=0, d=128)
     assert not la.cross_forward(p, one, none, none).any()
+
+
+def test_first_call_of_a_host_thread():
+    """A thread that has not used CUDA before, and whose call finds everything else in place already."""
+    Q, K = (rnd((2, 4, n, 128), torch.bfloat16, gen(n)) for n in (300, 170))
+    p = la.CrossProblem(B=2, H=4, Nq=300, Nk=170, d=128)
+    ws = la.cross_workspace(p)
+    O, lse = la.cross_forward(p, Q, K, K, return_lse=True, ws=ws)
+    grads = la.cross_backward(p, Q, K, K, O, lse, Q.clone(), ws=ws)
+    dO = Q.clone()
+    torch.cuda.synchronize()
+    got = []
+
+    def forward():
+        got.append(la.cross_forward(p, Q, K, K, return_lse=True, ws=ws, O=torch.empty_like(O)))
+
+    def backward():
+        got.append(la.cross_backward(p, Q, K, K, O, lse, dO, ws=ws))
+
+    for call, want in ((forward, (O, lse)), (backward, grads)):
+        t = threading.Thread(target=call)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert len(got) == 1, "the call raised"
+        assert all(torch.equal(a, b) for a, b in zip(got.pop(), want))

@@ -8,7 +8,6 @@ import pytest
 import torch
 
 import gated_linear_attention_relu_b200 as la
-from gated_linear_attention_relu_b200 import block as blk
 from gated_linear_attention_relu_b200 import build
 from oracle import block_oracle as bo
 from test_gpu_block import P_UNIT, close, gen, inputs, rnd
