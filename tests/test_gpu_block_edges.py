@@ -1,5 +1,6 @@
-"""The operators of the block around the token mixer where calls are legal but unusual: workspaces of odd
-boundaries and exact sizes, host threads that have not used CUDA."""
+"""The operators of the block around the token mixer at sizes where a block works on one item after
+another, through every kernel that calls choose, on workspaces of odd boundaries and exact sizes, and from
+two threads."""
 import ctypes
 import threading
 
@@ -8,7 +9,8 @@ import torch
 
 import gated_linear_attention_relu_b200 as la
 from gated_linear_attention_relu_b200 import block as blk
-from test_gpu_block import DT, gen, inputs, rnd
+from oracle import block_oracle as bo
+from test_gpu_block import DT, close, gen, inputs, rnd, unit
 from test_gpu_block_use import same_bits
 
 pytestmark = pytest.mark.gpu
@@ -85,6 +87,83 @@ def test_out_of_memory_is_torchs_error():
     assert not la.cross_forward(p, one, none, none).any()
 
 
+# (B, H, Hkv, Nq, Nk, d): more work items than SMs in the tensor-core kernels (forward: pairs of query tiles,
+# the last of a head with one tile or two; gradients: query tiles, key tiles), shared heads, split keys
+ITEMS = [(3, 24, 24, 1100, 300, 128), (3, 24, 8, 1100, 300, 64), (5, 40, 40, 130, 300, 64), (5, 40, 40, 130, 300, 128),
+         (3, 32, 32, 513, 260, 32), (1, 100, 50, 200, 2100, 64), (2, 80, 80, 90, 700, 128)]
+
+
+@pytest.mark.parametrize("pad", ["none", "both", "len"])
+@pytest.mark.parametrize("shape", ITEMS, ids=str)
+def test_cross_items_one_after_another(shape, pad):
+    B, H, Hkv, Nq, Nk, d = shape
+    Q, K, V, kv_len, key_mask, ok = inputs(B, H, Hkv, Nq, Nk, d, "bf16", pad, "bnhd" if Nk % 200 else "bhnd")
+    dO = rnd((B, H, Nq, d), torch.bfloat16, gen(5), "bnhd")
+    p = la.CrossProblem(B=B, H=H, Hkv=Hkv, Nq=Nq, Nk=Nk, d=d)
+    kw = dict(kv_len=kv_len, key_mask=key_mask, ws=la.cross_workspace(p))
+    got = la.cross_forward(p, Q, K, V, return_lse=True, **kw)
+    o, l, to, tl = bo.cross_forward(Q, K, V, d ** -0.5, ok, unit("bf16", False))
+    close(got[0], o, to, "O")
+    close(got[1], l, tl, "lse")
+    args = (Q, K, V, o.to(torch.bfloat16), l.float(), dO)
+    grads = la.cross_backward(p, *args, **kw)
+    want, tol = bo.cross_backward(Q, K, V, dO, d ** -0.5, ok, unit("bf16", False))
+    for a, b, t, n in zip(grads, want, tol, ("dQ", "dK", "dV")):
+        close(a, b, t, n)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(la.cross_forward(p, Q, K, V, return_lse=True, **kw), got))
+        assert all(torch.equal(a, b) for a, b in zip(la.cross_backward(p, *args, **kw), grads))
+    assert la.device_error() == 0
+
+
+# 5 to 8 rows of a key head in one pass
+FEW = [(2, 8, 1, 1, 700, 128), (1, 6, 2, 2, 500, 64), (1, 5, 1, 1, 4099, 128), (3, 14, 2, 1, 65, 64), (2, 2, 2, 7, 300, 128)]
+
+
+@pytest.mark.parametrize("pad", ["none", "both"])
+@pytest.mark.parametrize("shape", FEW, ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_cross_forward_of_five_to_eight_rows(shape, dtype, pad):
+    B, H, Hkv, Nq, Nk, d = shape
+    Q, K, V, kv_len, key_mask, ok = inputs(B, H, Hkv, Nq, Nk, d, dtype, pad)
+    p = la.CrossProblem(B=B, H=H, Hkv=Hkv, Nq=Nq, Nk=Nk, d=d, dtype=dtype)
+    O, lse = la.cross_forward(p, Q, K, V, kv_len=kv_len, key_mask=key_mask, return_lse=True)
+    o, l, to, tl = bo.cross_forward(Q, K, V, d ** -0.5, ok, unit(dtype, False))
+    close(O, o, to, "O")
+    close(lse, l, tl, "lse")
+
+
+# (rows, cols, groups): more rows than the few-row kernels take, a width for every kernel of 16-byte packs and
+# of single elements; many rows to a block where rows come through a ring
+WIDE = [(700, c, 2) for c in (24, 32, 48, 64, 72, 120, 136, 256, 264, 504, 512, 520, 1000, 1024, 1032, 2048, 2056, 4096)] + \
+    [(700, c, 1) for c in (7, 31, 127, 301, 1001, 2001, 5001, 10001)] + \
+    [(2500, 5000, 1), (2500, 8192, 2), (2400, 16384, 1), (2400, 12296, 3), (6000, 1000, 1), (6000, 4096, 2)]
+
+
+@pytest.mark.parametrize("shape", WIDE, ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_layernorm_of_many_rows(dtype, shape):
+    rows, cols, groups = shape
+    g = gen(cols)
+    x = (torch.randn((rows, cols), generator=g, device="cuda") * 1.5 + 4.0).to(DT[dtype])
+    dy = torch.randn((rows, cols), generator=g, device="cuda").to(DT[dtype])
+    w = 1 + 0.2 * torch.randn((groups, cols), generator=g, device="cuda")
+    b = torch.randn((groups, cols), generator=g, device="cuda")
+    p = la.NormProblem(rows=rows, cols=cols, groups=groups, dtype=dtype)
+    got = la.layernorm_forward(p, x, w, b, return_stats=True)
+    want, tol = bo.norm_forward(x, w, b, p.eps)
+    for a, r, t, n in zip(got, want, tol, ("y", "mean", "rstd")):
+        close(a, r, t, n)
+    del want, tol
+    grads = la.layernorm_backward(p, x, dy, got[1], got[2], w)
+    want, tol = bo.norm_backward(x, dy, w, got[1], got[2], groups)
+    for a, r, t, n in zip(grads, want, tol, ("dx", "dweight", "dbias")):
+        close(a, r, t, n)
+    assert all(torch.equal(a, c) for a, c in zip(la.layernorm_forward(p, x, w, b, return_stats=True), got))
+    assert all(torch.equal(a, c) for a, c in zip(la.layernorm_backward(p, x, dy, got[1], got[2], w), grads))
+    assert la.device_error() == 0
+
+
 def test_first_call_of_a_host_thread():
     """A thread that has not used CUDA before, and whose call finds everything else in place already."""
     Q, K = (rnd((2, 4, n, 128), torch.bfloat16, gen(n)) for n in (300, 170))
@@ -109,3 +188,45 @@ def test_first_call_of_a_host_thread():
         torch.cuda.synchronize()
         assert len(got) == 1, "the call raised"
         assert all(torch.equal(a, b) for a, b in zip(got.pop(), want))
+
+
+def test_two_threads_at_once():
+    """Host threads that call into the library at the same time (the C entry points, which take no lock), each
+    with a stream and a workspace of its own."""
+    lib = blk._lib()
+    ptrs = lambda *ts: [t.data_ptr() for t in ts]  # noqa: E731
+    jobs = []
+    for seed, (B, H, Nq, Nk, d) in enumerate([(2, 6, 300, 170, 64), (1, 4, 700, 1300, 128)]):
+        Q, K, V, *_ = inputs(B, H, H, Nq, Nk, d, "bf16", "none", seed=seed)
+        dO, x = rnd(Q.shape, torch.bfloat16, gen(seed)), rnd((900, 1000 + 24 * seed), torch.bfloat16, gen(seed))
+        p, n = la.CrossProblem(B=B, H=H, Nq=Nq, Nk=Nk, d=d), la.NormProblem(*x.shape)
+        O, lse = la.cross_forward(p, Q, K, V, return_lse=True)
+        want = [O, lse, *la.cross_backward(p, Q, K, V, O, lse, dO), *la.layernorm_forward(n, x, return_stats=True)]
+        want += la.layernorm_backward(n, x, x, want[6], want[7])
+        jobs.append((p.c(), n.c(), Q, K, V, O, lse, dO, x, want, [torch.empty_like(t) for t in want],
+                     la.cross_workspace(p), la.layernorm_workspace(n), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    codes = [[], []]
+    start = threading.Barrier(2)
+
+    def work(i):
+        c, n, Q, K, V, O, lse, dO, x, want, out, ws, nws, stream = jobs[i]
+        st, c, n = stream.cuda_stream, ctypes.byref(c), ctypes.byref(n)
+        start.wait()
+        for _ in range(100):
+            codes[i] += [
+                lib.la_cross_forward(c, *ptrs(Q, K, V), None, None, *ptrs(out[0], out[1], ws), ws.numel(), st),
+                lib.la_cross_backward(c, *ptrs(Q, K, V), None, None, *ptrs(O, lse, dO, *out[2:5], ws), ws.numel(), st),
+                lib.la_layernorm_forward(n, *ptrs(x), None, None, *ptrs(*out[5:8]), st),
+                lib.la_layernorm_backward(n, *ptrs(x, x), None, *ptrs(*want[6:8], *out[8:11], nws), nws.numel(), st)]
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [[0] * 400] * 2
+    for job in jobs:
+        assert all(torch.equal(a, b) for a, b in zip(job[10], job[9]))
+    assert la.device_error() == 0
