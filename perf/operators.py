@@ -151,6 +151,11 @@ def _cross_inputs(c, seed):
 
 
 def prepare(case, seed):
+    s = _inputs(case, seed)
+    return _kept(s) if own else s
+
+
+def _inputs(case, seed):
     op = case["op"]
     if op.startswith("cross"):
         s, g, dt = _cross_inputs(case, seed)
@@ -276,31 +281,40 @@ def _views(flat, spans):
     return [flat[a:a + n] for a, n in spans]
 
 
+def _kept(s):
+    """What a program keeps beside its tensors: the problem and its workspace, as a model does, or the lists of
+    the parameters' gradients and of where the clipped ones go."""
+    import gated_linear_attention_relu_b200 as la
+
+    if s["op"].startswith("cross"):
+        s["problem"] = la.CrossProblem(B=s["B"], H=s["H"], Hkv=s["Hkv"], Nq=s["Nq"], Nk=s["Nk"], d=s["d"],
+                                       scale=s["scale"], dtype=s["dtype"])
+        s["ws"] = la.cross_workspace(s["problem"])
+    elif s["op"].startswith("ln"):
+        s["problem"] = la.NormProblem(rows=s["rows"], cols=s["cols"], groups=s["groups"], eps=s["eps"], dtype=s["dtype"])
+        s["ws"] = la.layernorm_workspace(s["problem"])
+    else:
+        s["grads"] = [t for n in DTYPES for t in _views(s["flat_" + n], s["spans_" + n])]
+        s["outs"] = [t for n in DTYPES for t in _views(s["out_" + n], s["spans_" + n])]
+    return s
+
+
 def _own(s):
     import gated_linear_attention_relu_b200 as la
 
+    if "problem" not in s and "grads" not in s:  # (a state that was prepared for the plain form)
+        _kept(s)
     op = s["op"]
     if op.startswith("cross"):
-        if "problem" not in s:  # kept from call to call, with its workspace, as a model keeps them
-            s["problem"] = la.CrossProblem(B=s["B"], H=s["H"], Hkv=s["Hkv"], Nq=s["Nq"], Nk=s["Nk"], d=s["d"],
-                                           scale=s["scale"], dtype=s["dtype"])
-            s["ws"] = la.cross_workspace(s["problem"])
         p, kw = s["problem"], dict(kv_len=s["kv_len"], key_mask=s["key_mask"], ws=s["ws"])
         if op == "cross_fwd":
             return la.cross_forward(p, s["Q"], s["K"], s["V"], return_lse=True, **kw)
         return la.cross_backward(p, s["Q"], s["K"], s["V"], s["O"], s["lse"], s["dO"], **kw)
     if op.startswith("ln"):
-        if "problem" not in s:
-            s["problem"] = la.NormProblem(rows=s["rows"], cols=s["cols"], groups=s["groups"], eps=s["eps"],
-                                          dtype=s["dtype"])
-            s["ws"] = la.layernorm_workspace(s["problem"])
         p = s["problem"]
         if op == "ln_fwd":
             return la.layernorm_forward(p, s["x"], s["weight"], s["bias"], return_stats=True)
         return la.layernorm_backward(p, s["x"], s["dy"], s["mean"], s["rstd"], s["weight"], ws=s["ws"])
-    if "grads" not in s:  # the parameters' gradients and where the clipped ones go, once per model
-        s["grads"] = [t for n in DTYPES for t in _views(s["flat_" + n], s["spans_" + n])]
-        s["outs"] = [t for n in DTYPES for t in _views(s["out_" + n], s["spans_" + n])]
     norm = la.clip_grad_norm(s["grads"], s["max_norm"], out=s["outs"])
     return dict({n: s["out_" + n] for n in DTYPES if s["flat_" + n].numel()}, norm=norm)
 
@@ -400,7 +414,7 @@ def _exact_norm(c, s):
 
 
 def exact(case, seed):
-    s = prepare(case, seed)
+    s = _inputs(case, seed)
     if case["op"].startswith("cross"):
         return _exact_cross(case, s)
     if case["op"].startswith("ln"):
