@@ -116,6 +116,25 @@ def test_cross_items_one_after_another(shape, pad):
     assert la.device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pad", ["mask", "both"])
+def test_cross_long_masks_of_several_rows(dtype, pad):
+    # masks that are counted in spans first, a length that ends within a span, a row without keys
+    B, H, Hkv, Nq, Nk, d = 3, 4, 2, 20, 40001, 64
+    Q, K, V, kv_len, key_mask, ok = inputs(B, H, Hkv, Nq, Nk, d, dtype, pad)
+    p = la.CrossProblem(B=B, H=H, Hkv=Hkv, Nq=Nq, Nk=Nk, d=d, dtype=dtype)
+    kw = dict(kv_len=kv_len, key_mask=key_mask)
+    O, lse = la.cross_forward(p, Q, K, V, return_lse=True, **kw)
+    o, l, to, tl = bo.cross_forward(Q, K, V, d ** -0.5, ok, unit(dtype, False))
+    close(O, o, to, "O")
+    close(lse, l, tl, "lse")
+    dO = rnd((B, H, Nq, d), DT[dtype], gen(5))
+    got = la.cross_backward(p, Q, K, V, o.to(DT[dtype]), l.float(), dO, **kw)
+    want, tol = bo.cross_backward(Q, K, V, dO, d ** -0.5, ok, unit(dtype, False))
+    for a, b, t, n in zip(got, want, tol, ("dQ", "dK", "dV")):
+        close(a, b, t, n)
+
+
 # 5 to 8 rows of a key head in one pass
 FEW = [(2, 8, 1, 1, 700, 128), (1, 6, 2, 2, 500, 64), (1, 5, 1, 1, 4099, 128), (3, 14, 2, 1, 65, 64), (2, 2, 2, 7, 300, 128)]
 
