@@ -10,8 +10,8 @@
 // and ds go back to tensor memory as bf16 (rounded once each, for the product that follows); the
 // softmax scale is applied to the fp32 sums at the end.
 //
-// 32 heads of 75600 queries and 300 keys (929 GFLOP in 5 products): 1590 us with D's pass of 240, which
-// is 584 TFLOP/s, or 818 for the 7 products.  What bounds it is the chain of a step, score product ->
+// 32 heads of 75600 queries and 300 keys (929 GFLOP in 5 products) at 1965 MHz: 1588 us with D's pass of 227,
+// which is 585 TFLOP/s, or 819 for the 7 products.  What bounds it is the chain of a step, score product ->
 // exponentials -> dP -> ds -> product, of which tensor memory holds one and a half steps; the third key
 // tile of 44 keys costs dkv_kernel as much as a full one.
 //

@@ -6,7 +6,7 @@
 // One pass over the keys with the running maximum and sum of the softmax; 64 x 64 score tiles,
 // 4 x 4 scores a thread, so a step along d feeds 16 FMAs from 8 shared-memory values; tiles of global
 // memory are fetched into registers during the products of the tile before.  8 heads, 2048 x 1000,
-// d = 64: forward 317 us (26 of 74.5 TFLOP/s), gradients 895 (23 in 5 products, 33 in the 7 done):
+// d = 128: forward 317 us (26 of 74.5 TFLOP/s), gradients 896 (23 in 5 products, 33 in the 7 done):
 // the barriers between a tile's products and its exponentials leave the FMA pipe idle for the rest.
 // Products over many keys (or, in the gradients, many queries) are summed
 // per tile and the tiles' sums then added up, which keeps the rounding of long sums at the level of

@@ -13,10 +13,11 @@
 // The last key tile is cut to a multiple of 16 keys in both products and to a multiple of 32 in the
 // softmax.
 //
-// 32 heads of 75600 queries: 300 keys 442 us (840 TFLOP/s, 2.8 TB/s), 8192 x 8192 keys 980 us (1120
-// TFLOP/s of the 1684 that a large matrix product reaches).  Both are bound by the exponentials and
-// their warps' issue slots, which two tiles in turn keep at work about all the time; short keys add the
-// epilogue of every 3 key tiles.
+// 32 heads at 1965 MHz: 75600 queries and 300 keys 442 us (840 TFLOP/s, 2.8 TB/s), 8192 x 8192 986 us (1115
+// TFLOP/s of the 1684 that a large matrix product reaches).  At 8192 x 8192 a tile of 128 x 128 scores takes
+// 2190 cycles, with half the channels 2060: its products 1450 (725) at that rate, its exponentials 1024.  So
+// the softmax warps bound it: a turn has one warp a scheduler, which scales, converts, loads and stores
+// too, and the exponentials' unit runs at half its rate.  Short keys add the epilogue of every 3 key tiles.
 //
 // Warps (one CTA per SM, persistent; work item = pair of query tiles of a head, or a part of its
 // keys where there are too few items):

@@ -56,7 +56,7 @@ typedef enum {
   LA_ERR_NULL = 1,        /* a required pointer is NULL */
   LA_ERR_SHAPE = 2,       /* negative / inconsistent sizes, or sizes beyond the limits */
   LA_ERR_BANDS = 3,       /* dt + dh + dw != d, or a band width is odd or negative */
-  LA_ERR_ALIGN = 4,       /* a device pointer is not 16-byte aligned */
+  LA_ERR_ALIGN = 4,       /* a device pointer or stride is not 16-byte aligned */
   LA_ERR_UNSUPPORTED = 5, /* d not in {32, 64, 128}, unknown dtype or flag */
   LA_ERR_WORKSPACE = 6,   /* workspace NULL or smaller than la_workspace_bytes() */
   LA_ERR_CUDA = 7,        /* a CUDA runtime call or kernel launch failed */
