@@ -176,7 +176,12 @@ scale_kernel(const __grid_constant__ Table<CAP> t, const double* partial, int pa
   const double total = total_norm(partial, parts, red);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = static_cast<float>(total);
   const double ratio = double(max_norm) / (total + 1e-6);
-  const float c = ratio > 1.0 ? 1.f : static_cast<float>(ratio);  // (NaN stays NaN)
+  // A coefficient near fp32's smallest numbers would lose its bits: below 2^-100 it is taken 2^128 times as
+  // large and 2^-64 is applied before it and after it (both exactly, or to results below fp32's range).
+  const bool far = ratio < 0x1p-100;
+  const float s = far ? 0x1p-64f : 1.f;
+  const float c = ratio > 1.0 ? 1.f : static_cast<float>(far ? ratio * 0x1p128 : ratio);  // (NaN stays NaN)
+  auto scaled = [&](float v) { return v * s * c * s; };
   for_chunks<CAP, true>(t, [&](int k, int64_t e0, int n, bool is32) {
     if (c == 1.f && t.in[k] == t.out[k]) return;  // nothing to change in place
     const int tid = threadIdx.x;
@@ -191,12 +196,12 @@ scale_kernel(const __grid_constant__ Table<CAP> t, const double* partial, int pa
 #pragma unroll 2
         for (int i = tid; i < n4; i += THREADS) {
           const uint4 u = load16(p4 + i);
-          __stcs(o4 + i, make_float4(__uint_as_float(u.x) * c, __uint_as_float(u.y) * c, __uint_as_float(u.z) * c,
-                              __uint_as_float(u.w) * c));
+          __stcs(o4 + i, make_float4(scaled(__uint_as_float(u.x)), scaled(__uint_as_float(u.y)),
+                                     scaled(__uint_as_float(u.z)), scaled(__uint_as_float(u.w))));
         }
         done = n4 << 2;
       }
-      for (int i = done + tid; i < n; i += THREADS) o[i] = p[i] * c;
+      for (int i = done + tid; i < n; i += THREADS) o[i] = scaled(p[i]);
     } else {
       const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(t.in[k]) + e0;
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(t.out[k]) + e0;
@@ -209,15 +214,15 @@ scale_kernel(const __grid_constant__ Table<CAP> t, const double* partial, int pa
           float v[8];
           unpack(load16(p8 + i), v);
           uint4 u;
-          u.x = pack_bf16(v[0] * c, v[1] * c);
-          u.y = pack_bf16(v[2] * c, v[3] * c);
-          u.z = pack_bf16(v[4] * c, v[5] * c);
-          u.w = pack_bf16(v[6] * c, v[7] * c);
+          u.x = pack_bf16(scaled(v[0]), scaled(v[1]));
+          u.y = pack_bf16(scaled(v[2]), scaled(v[3]));
+          u.z = pack_bf16(scaled(v[4]), scaled(v[5]));
+          u.w = pack_bf16(scaled(v[6]), scaled(v[7]));
           __stcs(o8 + i, u);
         }
         done = n8 << 3;
       }
-      for (int i = done + tid; i < n; i += THREADS) o[i] = __float2bfloat16_rn(__bfloat162float(p[i]) * c);
+      for (int i = done + tid; i < n; i += THREADS) o[i] = __float2bfloat16_rn(scaled(__bfloat162float(p[i])));
     }
   });
 }

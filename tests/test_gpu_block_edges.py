@@ -249,3 +249,20 @@ def test_two_threads_at_once():
     for job in jobs:
         assert all(torch.equal(a, b) for a, b in zip(job[10], job[9]))
     assert la.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=("f32", "bf16"))
+@pytest.mark.parametrize("max_norm", [1e30, 1e9, 1.0, 1e-3, 1e-30])
+def test_clipping_by_coefficients_below_fp32s_range(dtype, max_norm):
+    """A norm of about 1e40 is beyond fp32 itself, and what clips it may be too; the clipped values are not.
+    Half a step of the type, 6 of fp32 for the products and the coefficient, and of the smallest numbers two
+    (a product's and the type's)."""
+    t = torch.linspace(-3e38, 3e38, 40001, dtype=torch.float64).float().to(dtype).cuda()
+    t[:100] = torch.linspace(0.5, 3.0, 100).to(dtype).cuda()
+    t[100:200] = torch.linspace(1e-38, 1e-20, 100).to(dtype).cuda()
+    ref = float(t.double().square().sum().sqrt())
+    want = t.double() * min(1.0, max_norm / (ref + 1e-6))
+    smallest = 2.0 ** -149 if dtype == torch.float32 else 2.0 ** -133
+    for out in (torch.empty_like(t), t):
+        la.clip_grad_norm([t], max_norm, out=[out])
+        close(out, want, (bo.HALF_STEP[dtype] + 6 * bo.U32) * want.abs() + 2 * smallest, "clipped")
