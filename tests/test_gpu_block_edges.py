@@ -2,6 +2,9 @@
 another, through every kernel that calls choose, on workspaces of odd boundaries and exact sizes, and from
 two threads."""
 import ctypes
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -207,6 +210,39 @@ def test_first_call_of_a_host_thread():
         torch.cuda.synchronize()
         assert len(got) == 1, "the call raised"
         assert all(torch.equal(a, b) for a, b in zip(got.pop(), want))
+
+
+CAPTURE = """
+import torch
+import gated_linear_attention_relu_b200 as la
+torch.manual_seed(0)
+r = lambda *s: torch.randn(s, device="cuda")
+Q, K, V, dO = (r(2, 4, n, 64).to(torch.bfloat16) for n in (300, 170, 170, 300))
+mask, x, grads = r(2, 170) > 0, r(700, 1000), [r(1000), r(70000).to(torch.bfloat16)]
+p, n = la.CrossProblem(B=2, H=4, Nq=300, Nk=170, d=64), la.NormProblem(700, 1000, dtype="f32")
+outs = [torch.empty_like(t) for t in grads]
+
+def call():
+    O, lse = la.cross_forward(p, Q, K, V, key_mask=mask, return_lse=True)
+    y, mean, rstd = la.layernorm_forward(n, x, return_stats=True)
+    return (O, lse, *la.cross_backward(p, Q, K, V, O, lse, dO, key_mask=mask), y, mean, rstd,
+            *la.layernorm_backward(n, x, x, mean, rstd), la.clip_grad_norm(grads, 1.0, out=outs), *outs)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = call()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in captured]
+assert all(torch.equal(a, b) for a, b in zip(got, call())) and la.device_error() == 0
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_two_threads_at_once():
